@@ -655,6 +655,99 @@ int zero_step_noalloc(zero_ctx *ctx, const void *const *grads, int32_t n_grads, 
                       double beta1, double beta2, double eps, int64_t t, float loss_scale,
                       void *stream);
 
+/* ------------------------------------------------------ training operators */
+
+/* What a rank's forward and backward compute around the flat vector: the
+ * token table's lookup and its gradient (which goes into the table's place of
+ * the rank's flat gradient), dropout, and linear layers whose operands are
+ * quantised to 4 bits.  The pages have no counterpart; the calls follow the
+ * conventions above (caller's buffers, caller's stream, nothing allocated,
+ * nothing launched on an error) and take no context.  They run on the current
+ * device.  Rows, columns and tokens are at most 2^31 - 2; row strides are in
+ * elements, at least the row's length, and need no alignment: rows on
+ * 16-byte boundaries are fastest.  Inputs and outputs must not overlap unless
+ * a call says so. */
+
+/* out[i] = scale * table[tokens[i]], i < n: rows of `dim` elements of
+ * `dtype`, the product rounded once to it.  tokens: token_bytes is 4 or 8
+ * (signed ids).  A token equal to `pad` (-1: none) gives a row of zeros; so
+ * does one outside [0, rows), and it is counted: *bad (device memory, may be
+ * NULL) grows by the number of such tokens. */
+int zero_embed(const void *table, int32_t dtype, int64_t rows, int64_t dim, int64_t table_stride,
+               const void *tokens, int32_t token_bytes, int64_t n, int64_t pad, float scale,
+               void *out, int64_t out_stride, uint64_t *bad, void *stream);
+
+/* The gradient of zero_embed with respect to the table:
+ *   dtable[r] = scale * sum of dy[i] over the i with tokens[i] == r
+ * for every row r (rows that no token names become zero), or, with
+ * accumulate != 0, dtable[r] += that for the rows that a token names; the
+ * others are not touched.  Tokens equal to `pad` or outside [0, rows) take no
+ * part.  The sum is in fp32 and its order depends on the tokens alone: the
+ * same call gives the same bits.  workspace: device memory of at least
+ * zero_embed_grad_workspace(rows, dim, n) bytes (-1 on a bad argument),
+ * 16-byte aligned; its contents before and after mean nothing. */
+int64_t zero_embed_grad_workspace(int64_t rows, int64_t dim, int64_t n);
+int zero_embed_grad(const void *dy, int32_t dy_dtype, int64_t dy_stride, const void *tokens,
+                    int32_t token_bytes, int64_t n, int64_t pad, float scale, void *dtable,
+                    int32_t grad_dtype, int64_t rows, int64_t dim, int64_t dtable_stride,
+                    int32_t accumulate, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* out[e] = residual[e] + (kept(e) ? x[e] / (1 - p) : 0), e < n; residual may
+ * be NULL (no addition).  Element e of the call is element first + e of the
+ * stream of random words named by (seed, offset): it is kept where word
+ * (first + e) % 4 of Philox4x32-10 (Salmon et al. 2011) with the key
+ * (seed's low, high 32 bits) at the counter ((first + e) / 4's low, high,
+ * offset's low, high) is at least floor(p * 2^32).  No mask is stored: the
+ * gradient is the same call on dy with the same seed, offset and first and
+ * no residual.  p in [0, 1] (1 drops everything); first a multiple of 4, so
+ * that a long tensor can be taken in pieces.  x * (1 / (1 - p)) and the
+ * addition are single fp32 operations, rounded once to `dtype`; what is
+ * dropped is dropped even if it is infinite or NaN.  out may be x or
+ * residual. */
+int zero_dropout(const void *x, const void *residual, void *out, int32_t dtype, int64_t n,
+                 double p, uint64_t seed, uint64_t offset, int64_t first, void *stream);
+
+/* Microscaled 4-bit matrices (OCP Microscaling Formats 1.0, MXFP4): E2M1
+ * elements, one power-of-two scale (E8M0) per block of 32 consecutive
+ * elements of a row.  A matrix of `rows` by `cols` takes
+ * zero_mx4_bytes(rows, cols) bytes (-1 on a bad argument), 16-byte aligned:
+ * ceil(rows / 128) by ceil(cols / 256) records, row-major, of 17408 bytes.  A
+ * record holds 128 rows of 128 bytes of codes, columns 2b and 2b + 1 in the
+ * low and high half of byte b, the 16-byte piece p of row r lying at piece
+ * p ^ (r & 7); then 1024 bytes of scales, that of row r and block b at
+ * (b / 4) * 512 + (r % 32) * 16 + (r / 32) * 4 + b % 4.  Codes and scales of
+ * columns past `cols` are zero; rows past `rows` are not written and never
+ * read into a result. */
+int64_t zero_mx4_bytes(int64_t rows, int64_t cols);
+
+/* Quantises x (rows by cols of `dtype`): q with blocks along the rows of x,
+ * qt with blocks along its columns, laid out as the matrix x^T (cols by rows);
+ * either may be NULL.  A block's scale is 2^(floor(log2 of its largest
+ * magnitude) - 2), not below 2^-127; an element is divided by it and rounded to the nearest
+ * of 0, .5, 1, 1.5, 2, 3, 4, 6, ties to the even code, larger ones to 6, its
+ * sign kept.  A block that holds an infinity or NaN gets the NaN scale, so
+ * that whatever is computed from it is NaN. */
+int zero_mx4_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride,
+                      void *q, void *qt, void *stream);
+
+/* The values of a quantised matrix, rounded once to `dtype`. */
+int zero_mx4_dequantize(const void *q, int64_t rows, int64_t cols, void *out, int32_t dtype,
+                        int64_t stride, void *stream);
+
+/* out = alpha * A B^T, or out += that with accumulate != 0: A is m by k and B
+ * n by k, both as zero_mx4_quantize lays them out, out m by n of `dtype`.  The
+ * products are exact and summed in fp32 on the tensor cores.  A linear layer
+ * y = x W^T and its gradients dx = dy W and dW = dy^T x are
+ *   zero_mx4_matmul(x's q, m, W's q, n, k)         -> y
+ *   zero_mx4_matmul(dy's q, m, W's qt, k, n)       -> dx
+ *   zero_mx4_matmul(dy's qt, n, x's qt, k, m)      -> dW
+ * The kernel's waits are bounded; zero_mx4_timeouts() (which synchronizes)
+ * returns ZERO_ETIMEOUT and the count once one has run out in this process:
+ * the results of the products since then are not to be used. */
+int zero_mx4_matmul(const void *a, int64_t m, const void *b, int64_t n, int64_t k, float alpha,
+                    int32_t accumulate, void *out, int32_t dtype, int64_t stride, void *stream);
+int zero_mx4_timeouts(uint32_t *count);
+
 #ifdef __cplusplus
 }
 #endif

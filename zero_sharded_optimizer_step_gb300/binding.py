@@ -102,6 +102,18 @@ _SIGS = {
     "zero3_reduce_group": (ctypes.c_int, [_ctxp, _i32, _i32, _vpp, _i32, _f32, _vp]),
     "zero_step_noalloc": (ctypes.c_int, [_ctxp, _vpp, _i32, _f64, _f64, _f64, _f64, _i64, _f32,
                                          _vp]),
+    "zero_embed": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _f32, _vp,
+                                  _i64, _vp, _vp]),
+    "zero_embed_grad_workspace": (_i64, [_i64, _i64, _i64]),
+    "zero_embed_grad": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _f32, _vp, _i32,
+                                       _i64, _i64, _i64, _i32, _vp, _i64, _vp]),
+    "zero_dropout": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _f64, _u64, _u64, _i64, _vp]),
+    "zero_mx4_bytes": (_i64, [_i64, _i64]),
+    "zero_mx4_quantize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "zero_mx4_dequantize": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i32, _i64, _vp]),
+    "zero_mx4_matmul": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _f32, _i32, _vp, _i32, _i64,
+                                       _vp]),
+    "zero_mx4_timeouts": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_L, _name)
@@ -495,3 +507,63 @@ def zero_step_noalloc(ctx, grads, lr: float, beta1: float, beta2: float, eps: fl
     (for callers that cannot allocate device memory; see include/zero.h)."""
     _check(_L.zero_step_noalloc(_h(ctx), _ptrs(grads), len(grads), lr, beta1, beta2, eps, t,
                                 loss_scale, _stream(stream)))
+
+
+# ------------------------------------------------------- training operators
+
+def zero_embed(table, dtype: int, rows: int, dim: int, table_stride: int, tokens,
+               token_bytes: int, n: int, pad: int, scale: float, out, out_stride: int, bad=None,
+               stream=None) -> None:
+    _check(_L.zero_embed(_ptr(table), dtype, rows, dim, table_stride, _ptr(tokens), token_bytes,
+                         n, pad, scale, _ptr(out), out_stride, _ptr(bad), _stream(stream)))
+
+
+def zero_embed_grad_workspace(rows: int, dim: int, n: int) -> int:
+    return _L.zero_embed_grad_workspace(rows, dim, n)
+
+
+def zero_embed_grad(dy, dy_dtype: int, dy_stride: int, tokens, token_bytes: int, n: int,
+                    pad: int, scale: float, dtable, grad_dtype: int, rows: int, dim: int,
+                    dtable_stride: int, accumulate: bool, workspace, workspace_bytes: int,
+                    stream=None) -> None:
+    _check(_L.zero_embed_grad(_ptr(dy), dy_dtype, dy_stride, _ptr(tokens), token_bytes, n, pad,
+                              scale, _ptr(dtable), grad_dtype, rows, dim, dtable_stride,
+                              int(accumulate), _ptr(workspace), workspace_bytes,
+                              _stream(stream)))
+
+
+def zero_dropout(x, residual, out, dtype: int, n: int, p: float, seed: int, offset: int,
+                 first: int = 0, stream=None) -> None:
+    _check(_L.zero_dropout(_ptr(x), _ptr(residual), _ptr(out), dtype, n, p, seed, offset, first,
+                           _stream(stream)))
+
+
+def zero_mx4_bytes(rows: int, cols: int) -> int:
+    return _L.zero_mx4_bytes(rows, cols)
+
+
+def zero_mx4_quantize(x, dtype: int, rows: int, cols: int, stride: int, q, qt=None,
+                      stream=None) -> None:
+    _check(_L.zero_mx4_quantize(_ptr(x), dtype, rows, cols, stride, _ptr(q), _ptr(qt),
+                                _stream(stream)))
+
+
+def zero_mx4_dequantize(q, rows: int, cols: int, out, dtype: int, stride: int,
+                        stream=None) -> None:
+    _check(_L.zero_mx4_dequantize(_ptr(q), rows, cols, _ptr(out), dtype, stride,
+                                  _stream(stream)))
+
+
+def zero_mx4_matmul(a, m: int, b, n: int, k: int, alpha: float, accumulate: bool, out,
+                    dtype: int, stride: int, stream=None) -> None:
+    _check(_L.zero_mx4_matmul(_ptr(a), m, _ptr(b), n, k, alpha, int(accumulate), _ptr(out),
+                              dtype, stride, _stream(stream)))
+
+
+def zero_mx4_timeouts() -> int:
+    """Waits of the product kernel that ran out (0 when all is well)."""
+    n = ctypes.c_uint32()
+    rc = _L.zero_mx4_timeouts(ctypes.byref(n))
+    if rc != ZERO_ETIMEOUT:
+        _check(rc)
+    return int(n.value)

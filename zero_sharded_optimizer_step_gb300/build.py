@@ -16,8 +16,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzero.so")
-SOURCES = ["zero_abi.cu", "zero_step_kernels.cu", "zero_gather.cu", "zero_advance.cu"]
-HEADERS = ["zero_internal.h", "zero_row_copy.cuh", os.path.join("..", "..", "include", "zero.h")]
+SOURCES = ["zero_abi.cu", "zero_step_kernels.cu", "zero_gather.cu", "zero_advance.cu",
+           "zero_embed.cu", "zero_dropout.cu", "zero_mx4.cu", "zero_mx4_matmul.cu",
+           "zero_ops_abi.cu"]
+HEADERS = ["zero_internal.h", "zero_ops.h", "zero_row_copy.cuh", "zero_elems.cuh", os.path.join("..", "..", "include", "zero.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -99,6 +99,17 @@ struct zero_ctx {
 
 namespace zgb {
 
+int report(int code, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return code;
+}
+
 int resident_blocks_per_sm(const void *kernel, int threads)
 {
     struct Entry { const void *k; int dev, threads, blocks; };

@@ -169,6 +169,9 @@ cudaError_t load_hyper_slot(int slot, const DeviceHyper *block, cudaStream_t s);
 // Device address of a slot (a caller may copy its block straight there).
 cudaError_t hyper_slot_address(int slot, void **addr);
 
+// Records a message for zero_last_error and returns `code` (zero_abi.cu).
+int report(int code, const char *fmt, ...);
+
 // Blocks of `threads` threads of `kernel` that fit on one SM of the current
 // device (cached per kernel and device; at least 1).
 int resident_blocks_per_sm(const void *kernel, int threads);
