@@ -22,6 +22,10 @@
 //
 // Every wait on a barrier is bounded; one that runs out is counted and ends
 // the block without a store.
+#include <atomic>
+
+#include <cuda.h>
+
 #include "zero_elems.cuh"
 #include "zero_ops.h"
 
@@ -58,6 +62,33 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
         if (done) return true;
     }
     return false;
+}
+
+// Both barriers' phases; the two polls' latencies overlap.
+__device__ __forceinline__ bool bar_wait_both(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1)
+{
+    for (long long i = 0; i < kPolls; ++i) {
+        uint32_t done;
+        asm volatile("{\n .reg .pred p, q;\n"
+                     " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                     " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n"
+                     " and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(done) : "r"(b0), "r"(p0), "r"(b1), "r"(p1) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
+// One lane of a converged warp.  The warps that issue run whole, with a lane
+// elected for the instructions themselves: their addresses are then
+// uniform over the warp and need no copies to uniform registers, which would cost
+// more than the products take.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
@@ -132,14 +163,24 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank)
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank)
 {
     uint32_t p;
-    float v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+    return p;
+}
+
+__device__ __forceinline__ float4 load_peer4(uint32_t addr, uint32_t rank)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(peer_addr(addr, rank)) : "memory");
     return v;
 }
+
+constexpr int kSmemSm = 233472;      // shared memory of an SM
+constexpr int kSmemBlock = 231424;   // dynamic shared memory that leaves room for no other block
 
 template <int NT> struct Tile {
     static constexpr int kRecs = (NT + 127) / 128;          // records of A side by side
@@ -149,20 +190,26 @@ template <int NT> struct Tile {
     static constexpr int kTmemUsed = NT + 8 + 8 * kRecs;
     static constexpr int kTmem = kTmemUsed <= 32 ? 32 : kTmemUsed <= 64 ? 64
                                  : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-    // Shared memory holds at most 512 / kTmem blocks on an SM, so that no block
-    // waits for tensor memory that another one holds.
-    static constexpr int kStages = NT >= 256 ? 4 : NT >= 128 ? 3 : 4;
+    static constexpr int kStages = 4;                       // at most
     static constexpr int kPart = NT * 128 * 4;              // a split's partial sums
-    static constexpr int kSmem = (kStages * kStage > kPart ? kStages * kStage : kPart) + 1024;
+    // Shared memory of a block, for so many stages.  A block's share of it is
+    // at least its share of the tensor memory, so that no block on an
+    // SM waits for tensor memory that another one holds: two that wait for
+    // their cluster peers so would wait forever.
+    static constexpr int smem(int stages)
+    {
+        const int ring = stages * kStage > kPart ? stages * kStage : kPart;
+        const int share = kTmem == 512 ? kSmemBlock : (kSmemSm / (512 / kTmem) + 127) / 128 * 128;
+        return ring + 1024 > share ? ring + 1024 : share;
+    }
     static_assert(kStage % 1024 == 0, "stages start on the swizzle's boundary");
-    static_assert((232448 / kSmem) * kTmem <= 512, "tensor memory for every resident block");
 };
 
 constexpr int kMmThreads = 192;
 
 struct MxSplit {
     int64_t kt, tiles_n;
-    int32_t splits;
+    int32_t splits, stages;
 };
 
 template <int DT>
@@ -172,6 +219,51 @@ __device__ __forceinline__ void put(const MxMatmulArgs &a, int64_t i, int64_t j,
     v = __fmul_rn(v, a.alpha);
     if (a.accumulate) v = __fadd_rn(elems::load1<DT>(a.out, at), v);
     elems::store1<DT>(a.out, at, v);
+}
+
+// Adds up the splits' partial sums, [column][lane] in every block's shared
+// memory, in the blocks' order, and writes them: this block the columns
+// rank, rank + splits, ..., a warp one at a time, 4 lanes of the tile a
+// thread.  Four columns are in flight, so that the peers' latency is paid
+// once for them.
+template <int DT, int NT>
+__device__ __forceinline__ void join(const MxMatmulArgs &a, const float *part, uint32_t rank,
+                                     int splits, int64_t i0, int64_t j0)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t j = j0 + lane * 4;
+    const int cols = (int)(a.m - i0 < NT ? a.m - i0 : NT);
+    for (int c0 = (int)rank + warp * splits; c0 < cols; c0 += 16 * splits) {
+        float4 sum[4];
+        for (int q = 0; q < splits; ++q) {
+            float4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int c = c0 + u * 4 * splits;
+                if (c < cols) v[u] = load_peer4(saddr(part + c * 128 + lane * 4), q);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (q == 0) {
+                    sum[u] = v[u];
+                } else {
+                    sum[u].x = __fadd_rn(sum[u].x, v[u].x);
+                    sum[u].y = __fadd_rn(sum[u].y, v[u].y);
+                    sum[u].z = __fadd_rn(sum[u].z, v[u].z);
+                    sum[u].w = __fadd_rn(sum[u].w, v[u].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int c = c0 + u * 4 * splits;
+            if (c >= cols) break;
+            if (j < a.n) put<DT>(a, i0 + c, j, sum[u].x);
+            if (j + 1 < a.n) put<DT>(a, i0 + c, j + 1, sum[u].y);
+            if (j + 2 < a.n) put<DT>(a, i0 + c, j + 2, sum[u].z);
+            if (j + 3 < a.n) put<DT>(a, i0 + c, j + 3, sum[u].w);
+        }
+    }
 }
 
 template <int DT, int NT>
@@ -223,8 +315,8 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
         const uint32_t bytes = kMxRecord + (NT < kMxRows ? Tl::kACodes : nrec * kMxCodes) +
                                nrec * kMxScales;
         for (int64_t kt = k0; kt < k1; ++kt) {
-            const int it = (int)(kt - k0), s = it % Tl::kStages;
-            if (it >= Tl::kStages && !bar_wait(empty(s), ((it / Tl::kStages) - 1) & 1)) {
+            const int it = (int)(kt - k0), s = it % sp.stages;
+            if (it >= sp.stages && !bar_wait(empty(s), ((it / sp.stages) - 1) & 1)) {
                 atomicAdd(&g_mx4_timeouts, 1u);
                 failed = 1;
                 break;
@@ -244,8 +336,8 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
         const uint32_t sb = tmem + NT, sa = sb + 8;
         bool ok = true;
         for (int64_t kt = k0; kt < k1; ++kt) {
-            const int it = (int)(kt - k0), s = it % Tl::kStages;
-            if (!bar_wait(full(s), (it / Tl::kStages) & 1)) {
+            const int it = (int)(kt - k0), s = it % sp.stages;
+            if (!bar_wait(full(s), (it / sp.stages) & 1)) {
                 ok = false;
                 break;
             }
@@ -322,17 +414,7 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
             }
         }
         cluster_sync();
-        if (warp < 4 && ok) {
-            for (int c = (int)rank; c < NT; c += sp.splits) {
-                if (i0 + c >= a.m) break;
-                float v = 0.0f;
-                for (int q = 0; q < sp.splits; ++q) {
-                    const float u = load_peer(saddr(part + c * 128 + warp * 32 + lane), q);
-                    v = q == 0 ? u : __fadd_rn(v, u);
-                }
-                if (j < a.n) put<DT>(a, i0 + c, j, v);
-            }
-        }
+        if (warp < 4 && ok) join<DT, NT>(a, part, rank, sp.splits, i0, tn * kMxRows);
         cluster_sync();       // the peers have read this block's shared memory
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -343,6 +425,429 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
     if (warp == 5)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"((uint32_t)Tl::kTmem));
+}
+
+// ------------------------------------------------------------ the pair kernel
+//
+// Large products: two SMs share a tile of 256 lanes (rows of B) by 256 columns
+// (rows of A), so that either reads only its own 128 rows of both operands.
+// The first block's MMA warp issues for both (cta_group::2), and both blocks'
+// copies arrive at its barriers: a record is a tensor of 136 rows of 128 bytes
+// to the copy engine, because only tensor copies may signal the other block.
+//
+// The scales have a warp of their own, which copies them a stage ahead into
+// one of two sets of columns.  A thread that issues both the copies and the
+// products stands at its next barrier until the copies are done, and
+// the tensor cores run dry: 177 clocks a product of 256 x 256 x 64, against
+// 134 with two warps and 128 for the products alone.
+//
+// The blocks are persistent.  The accumulators of consecutive tiles lie at
+// columns 0 and 192 of the tensor memory (of 512, 48 hold the scales): they
+// overlap in 64 columns, which the result warps read first, so that the next
+// tile's products start as soon as those are out and run while the other
+// 192 are read, converted and stored.
+constexpr int kPairStages = 6;
+constexpr int kPairStage = kMxRecord + kMxCodes + 2 * kMxScales;
+constexpr int kPairSmem = kPairStages * kPairStage + 1024;
+constexpr int kPairThreads = 224;
+constexpr int kOverlap = 64;
+constexpr uint32_t kPairAcc = 256 - kOverlap;            // the upper accumulator
+constexpr uint32_t kPairScales = 2 * 256 - kOverlap;     // two sets: 8 columns for B, 16 for A
+static_assert(kPairSmem <= kSmemBlock, "one block's shared memory");
+static_assert(kPairScales + 48 <= 512, "the tensor memory's columns");
+
+constexpr int kMxLines = kMxRecord / 128;               // 128-byte lines of a record
+
+struct MxPair {
+    CUtensorMap lanes, codes, scales;               // boxes of 136, 128 and 8 lines
+    int64_t kt, tiles_n, tiles_m, recs_n, recs_m;   // 256 and 128 rows of the lanes' operand
+};                                                  // (n) and of the columns' (m)
+
+
+// At the pair's first block.  The accumulator's order is kept by the tcgen05
+// fences around it, so the arrival itself need not wait for earlier stores.
+__device__ __forceinline__ void arrive_first(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, 0))
+                 : "memory");
+}
+
+// Rows y, y + 1, ... of the record rows that `map` describes (its box's height
+// of them), into this block, signalled at `bar` of the first one.
+__device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap *map, int32_t y,
+                                            uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+                 ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(0), "r"(y), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void copy_scales2(uint32_t tmem, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                     uint32_t sa, uint32_t sb, uint32_t add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+                 " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+                 " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "r"(sa), "r"(sb), "r"(add) : "memory");
+}
+
+__device__ __forceinline__ void commit2(uint32_t bar)             // at both blocks
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                 ".multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+
+__device__ __forceinline__ void commit2_first(uint32_t bar)       // at the issuing block alone
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::
+                     "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void load32(uint32_t tmem, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(tmem));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Tile t of the sweep: bands of 8 tiles of rows of A, so that the blocks at work
+// at one time share both operands' records in L2.
+__device__ __forceinline__ void pair_tile(const MxPair &g, int64_t t, int64_t &tn, int64_t &tm)
+{
+    const int64_t band = t / (8 * g.tiles_n), in = t - band * 8 * g.tiles_n;
+    const int64_t wide = g.tiles_m - band * 8 < 8 ? g.tiles_m - band * 8 : 8;
+    tn = in / wide;
+    tm = band * 8 + in - tn * wide;
+}
+
+// Stages that the pair `first` of every `step` goes through.
+__device__ __forceinline__ int64_t pair_stages(const MxPair &g, int64_t first, int64_t step)
+{
+    const int64_t tiles = g.tiles_n * g.tiles_m;
+    return first < tiles ? ((tiles - 1 - first) / step + 1) * g.kt : 0;
+}
+
+// 32 consecutive columns of row i of the result, from column j on, 32 bytes a
+// store: `out` and its rows lie on 32-byte boundaries.
+template <int DT>
+__device__ __forceinline__ void put_row32(const MxMatmulArgs &a, int64_t i, int64_t j,
+                                          const uint32_t (&r)[32])
+{
+    constexpr int kPer = DT == F32 ? 8 : 16;                 // elements of 32 bytes
+    const int64_t at = i * a.stride + j;
+#pragma unroll
+    for (int h = 0; h < 32 / kPer; ++h) {
+        if (j + (h + 1) * kPer > a.n) {                      // the row's ragged end
+            for (int e = h * kPer; e < (h + 1) * kPer; ++e)
+                if (j + e < a.n) put<DT>(a, i, j + e, __uint_as_float(r[e]));
+            continue;
+        }
+        float f[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) f[e] = __fmul_rn(__uint_as_float(r[h * kPer + e]), a.alpha);
+        if (a.accumulate) {
+            float o[8];
+#pragma unroll
+            for (int u = 0; u < kPer / 8; ++u) {
+                elems::Raw<DT, 8> old;
+                old.load(a.out, at + h * kPer + u * 8);
+                old.get(o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[u * 8 + e] = __fadd_rn(o[e], f[u * 8 + e]);
+            }
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (DT == F32) w[e] = __float_as_uint(f[e]);
+            else w[e] = elems::narrow2<DT>(f[2 * e], f[2 * e + 1]);
+        }
+        using T = typename elems::El<DT>::T;
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
+                         static_cast<T *>(a.out) + at + h * kPer),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                     "r"(w[7]) : "memory");
+    }
+}
+
+// The tile's lanes are rows of the operand `lanes`, its columns rows of the
+// operand `cols`.  WIDE: lanes = A, so that a thread holds consecutive
+// columns of a row of the result and stores them 32 bytes at a time.  A result
+// that is not aligned for that has lanes = B, so that a warp's stores are
+// consecutive whatever their alignment.
+template <int DT, bool WIDE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ MxPair g)
+{
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 5];
+    __shared__ uint32_t tmem_base, failed;
+    const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int64_t tiles = g.tiles_n * g.tiles_m, step = gridDim.x / 2;
+    auto full = [&](int s) { return saddr(&bars[s]); };                     // the first block's
+    auto empty = [&](int s) { return saddr(&bars[kPairStages + s]); };
+    auto done = [&](int b) { return saddr(&bars[2 * kPairStages + b]); };
+    auto scaled = [&](int b) { return saddr(&bars[2 * kPairStages + 2 + b]); };  // the first block's
+    const uint32_t drained = saddr(&bars[2 * kPairStages + 4]);             // the first block's
+
+    if (warp == 4) {
+        if (lane == 0) {
+            for (int s = 0; s < 2 * kPairStages + 4; ++s) bar_init(saddr(&bars[s]), 1);
+            bar_init(drained, 8);
+            failed = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+    } else if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         saddr(&tmem_base)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();             // both blocks' barriers and tensor memory are there
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_base;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    bool ok = true;
+    if (warp == 4) {                                         // the copies
+        const bool one = elect_one();
+        int s = 0;
+        uint32_t phase = 1;                                  // the stages start empty
+        for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
+            int64_t tn, tm;
+            pair_tile(g, t, tn, tm);
+            // past the last record the last one again: its results are not stored
+            const int64_t rb = tn * 2 + rank < g.recs_n ? tn * 2 + rank : g.recs_n - 1;
+            const int64_t ra0 = tm * 2, ra1 = ra0 + 1 < g.recs_m ? ra0 + 1 : ra0;
+            int32_t yb = (int32_t)(rb * g.kt * kMxLines);
+            int32_t y0 = (int32_t)(ra0 * g.kt * kMxLines), y1 = (int32_t)(ra1 * g.kt * kMxLines);
+            for (int64_t kt = 0; kt < g.kt; ++kt) {
+                ok = bar_wait(empty(s), phase);
+                if (!ok) break;
+                if (one) {
+                    const uint32_t st = ring + s * kPairStage, bar = peer_addr(full(s), 0);
+                    if (rank == 0) bar_expect(full(s), 2 * kPairStage);
+                    tensor_load(st, &g.lanes, yb, bar);
+                    tensor_load(st + kMxRecord, &g.codes, rank ? y1 : y0, bar);
+                    tensor_load(st + kMxRecord + kMxCodes, &g.scales, y0 + 128, bar);
+                    tensor_load(st + kMxRecord + kMxCodes + kMxScales, &g.scales, y1 + 128, bar);
+                }
+                __syncwarp();
+                yb += kMxLines;
+                y0 += kMxLines;
+                y1 += kMxLines;
+                if (++s == kPairStages) s = 0, phase ^= 1;
+            }
+        }
+    } else if (warp == 6 && rank == 0) {                     // the scales
+        const bool one = elect_one();
+        const uint32_t sets = tmem + kPairScales;
+        const int64_t total = pair_stages(g, blockIdx.x / 2, step);
+        int s = 0, last = 0;                                 // the stage, and that of two before
+        uint32_t phase = 0, last_phase = 0;
+        for (int64_t it = 0; it < total; ++it) {
+            // the products two stages before have read this set of columns
+            ok = it < 2 ? bar_wait(full(s), phase)
+                        : bar_wait_both(full(s), phase, empty(last), last_phase);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (one) {
+                const uint32_t sb = sets + (uint32_t)(it & 1) * 24, sa = sb + 8;
+                const uint64_t db = scale_desc(ring + s * kPairStage + kMxCodes);
+                const uint64_t da = db + ((kMxScales + kMxCodes) >> 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    copy_scales2(sb + 4 * h, db + h * (512 >> 4));
+                    copy_scales2(sa + 8 * h, da + h * (512 >> 4));
+                    copy_scales2(sa + 8 * h + 4, da + ((kMxScales + h * 512) >> 4));
+                }
+                commit2_first(scaled((int)(it & 1)));
+            }
+            __syncwarp();
+            if (++s == kPairStages) s = 0, phase ^= 1;
+            if (it >= 2 && ++last == kPairStages) last = 0, last_phase ^= 1;
+        }
+    } else if (warp == 5 && rank == 0) {                     // the products
+        const bool one = elect_one();
+        constexpr uint32_t desc = (1u << 7) | (1u << 10) | ((256u >> 3) << 17) | (1u << 23) |
+                                  (2u << 27);
+        const uint32_t sets = tmem + kPairScales;
+        int s = 0;
+        uint32_t phase = 0, scaled_phase = 0;
+        uint32_t i = 0, it = 0;                              // parities of the tile and the stage
+        // the record's columns past k are zeros: their products are left out
+        const int last_steps = (int)((a.k - (g.kt - 1) * kMxCols + 63) / 64);
+        for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
+            const uint32_t acc = tmem + (i & 1) * kPairAcc;
+            // the tile before has left the columns that this one shares with it
+            // (and so, read earlier by the same warps, the one before that all)
+            if (t >= step) ok = bar_wait(drained, (i & 1) ^ 1);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (int64_t kt = 0; kt < g.kt; ++kt) {
+                ok = bar_wait_both(full(s), phase, scaled((int)it), scaled_phase);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                if (one) {
+                    const uint32_t sb = sets + it * 24, sa = sb + 8;
+                    const uint64_t db = operand_desc(ring + s * kPairStage);
+                    const uint64_t da = db + (kMxRecord >> 4);
+                    const int steps = kt == g.kt - 1 ? last_steps : 4;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= steps) break;
+                        const uint32_t id = (j & 1) * 2;
+                        mma2(acc, db + j * 2, da + j * 2, desc | (id << 4) | (id << 29),
+                             sb + 4 * (j >> 1), sa + 8 * (j >> 1), kt > 0 || j > 0);
+                    }
+                    commit2(empty(s));
+                    if (kt == g.kt - 1) commit2(done((int)i));
+                }
+                __syncwarp();
+                if (++s == kPairStages) s = 0, phase ^= 1;
+                it ^= 1;
+                if (it == 0) scaled_phase ^= 1;
+            }
+            i ^= 1;
+        }
+    } else if (warp < 4) {                                   // the results
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        uint32_t b = 0, done_phase = 0;
+        for (int64_t t = blockIdx.x / 2; t < tiles; t += step) {
+            int64_t tn, tm;
+            pair_tile(g, t, tn, tm);
+            ok = bar_wait(done((int)b), done_phase);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const int64_t l = (tn * 2 + rank) * kMxRows + warp * 32 + lane, c0 = tm * 256;
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {
+                // the shared columns first: the last of the lower accumulator,
+                // the first of the upper one
+                const int c = (b == 0 ? 7 - q : q) * 32;
+                uint32_t r[32];
+                load32(tmem + lanes + b * kPairAcc + c, r);
+                if (q == kOverlap / 32 - 1) {
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) arrive_first(drained);
+                }
+                if constexpr (WIDE) {
+                    if (l < a.m) put_row32<DT>(a, l, c0 + c, r);
+                } else if (l < a.n) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c0 + c + e < a.m) put<DT>(a, c0 + c + e, l, __uint_as_float(r[e]));
+                }
+            }
+            b ^= 1;
+            if (b == 0) done_phase ^= 1;
+        }
+    }
+    if (!ok) {
+        if (lane == 0) atomicAdd(&g_mx4_timeouts, 1u);
+        failed = 1;
+    }
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    // copies still in flight land before either block ends
+    if (failed && threadIdx.x == 0 && rank == 0)
+        for (int s = 0; s < kPairStages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
+    __syncthreads();
+    cluster_sync();             // nothing of either block is still in use by the other
+    if (warp == 5)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(512u));
+}
+
+// A quantised matrix as a tensor of 128-byte lines, copied `box` at a time.
+cudaError_t record_map(CUtensorMap *map, const void *base, int64_t lines, int box)
+{
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<Encode> encode{nullptr};
+    Encode f = encode.load(std::memory_order_relaxed);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                         cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (!p || found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+        f = reinterpret_cast<Encode>(p);
+        encode.store(f, std::memory_order_relaxed);
+    }
+    const cuuint64_t dims[2] = {128, (cuuint64_t)lines}, strides[1] = {128};
+    const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, one[2] = {1, 1};
+    const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims,
+                         strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The lines of both operands; whether the copies' 32-bit coordinates reach them.
+bool pair_lines(const MxMatmulArgs &a, int64_t &la, int64_t &lb)
+{
+    const int64_t kt = (a.k + kMxCols - 1) / kMxCols * kMxLines;
+    la = (a.m + kMxRows - 1) / kMxRows * kt;
+    lb = (a.n + kMxRows - 1) / kMxRows * kt;
+    return la <= 0x7fffffff && lb <= 0x7fffffff;
+}
+
+template <int DT, bool WIDE> cudaError_t pair_go(const MxMatmulArgs &a, int sms, cudaStream_t s)
+{
+    static int attr_device = -1;   // the attribute is per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (attr_device != dev) {
+        cudaError_t r = cudaFuncSetAttribute(mx4_pair_kernel<DT, WIDE>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSmemBlock);
+        if (r != cudaSuccess) return r;
+        attr_device = dev;
+    }
+    MxPair g;
+    int64_t lines_a = 0, lines_b = 0;
+    pair_lines(a, lines_a, lines_b);
+    const void *lanes = WIDE ? a.a : a.b, *cols = WIDE ? a.b : a.a;
+    const int64_t lines_l = WIDE ? lines_a : lines_b, lines_c = WIDE ? lines_b : lines_a;
+    cudaError_t e = record_map(&g.lanes, lanes, lines_l, kMxLines);
+    if (e == cudaSuccess) e = record_map(&g.codes, cols, lines_c, kMxCodes / 128);
+    if (e == cudaSuccess) e = record_map(&g.scales, cols, lines_c, kMxScales / 128);
+    if (e != cudaSuccess) return e;
+    g.kt = (a.k + kMxCols - 1) / kMxCols;
+    g.recs_n = ((WIDE ? a.m : a.n) + kMxRows - 1) / kMxRows;
+    g.recs_m = ((WIDE ? a.n : a.m) + kMxRows - 1) / kMxRows;
+    g.tiles_n = (g.recs_n + 1) / 2;
+    g.tiles_m = (g.recs_m + 1) / 2;
+    const int64_t tiles = g.tiles_n * g.tiles_m;
+    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    return launch_dependent(mx4_pair_kernel<DT, WIDE>, dim3((unsigned)(2 * pairs)),
+                            dim3(kPairThreads), kSmemBlock, s, a, g);
 }
 
 // NT < 128 serves m <= NT: a single tile of rows of A.
@@ -356,7 +861,7 @@ cudaError_t mm_go(const MxMatmulArgs &a, int sms, cudaStream_t s)
     if (attr_device != dev) {
         cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<DT, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Tl::kSmem);
+                                             Tl::smem(Tl::kStages));
         if (e != cudaSuccess) return e;
         attr_device = dev;
     }
@@ -364,16 +869,24 @@ cudaError_t mm_go(const MxMatmulArgs &a, int sms, cudaStream_t s)
     sp.kt = (a.k + kMxCols - 1) / kMxCols;
     sp.tiles_n = (a.n + kMxRows - 1) / kMxRows;
     const int64_t tiles = sp.tiles_n * ((a.m + NT - 1) / NT);
-    // halve the columns while there are SMs without a tile and each
-    // part keeps two records
+    // halve the columns while there are places without a block (as many
+    // per SM as shared memory lets in) and each part keeps two records
     sp.splits = 1;
-    while (sp.splits < 8 && tiles * sp.splits < sms && sp.kt >= 4 * sp.splits) sp.splits *= 2;
+    for (;;) {
+        const int64_t most = (sp.kt + sp.splits - 1) / sp.splits;
+        sp.stages = most < Tl::kStages ? (most > 0 ? (int)most : 1) : Tl::kStages;
+        const int64_t next = (most + 1) / 2;
+        const int st = next < Tl::kStages ? (int)next : Tl::kStages;
+        const int64_t places = (int64_t)sms * (kSmemSm / (Tl::smem(st > 0 ? st : 1) + 1024));
+        if (sp.splits == 8 || sp.kt < 4 * sp.splits || tiles * sp.splits * 2 > places) break;
+        sp.splits *= 2;
+    }
     const int64_t blocks = tiles * sp.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = Tl::kSmem;
+    cfg.dynamicSmemBytes = Tl::smem(sp.stages);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -389,9 +902,15 @@ cudaError_t mm_go(const MxMatmulArgs &a, int sms, cudaStream_t s)
 
 template <int DT> cudaError_t mm_pick(const MxMatmulArgs &a, int sms, cudaStream_t s)
 {
+    const int64_t pairs = ((a.n + 255) / 256) * ((a.m + 255) / 256);
+    int64_t la, lb;
+    if (a.k > 0 && pairs >= sms / 4 && pair_lines(a, la, lb)) {
+        const int es = DT == F32 ? 4 : 2;
+        const bool wide = ((uintptr_t)a.out & 31) == 0 && a.stride * es % 32 == 0;
+        return wide ? pair_go<DT, true>(a, sms, s) : pair_go<DT, false>(a, sms, s);
+    }
     return a.m <= 16 ? mm_go<DT, 16>(a, sms, s)
-           : a.m <= 64 ? mm_go<DT, 64>(a, sms, s)
-           : a.m <= 128 ? mm_go<DT, 128>(a, sms, s) : mm_go<DT, 256>(a, sms, s);
+           : a.m <= 64 ? mm_go<DT, 64>(a, sms, s) : mm_go<DT, 128>(a, sms, s);
 }
 
 }  // namespace
