@@ -13,62 +13,100 @@
 namespace zgb {
 namespace {
 
-__device__ __forceinline__ uint4 philox(unsigned long long c, const DropoutArgs &a)
+// The words at the counters c[0 .. N).  The chains go round by round together,
+// so that a round's keys are fetched once for all of them.  LOW: counters below 2^32, and
+// half of the first two rounds' products are those of the offset alone, made
+// on the host (a.pre).
+template <bool LOW, int N>
+__device__ __forceinline__ void philox(const unsigned long long (&c)[N], const DropoutArgs &a,
+                                       uint4 (&w)[N])
 {
-    uint32_t c0 = (uint32_t)c, c1 = (uint32_t)(c >> 32), c2 = a.off0, c3 = a.off1;
-    uint32_t k0 = a.key0, k1 = a.key1;
 #pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        const unsigned long long p0 = (unsigned long long)c0 * 0xD2511F53u;
-        const unsigned long long p1 = (unsigned long long)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
-        c1 = (uint32_t)p1;
-        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
-        c3 = (uint32_t)p0;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
+    for (int i = 0; i < N; ++i) {
+        if (LOW) {
+            const unsigned long long p0 = (unsigned long long)(uint32_t)c[i] * 0xD2511F53u;
+            const unsigned long long p1 =
+                (unsigned long long)((uint32_t)(p0 >> 32) ^ a.pre[0]) * 0xCD9E8D57u;
+            w[i] = make_uint4((uint32_t)(p1 >> 32) ^ a.pre[1], (uint32_t)p1,
+                              (uint32_t)p0 ^ a.pre[2], a.pre[3]);
+        } else {
+            w[i] = make_uint4((uint32_t)c[i], (uint32_t)(c[i] >> 32), a.off0, a.off1);
+        }
     }
-    return make_uint4(c0, c1, c2, c3);
+#pragma unroll
+    for (int r = LOW ? 2 : 0; r < 10; ++r) {
+        const uint32_t k0 = a.key0[r], k1 = a.key1[r];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const unsigned long long p0 = (unsigned long long)w[i].x * 0xD2511F53u;
+            const unsigned long long p1 = (unsigned long long)w[i].z * 0xCD9E8D57u;
+            w[i] = make_uint4((uint32_t)(p1 >> 32) ^ w[i].y ^ k0, (uint32_t)p1,
+                              (uint32_t)(p0 >> 32) ^ w[i].w ^ k1, (uint32_t)p0);
+        }
+    }
 }
 
 __device__ __forceinline__ float drop(float x, uint32_t word, const DropoutArgs &a)
 {
-    return (unsigned long long)word >= a.threshold ? __fmul_rn(x, a.up) : 0.0f;
+    return word >= a.threshold && a.any ? __fmul_rn(x, a.up) : 0.0f;
 }
 
-// VEC: 8 elements a thread on 16-byte boundaries.  Otherwise (an unaligned
-// buffer, and the ragged end) 4 elements a thread, one by one.
-template <int DT, bool RES, bool VEC>
+// VEC: kGroups groups of 8 elements a thread, on 16-byte boundaries, all loaded
+// before the words are made.  Otherwise (an unaligned buffer, and the ragged
+// end) 4 elements a thread, one by one.
+constexpr int kGroups = 2;
+
+template <int DT, bool RES, bool VEC, bool LOW>
 __global__ void __launch_bounds__(kThreads)
 dropout_kernel(const __grid_constant__ DropoutArgs a)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t T = (int64_t)gridDim.x * kThreads;
-    const int64_t t0 = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t groups = VEC ? a.n / 8 : 0;
-    for (int64_t g = t0; g < groups; g += T) {
-        elems::Raw<DT, 8> rx, rr;
-        rx.load(a.x, g * 8);
-        if (RES) rr.load(a.residual, g * 8);
-        const uint4 w0 = philox(a.first + 2 * g, a), w1 = philox(a.first + 2 * g + 1, a);
-        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        float x[8];
-        rx.get(x);
+    if (VEC) {
+        const int64_t g0 = (int64_t)blockIdx.x * (kThreads * kGroups) + threadIdx.x;
+        elems::Raw<DT, 8> rx[kGroups], rr[kGroups];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = drop(x[i], w[i], a);
-        if (RES) {
-            float r[8];
-            rr.get(r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], r[i]);
+        for (int k = 0; k < kGroups; ++k) {
+            const int64_t g = g0 + k * kThreads;
+            if (g < groups) {
+                rx[k].load(a.x, g * 8);
+                if (RES) rr[k].load(a.residual, g * 8);
+            }
         }
-        rx.set(x);
-        rx.store(a.out, g * 8);
+        unsigned long long c[2 * kGroups];
+        uint4 w[2 * kGroups];
+#pragma unroll
+        for (int k = 0; k < 2 * kGroups; ++k)
+            c[k] = a.first + 2 * (g0 + (k >> 1) * kThreads) + (k & 1);
+        philox<LOW>(c, a, w);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int64_t g = g0 + k * kThreads;
+            if (g >= groups) break;
+            const uint32_t u[8] = {w[2 * k].x,     w[2 * k].y,     w[2 * k].z,     w[2 * k].w,
+                                   w[2 * k + 1].x, w[2 * k + 1].y, w[2 * k + 1].z, w[2 * k + 1].w};
+            float x[8];
+            rx[k].get(x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = drop(x[i], u[i], a);
+            if (RES) {
+                float r[8];
+                rr[k].get(r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], r[i]);
+            }
+            rx[k].set(x);
+            rx[k].store(a.out, g * 8);
+        }
     }
-    for (int64_t e = groups * 8 + t0 * 4; e < a.n; e += T * 4) {
-        const uint4 v = philox(a.first + e / 4, a);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int64_t T = (int64_t)gridDim.x * kThreads;
+    for (int64_t e = groups * 8 + ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; e < a.n;
+         e += T * 4) {
+        const unsigned long long c[1] = {a.first + e / 4};
+        uint4 v[1];
+        philox<LOW>(c, a, v);
+        const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (e + i >= a.n) break;
@@ -79,32 +117,35 @@ dropout_kernel(const __grid_constant__ DropoutArgs a)
     }
 }
 
-template <int DT, bool RES, bool VEC>
-cudaError_t go(const DropoutArgs &a, int sms, cudaStream_t s)
+template <int DT, bool RES, bool VEC, bool LOW>
+cudaError_t go(const DropoutArgs &a, cudaStream_t s)
 {
-    const int per_sm = resident_blocks_per_sm(
-        reinterpret_cast<const void *>(dropout_kernel<DT, RES, VEC>), kThreads);
-    const int64_t per_block = (int64_t)kThreads * (VEC ? 8 : 4);
+    const int64_t per_block = (int64_t)kThreads * (VEC ? 8 * kGroups : 4);
     int64_t blocks = (a.n + per_block - 1) / per_block;
-    if (blocks > (int64_t)sms * per_sm) blocks = (int64_t)sms * per_sm;
-    return launch_dependent(dropout_kernel<DT, RES, VEC>, dim3((unsigned)blocks), dim3(kThreads),
+    if (VEC ? blocks > 0x7fffffff : blocks > (1 << 20)) {
+        if (VEC) return cudaErrorInvalidValue;
+        blocks = 1 << 20;       // element by element, the threads go around
+    }
+    return launch_dependent(dropout_kernel<DT, RES, VEC, LOW>, dim3((unsigned)blocks), dim3(kThreads),
                             0, s, a);
 }
 
-template <int DT> cudaError_t pick(const DropoutArgs &a, int sms, cudaStream_t s)
+template <int DT> cudaError_t pick(const DropoutArgs &a, cudaStream_t s)
 {
     const bool vec = (((uintptr_t)a.x | (uintptr_t)a.residual | (uintptr_t)a.out) & 15) == 0;
-    if (a.residual) return vec ? go<DT, true, true>(a, sms, s) : go<DT, true, false>(a, sms, s);
-    return vec ? go<DT, false, true>(a, sms, s) : go<DT, false, false>(a, sms, s);
+    const bool low = a.first + (unsigned long long)a.n / 4 < 0xffffffffull;
+    if (vec && low) return a.residual ? go<DT, true, true, true>(a, s) : go<DT, false, true, true>(a, s);
+    if (vec) return a.residual ? go<DT, true, true, false>(a, s) : go<DT, false, true, false>(a, s);
+    return a.residual ? go<DT, true, false, false>(a, s) : go<DT, false, false, false>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_dropout(int32_t dt, const DropoutArgs &a, int sms, cudaStream_t s)
+cudaError_t launch_dropout(int32_t dt, const DropoutArgs &a, cudaStream_t s)
 {
     if (a.n <= 0) return cudaSuccess;
-    return dt == F32 ? pick<F32>(a, sms, s) : dt == BF16 ? pick<BF16>(a, sms, s)
-                                                         : pick<F16>(a, sms, s);
+    return dt == F32 ? pick<F32>(a, s) : dt == BF16 ? pick<BF16>(a, s)
+                                                         : pick<F16>(a, s);
 }
 
 }  // namespace zgb

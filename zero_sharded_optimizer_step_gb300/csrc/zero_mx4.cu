@@ -29,22 +29,25 @@ __device__ __forceinline__ float block_inverse(uint32_t scale)
     return __uint_as_float((254u - (scale < 253u ? scale : 253u)) << 23);
 }
 
-// Two floats to two E2M1 codes, `lo` in the low half of the byte.
-__device__ __forceinline__ uint32_t codes2(float lo, float hi)
+// Eight floats to E2M1 codes, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8])
 {
     uint32_t r;
-    asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n cvt.u32.u8 %0, b;\n}"
-        : "=r"(r) : "f"(lo), "f"(hi));
+    asm("{\n .reg .b8 p, q, r, s;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n"
+        " mov.b32 %0, {p, q, r, s};\n}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return r;
 }
 
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float inv)
 {
-    uint32_t w = 0;
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w |= codes2(__fmul_rn(x[2 * i], inv), __fmul_rn(x[2 * i + 1], inv)) << (8 * i);
-    return w;
+    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
+    return codes8(y);
 }
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
@@ -85,6 +88,176 @@ __device__ __forceinline__ void load8(const void *x, int64_t at, int64_t c, int6
         }
     }
 }
+
+// ---- 16-bit types, two elements a word
+//
+// The largest magnitude of 16-bit floats is that of the words' halves as
+// whole numbers, two at a time; only the block's scale needs it as a float.
+
+__device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b)
+{
+    return __vmaxu2(a, b & 0x7fff7fffu);
+}
+
+// The scale byte of a block whose largest magnitude has these 15 bits.
+template <int DT> __device__ __forceinline__ uint32_t block_scale16(uint32_t top)
+{
+    if constexpr (DT == BF16) return block_scale(top << 16);
+    float lo, hi;
+    elems::widen2<F16>(top, lo, hi);
+    return block_scale(__float_as_uint(lo));
+}
+
+// A word's elements times their blocks' 2^-exponent.  Of bf16 the product is
+// taken two at a time: it is exact, or below every threshold of the rounding.
+template <int DT>
+__device__ __forceinline__ void scaled2(uint32_t w, float inv_lo, float inv_hi, float &lo,
+                                        float &hi)
+{
+    if constexpr (DT == BF16) {
+        const uint32_t inv = (__float_as_uint(inv_hi) & 0xffff0000u) | (__float_as_uint(inv_lo) >> 16);
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&inv));
+        elems::widen2<BF16>(*reinterpret_cast<const uint32_t *>(&y), lo, hi);
+    } else {
+        elems::widen2<DT>(w, lo, hi);
+        lo = __fmul_rn(lo, inv_lo);
+        hi = __fmul_rn(hi, inv_hi);
+    }
+}
+
+// 8 consecutive elements from column c of a row as words, zeros past its end.
+template <int E>
+__device__ __forceinline__ uint4 load_words(const void *x, int64_t at, int64_t c, int64_t cols)
+{
+    uint32_t w[4] = {0, 0, 0, 0};
+    const unsigned short *p = static_cast<const unsigned short *>(x) + at + c;
+    if constexpr (E == 8) {
+        if (c < cols) return *reinterpret_cast<const uint4 *>(p);
+    } else if constexpr (E == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + 2 * j < cols) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < cols) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A warp's row of 256 columns of a record, 8 elements a lane, a block over 4
+// lanes: the codes, and the scales (four blocks' are one word).
+template <int DT>
+__device__ __forceinline__ void put_row16(unsigned char *rec, int r, uint4 v)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t top = top2(top2(top2(top2(0, v.x), v.y), v.z), v.w);
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t scale = block_scale16<DT>(max(top & 0xffffu, top >> 16));
+    const float inv = block_inverse(scale);
+    float y[8];
+    scaled2<DT>(v.x, inv, inv, y[0], y[1]);
+    scaled2<DT>(v.y, inv, inv, y[2], y[3]);
+    scaled2<DT>(v.z, inv, inv, y[4], y[5]);
+    scaled2<DT>(v.w, inv, inv, y[6], y[7]);
+    uint32_t w = scale << (8 * ((lane >> 2) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    if (!rec) return;
+    *reinterpret_cast<uint32_t *>(rec + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                  (lane & 3) * 4) = codes8(y);
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(rec + scale_at(r, lane >> 2)) = w;
+}
+
+// R rows a warp, loaded before any is quantised.
+template <int DT, int E, int R>
+__global__ void __launch_bounds__(kThreads)
+mx4_rows16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t row0 = task / kt * R, t = task % kt;
+    if (row0 >= a.rows) return;
+    uint4 v[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        v[j] = row0 + j < a.rows ? load_words<E>(a.x, (row0 + j) * a.stride,
+                                                 t * kMxCols + lane * 8, a.cols)
+                                 : make_uint4(0, 0, 0, 0);
+    unsigned char *rec = a.q + ((row0 / kMxRows) * kt + t) * kMxRecord;   // R divides 128
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        put_row16<DT>(row0 + j < a.rows ? rec : nullptr, (int)(row0 % kMxRows) + j, v[j]);
+}
+
+// Both directions from one read: a block takes 64 rows by 256 columns.  The
+// rows are quantised from the registers that they were read into; through
+// shared memory every thread then takes 32 rows of two neighbouring columns,
+// which are two blocks of the transpose.  Past the matrix's last row the
+// transpose gets zeros, up to the end of its record.
+template <int DT, int E>
+__global__ void __launch_bounds__(kThreads)
+mx4_both16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt)
+{
+    __shared__ __align__(16) uint32_t strip[64][kMxCols / 2];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t ct = blockIdx.x % kt, r0 = (blockIdx.x / kt) * 64, c0 = ct * kMxCols;
+    uint4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t row = r0 + warp * 8 + j;
+        v[j] = row < a.rows ? load_words<E>(a.x, row * a.stride, c0 + lane * 8, a.cols)
+                            : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4 *>(&strip[warp * 8 + j][lane * 4]) = v[j];
+    __syncthreads();
+    if (a.q) {
+        unsigned char *rec = a.q + ((r0 / kMxRows) * kt + ct) * kMxRecord;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            put_row16<DT>(r0 + warp * 8 + j < a.rows ? rec : nullptr,
+                          (int)(r0 % kMxRows) + warp * 8 + j, v[j]);
+    }
+    const int pair = threadIdx.x & 127, half = threadIdx.x >> 7;
+    const int64_t col = c0 + 2 * pair;
+    if (!a.qt || col >= a.cols) return;
+    uint32_t w[32], top = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        w[i] = strip[half * 32 + i][pair];
+        top = top2(top, w[i]);
+    }
+    const uint32_t s0 = block_scale16<DT>(top & 0xffffu), s1 = block_scale16<DT>(top >> 16);
+    const float inv0 = block_inverse(s0), inv1 = block_inverse(s1);
+    uint32_t q0[4], q1[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float y0[8], y1[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) scaled2<DT>(w[g * 8 + i], inv0, inv1, y0[i], y1[i]);
+        q0[g] = codes8(y0);
+        q1[g] = codes8(y1);
+    }
+    unsigned char *rec = a.qt + ((col / kMxRows) * ktt + r0 / kMxCols) * kMxRecord;
+    const int r = (int)(col % kMxRows), blk = (int)(r0 % kMxCols) / 32 + half;
+    *reinterpret_cast<uint4 *>(rec + r * 128 + ((blk ^ (r & 7)) << 4)) =
+        make_uint4(q0[0], q0[1], q0[2], q0[3]);
+    rec[scale_at(r, blk)] = (unsigned char)s0;
+    if (col + 1 >= a.cols) return;
+    *reinterpret_cast<uint4 *>(rec + (r + 1) * 128 + ((blk ^ ((r + 1) & 7)) << 4)) =
+        make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    rec[scale_at(r + 1, blk)] = (unsigned char)s1;
+}
+
+// ---- fp32
 
 // A warp quantises one row's 256 columns of a record: 8 elements a lane, a
 // block over 4 lanes.
@@ -199,28 +372,41 @@ mx4_both_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt)
     if (rect) *reinterpret_cast<uint32_t *>(rect + scale_at(tr, tb0)) = tscales;
 }
 
-template <int DT, int E> cudaError_t quant_go(const MxQuantArgs &a, cudaStream_t s)
+template <int DT, int E> cudaError_t quant_go(const MxQuantArgs &a, int sms, cudaStream_t s)
 {
     const int64_t kt = (a.cols + kMxCols - 1) / kMxCols;
+    const int64_t ktt = (a.rows + kMxCols - 1) / kMxCols;
+    const int64_t limit = 0x7fffffff;
     if (!a.qt) {
-        const int64_t warps = a.rows * kt;
+        // four rows a warp once that still gives every SM a block; before that
+        // a row and warp a block, for latency
+        const bool many = DT != F32 && a.rows * kt >= (int64_t)sms * 32;
+        const int64_t warps = (many ? (a.rows + 3) / 4 : a.rows) * kt;
         const int threads = warps <= 1024 ? 32 : kThreads;
         const int64_t blocks = (warps * 32 + threads - 1) / threads;
-        if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-        return launch_dependent(mx4_rows_kernel<DT, E>, dim3((unsigned)blocks),
-                                dim3((unsigned)threads), 0, s, a, kt);
+        if (blocks > limit) return cudaErrorInvalidValue;
+        const dim3 grid((unsigned)blocks), block((unsigned)threads);
+        if constexpr (DT == F32)
+            return launch_dependent(mx4_rows_kernel<DT, E>, grid, block, 0, s, a, kt);
+        else
+            return many ? launch_dependent(mx4_rows16_kernel<DT, E, 4>, grid, block, 0, s, a, kt)
+                        : launch_dependent(mx4_rows16_kernel<DT, E, 1>, grid, block, 0, s, a, kt);
     }
-    const int64_t ktt = (a.rows + kMxCols - 1) / kMxCols;
-    const int64_t blocks = kt * ktt * 2;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_dependent(mx4_both_kernel<DT, E>, dim3((unsigned)blocks), dim3(kThreads), 0, s,
-                            a, kt, ktt);
+    const int64_t blocks = kt * ktt * (DT == F32 ? 2 : 4);
+    if (blocks > limit) return cudaErrorInvalidValue;
+    if constexpr (DT == F32)
+        return launch_dependent(mx4_both_kernel<DT, E>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                                s, a, kt, ktt);
+    else
+        return launch_dependent(mx4_both16_kernel<DT, E>, dim3((unsigned)blocks), dim3(kThreads),
+                                0, s, a, kt, ktt);
 }
 
-template <int DT> cudaError_t quant_pick(const MxQuantArgs &a, cudaStream_t s)
+template <int DT> cudaError_t quant_pick(const MxQuantArgs &a, int sms, cudaStream_t s)
 {
     const int e = row_access(a.x, a.stride, DT == F32 ? 4 : 2, a.cols);
-    return e == 8 ? quant_go<DT, 8>(a, s) : e == 2 ? quant_go<DT, 2>(a, s) : quant_go<DT, 1>(a, s);
+    return e == 8 ? quant_go<DT, 8>(a, sms, s)
+                  : e == 2 ? quant_go<DT, 2>(a, sms, s) : quant_go<DT, 1>(a, sms, s);
 }
 
 // ---------------------------------------------------------------- to values
@@ -294,11 +480,11 @@ template <int DT> cudaError_t dequant_pick(const MxDequantArgs &a, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_mx4_quantize(int32_t dt, const MxQuantArgs &a, int, cudaStream_t s)
+cudaError_t launch_mx4_quantize(int32_t dt, const MxQuantArgs &a, int sms, cudaStream_t s)
 {
     if (a.rows <= 0 || a.cols <= 0 || (!a.q && !a.qt)) return cudaSuccess;
-    return dt == F32 ? quant_pick<F32>(a, s) : dt == BF16 ? quant_pick<BF16>(a, s)
-                                                          : quant_pick<F16>(a, s);
+    return dt == F32 ? quant_pick<F32>(a, sms, s)
+                     : dt == BF16 ? quant_pick<BF16>(a, sms, s) : quant_pick<F16>(a, sms, s);
 }
 
 cudaError_t launch_mx4_dequantize(int32_t dt, const MxDequantArgs &a, cudaStream_t s)

@@ -111,10 +111,6 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr)       // 16-byte r
     return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
 }
 
-// Instruction descriptor of kind mxf4 without the scale ids: both operands
-// E2M1 and K-major, scales UE8M0, 128 lanes by NT columns.
-constexpr uint32_t kDescBase = (1u << 7) | (1u << 10) | (1u << 23) | (1u << 27);
-
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc)
 {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
@@ -183,13 +179,13 @@ constexpr int kSmemSm = 233472;      // shared memory of an SM
 constexpr int kSmemBlock = 231424;   // dynamic shared memory that leaves room for no other block
 
 template <int NT> struct Tile {
-    static constexpr int kRecs = (NT + 127) / 128;          // records of A side by side
-    static constexpr int kACodes = NT * 128;                // their codes
-    static constexpr int kStage = kMxRecord + kACodes + kRecs * kMxScales;
-    // the accumulator, 8 columns of B's scales, 8 a record of A's
-    static constexpr int kTmemUsed = NT + 8 + 8 * kRecs;
+    static_assert(NT <= 128, "a record of A at most");
+    static constexpr int kACodes = NT * 128;                // A's codes of a stage
+    static constexpr int kStage = kMxRecord + kACodes + kMxScales;
+    // the accumulator, 8 columns of B's scales, 8 of A's
+    static constexpr int kTmemUsed = NT + 16;
     static constexpr int kTmem = kTmemUsed <= 32 ? 32 : kTmemUsed <= 64 ? 64
-                                 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+                                 : kTmemUsed <= 128 ? 128 : 256;
     static constexpr int kStages = 4;                       // at most
     static constexpr int kPart = NT * 128 * 4;              // a split's partial sums
     // Shared memory of a block, for so many stages.  A block's share of it is
@@ -199,7 +195,7 @@ template <int NT> struct Tile {
     static constexpr int smem(int stages)
     {
         const int ring = stages * kStage > kPart ? stages * kStage : kPart;
-        const int share = kTmem == 512 ? kSmemBlock : (kSmemSm / (512 / kTmem) + 127) / 128 * 128;
+        const int share = (kSmemSm / (512 / kTmem) + 127) / 128 * 128;
         return ring + 1024 > share ? ring + 1024 : share;
     }
     static_assert(kStage % 1024 == 0, "stages start on the swizzle's boundary");
@@ -212,56 +208,69 @@ struct MxSplit {
     int32_t splits, stages;
 };
 
-template <int DT>
-__device__ __forceinline__ void put(const MxMatmulArgs &a, int64_t i, int64_t j, float v)
+// Element e of v, `stride` elements apart from `p` on, for the first `valid`
+// of them, times alpha and, where the call says so, added to what is there.
+template <int DT, int E>
+__device__ __forceinline__ void put_run(const MxMatmulArgs &a, int64_t at, int64_t stride,
+                                        const float (&v)[E], int valid)
 {
-    const int64_t at = i * a.stride + j;
-    v = __fmul_rn(v, a.alpha);
-    if (a.accumulate) v = __fadd_rn(elems::load1<DT>(a.out, at), v);
-    elems::store1<DT>(a.out, at, v);
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = __fmul_rn(v[e], a.alpha);
+    if (a.accumulate) {
+        float o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] = e < valid ? elems::load1<DT>(a.out, at + e * stride) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = __fadd_rn(o[e], f[e]);
+    }
+    using T = typename elems::El<DT>::T;
+    T *p = static_cast<T *>(a.out) + at;
+    if (valid >= E) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) elems::store1<DT>(p + e * stride, 0, f[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (e < valid) elems::store1<DT>(p + e * stride, 0, f[e]);
+    }
 }
 
-// Adds up the splits' partial sums, [column][lane] in every block's shared
-// memory, in the blocks' order, and writes them: this block the columns
-// rank, rank + splits, ..., a warp one at a time, 4 lanes of the tile a
-// thread.  Four columns are in flight, so that the peers' latency is paid
-// once for them.
-template <int DT, int NT>
+// Adds up the SP splits' partial sums, [column][lane] in every block's shared
+// memory, in the blocks' order, and writes them.  The blocks and threads take
+// four lanes of a column each in turn; 8 loads are in flight a thread, so that
+// the peers' latency is paid once for them.
+template <int DT, int SP>
 __device__ __forceinline__ void join(const MxMatmulArgs &a, const float *part, uint32_t rank,
-                                     int splits, int64_t i0, int64_t j0)
+                                     int64_t i0, int64_t j0, int cols)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t j = j0 + lane * 4;
-    const int cols = (int)(a.m - i0 < NT ? a.m - i0 : NT);
-    for (int c0 = (int)rank + warp * splits; c0 < cols; c0 += 16 * splits) {
-        float4 sum[4];
-        for (int q = 0; q < splits; ++q) {
-            float4 v[4];
+    constexpr int U = 8 / SP;
+    for (int first = (int)rank * 128 + threadIdx.x; first < cols * 32; first += U * SP * 128) {
+        float4 v[U][SP];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int c = c0 + u * 4 * splits;
-                if (c < cols) v[u] = load_peer4(saddr(part + c * 128 + lane * 4), q);
-            }
+        for (int u = 0; u < U; ++u) {
+            const int at = first + u * SP * 128;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (q == 0) {
-                    sum[u] = v[u];
-                } else {
-                    sum[u].x = __fadd_rn(sum[u].x, v[u].x);
-                    sum[u].y = __fadd_rn(sum[u].y, v[u].y);
-                    sum[u].z = __fadd_rn(sum[u].z, v[u].z);
-                    sum[u].w = __fadd_rn(sum[u].w, v[u].w);
-                }
-            }
+            for (int q = 0; q < SP; ++q)
+                if (at < cols * 32) v[u][q] = load_peer4(saddr(part + at * 4), q);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int c = c0 + u * 4 * splits;
-            if (c >= cols) break;
-            if (j < a.n) put<DT>(a, i0 + c, j, sum[u].x);
-            if (j + 1 < a.n) put<DT>(a, i0 + c, j + 1, sum[u].y);
-            if (j + 2 < a.n) put<DT>(a, i0 + c, j + 2, sum[u].z);
-            if (j + 3 < a.n) put<DT>(a, i0 + c, j + 3, sum[u].w);
+        for (int u = 0; u < U; ++u) {
+            const int at = first + u * SP * 128;
+            if (at >= cols * 32) break;
+            float4 sum = v[u][0];
+#pragma unroll
+            for (int q = 1; q < SP; ++q) {
+                sum.x = __fadd_rn(sum.x, v[u][q].x);
+                sum.y = __fadd_rn(sum.y, v[u][q].y);
+                sum.z = __fadd_rn(sum.z, v[u][q].z);
+                sum.w = __fadd_rn(sum.w, v[u][q].w);
+            }
+            const int64_t i = i0 + (at >> 5), j = j0 + (at & 31) * 4;
+            const float w[4] = {sum.x, sum.y, sum.z, sum.w};
+            const int64_t left = a.n - j;
+            put_run<DT, 4>(a, i * a.stride + j, 1, w, left < 4 ? (int)left : 4);
         }
     }
 }
@@ -274,18 +283,21 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t bars[2 * Tl::kStages + 1];
     __shared__ uint32_t tmem_base, failed;
-    unsigned char *ring = dyn + ((1024 - (saddr(dyn) & 1023)) & 1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = sp.splits > 1 ? cluster_rank() : 0;
     const int64_t tile = blockIdx.x / sp.splits;
     const int64_t tn = tile % sp.tiles_n, tm = tile / sp.tiles_n;
     const int64_t k0 = sp.kt * rank / sp.splits, k1 = sp.kt * (rank + 1) / sp.splits;
+    const int rounds = (int)(k1 - k0);
     const uint32_t done_bar = saddr(&bars[2 * Tl::kStages]);
     auto full = [&](int s) { return saddr(&bars[s]); };
     auto empty = [&](int s) { return saddr(&bars[Tl::kStages + s]); };
 
-    if (warp == 4) {
-        if (lane == 0) {
+    bool ok = true;
+    if (warp == 4) {                                         // the copies
+        const bool one = elect_one();
+        if (one) {
             for (int s = 0; s < Tl::kStages; ++s) {
                 bar_init(full(s), 1);
                 bar_init(empty(s), 1);
@@ -295,118 +307,117 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-    } else if (warp == 5) {
+        __syncwarp();
+        pdl_wait();
+        // a single tile holds all rows of A when it is narrower than a record
+        const unsigned char *ra = a.a + (tm * sp.kt + k0) * kMxRecord;
+        const unsigned char *rb = a.b + (tn * sp.kt + k0) * kMxRecord;
+        constexpr uint32_t bytes = kMxRecord + Tl::kACodes + kMxScales;
+        // the first stages' copies need not wait for the other warps
+        const int ahead = rounds < sp.stages ? rounds : sp.stages;
+        for (int it = 0; it < ahead; ++it, ra += kMxRecord, rb += kMxRecord)
+            if (one) {
+                const uint32_t st = ring + it * Tl::kStage;
+                bar_expect(full(it), bytes);
+                bulk_load(st, rb, kMxRecord, full(it));
+                bulk_load(st + kMxRecord, ra, Tl::kACodes, full(it));
+                bulk_load(st + kMxRecord + Tl::kACodes, ra + kMxCodes, kMxScales, full(it));
+            }
+        __syncthreads();
+        int s = 0;
+        uint32_t phase = 0;
+        for (int it = ahead; it < rounds; ++it, ra += kMxRecord, rb += kMxRecord) {
+            ok = bar_wait(empty(s), phase);
+            if (!ok) break;
+            if (one) {
+                const uint32_t st = ring + s * Tl::kStage;
+                bar_expect(full(s), bytes);
+                bulk_load(st, rb, kMxRecord, full(s));
+                bulk_load(st + kMxRecord, ra, Tl::kACodes, full(s));
+                bulk_load(st + kMxRecord + Tl::kACodes, ra + kMxCodes, kMxScales, full(s));
+            }
+            __syncwarp();
+            if (++s == sp.stages) s = 0, phase ^= 1;
+        }
+    } else if (warp == 5) {                                  // the scales and the products
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          saddr(&tmem_base)), "r"((uint32_t)Tl::kTmem) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const uint32_t tmem = tmem_base;
-    pdl_wait();
-    pdl_launch_dependents();
-
-    const int64_t arecs = (a.m + kMxRows - 1) / kMxRows;
-    const int64_t arec0 = tm * Tl::kRecs;                    // NT < 128: a record's first rows
-    const int nrec = Tl::kRecs == 2 && arec0 + 1 < arecs ? 2 : 1;
-
-    if (warp == 4 && lane == 0) {                            // the copies
-        const uint32_t bytes = kMxRecord + (NT < kMxRows ? Tl::kACodes : nrec * kMxCodes) +
-                               nrec * kMxScales;
-        for (int64_t kt = k0; kt < k1; ++kt) {
-            const int it = (int)(kt - k0), s = it % sp.stages;
-            if (it >= sp.stages && !bar_wait(empty(s), ((it / sp.stages) - 1) & 1)) {
-                atomicAdd(&g_mx4_timeouts, 1u);
-                failed = 1;
-                break;
-            }
-            const uint32_t st = saddr(ring) + s * Tl::kStage;
-            bar_expect(full(s), bytes);
-            bulk_load(st, a.b + (tn * sp.kt + kt) * kMxRecord, kMxRecord, full(s));
-            const uint32_t ac = st + kMxRecord, as = ac + Tl::kACodes;
-            for (int r = 0; r < nrec; ++r) {
-                const unsigned char *rec = a.a + ((arec0 + r) * sp.kt + kt) * kMxRecord;
-                bulk_load(ac + r * kMxCodes, rec,
-                          NT < kMxRows ? Tl::kACodes : kMxCodes, full(s));
-                bulk_load(as + r * kMxScales, rec + kMxCodes, kMxScales, full(s));
-            }
-        }
-    } else if (warp == 5 && lane == 0) {                     // the products
-        const uint32_t sb = tmem + NT, sa = sb + 8;
-        bool ok = true;
-        for (int64_t kt = k0; kt < k1; ++kt) {
-            const int it = (int)(kt - k0), s = it % sp.stages;
-            if (!bar_wait(full(s), (it / sp.stages) & 1)) {
-                ok = false;
-                break;
-            }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t st = saddr(ring) + s * Tl::kStage;
-            const uint32_t ac = st + kMxRecord, as = ac + Tl::kACodes;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                copy_scales(sb + 4 * g, scale_desc(st + kMxCodes + g * 512));
-#pragma unroll
-                for (int r = 0; r < Tl::kRecs; ++r)
-                    copy_scales(sa + 4 * (g * Tl::kRecs + r),
-                                scale_desc(as + r * kMxScales + g * 512));
-            }
-            // the record's columns past k are zeros: their products are left out
-            const int64_t left = a.k - kt * kMxCols;
-            const int steps = left >= kMxCols ? 4 : (int)((left + 63) / 64);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j >= steps) break;
-                const uint32_t id = (j & 1) * 2;             // which half of the scale words
-                mma(tmem, operand_desc(st + j * 32), operand_desc(ac + j * 32),
-                    kDescBase | ((uint32_t)(NT >> 3) << 17) | (id << 4) | (id << 29), sb + 4 * (j >> 1),
-                    sa + 4 * Tl::kRecs * (j >> 1), it > 0 || j > 0);
-            }
-            commit(empty(s));
-        }
-        if (ok) {
-            commit(done_bar);
-        } else {
-            atomicAdd(&g_mx4_timeouts, 1u);
-            failed = 1;
-        }
-    }
-    __syncwarp();
-
-    bool ok = true;
-    if (warp < 4) {
-        ok = bar_wait(done_bar, 0);
-        if (!ok && lane == 0) failed = 1;
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncthreads();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const bool one = elect_one();
+        const uint32_t tmem = tmem_base, sb = tmem + NT, sa = sb + 8;
+        constexpr uint32_t desc = (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) |
+                                  (1u << 23) | (1u << 27);
+        int s = 0;
+        uint32_t phase = 0;
+        for (int it = 0; it < rounds; ++it) {
+            ok = bar_wait(full(s), phase);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (one) {
+                const uint32_t st = ring + s * Tl::kStage;
+                const uint64_t db = operand_desc(st), da = db + (kMxRecord >> 4);
+                const uint64_t qb = scale_desc(st + kMxCodes);
+                const uint64_t qa = scale_desc(st + kMxRecord + Tl::kACodes);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    copy_scales(sb + 4 * g, qb + g * (512 >> 4));
+                    copy_scales(sa + 4 * g, qa + g * (512 >> 4));
+                }
+                // the record's columns past k are zeros: their products are left out
+                const int64_t left = a.k - (k0 + it) * kMxCols;
+                const int steps = left >= kMxCols ? 4 : (int)((left + 63) / 64);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= steps) break;
+                    const uint32_t id = (j & 1) * 2;         // which half of the scale words
+                    mma(tmem, db + j * 2, da + j * 2, desc | (id << 4) | (id << 29),
+                        sb + 4 * (j >> 1), sa + 4 * (j >> 1), it > 0 || j > 0);
+                }
+                commit(empty(s));
+            }
+            __syncwarp();
+            if (++s == sp.stages) s = 0, phase ^= 1;
+        }
+        if (ok && one) commit(done_bar);
+        __syncwarp();
+    } else {                                                 // the results
+        pdl_wait();
+        __syncthreads();
+        pdl_launch_dependents();
+        ok = bar_wait(done_bar, 0);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    if (!ok) {
+        if (lane == 0) atomicAdd(&g_mx4_timeouts, 1u);
+        failed = 1;
     }
     const int64_t j = tn * kMxRows + warp * 32 + lane;       // this thread's column of the result
     const int64_t i0 = tm * NT;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const int cols = (int)(a.m - i0 < NT ? a.m - i0 : NT);
+    const uint32_t lanes = tmem_base + ((uint32_t)(warp * 32) << 16);
     if (sp.splits == 1) {
         if (warp < 4 && ok) {
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
-                if (i0 + c >= a.m) break;
+            for (int c = 0; c < cols; c += 16) {
                 float v[16];
                 load16(lanes + c, v);
                 if (sp.kt == 0) {                            // an empty sum
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = 0.0f;
                 }
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (i0 + c + e < a.m && j < a.n) put<DT>(a, i0 + c + e, j, v[e]);
+                if (j < a.n) put_run<DT, 16>(a, (i0 + c) * a.stride + j, a.stride, v, cols - c);
             }
         }
     } else {
         // partial sums [column][lane] where the stages were: all copies have
         // landed and all products have read them
-        float *part = reinterpret_cast<float *>(ring);
+        float *part = reinterpret_cast<float *>(dyn + (ring - saddr(dyn)));
         if (warp < 4 && ok) {
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
-                if (i0 + c >= a.m) break;
+            for (int c = 0; c < cols; c += 16) {
                 float v[16];
                 load16(lanes + c, v);
 #pragma unroll
@@ -414,16 +425,20 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
             }
         }
         cluster_sync();
-        if (warp < 4 && ok) join<DT, NT>(a, part, rank, sp.splits, i0, tn * kMxRows);
+        if (warp < 4 && ok) {
+            if (sp.splits == 2) join<DT, 2>(a, part, rank, i0, tn * kMxRows, cols);
+            else if (sp.splits == 4) join<DT, 4>(a, part, rank, i0, tn * kMxRows, cols);
+            else join<DT, 8>(a, part, rank, i0, tn * kMxRows, cols);
+        }
         cluster_sync();       // the peers have read this block's shared memory
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
-        for (int s = 0; s < Tl::kStages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
+        for (int s = 0; s < sp.stages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
     __syncthreads();
     if (warp == 5)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"((uint32_t)Tl::kTmem));
 }
 
@@ -553,8 +568,11 @@ __device__ __forceinline__ void put_row32(const MxMatmulArgs &a, int64_t i, int6
 #pragma unroll
     for (int h = 0; h < 32 / kPer; ++h) {
         if (j + (h + 1) * kPer > a.n) {                      // the row's ragged end
-            for (int e = h * kPer; e < (h + 1) * kPer; ++e)
-                if (j + e < a.n) put<DT>(a, i, j + e, __uint_as_float(r[e]));
+            float v[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) v[e] = __uint_as_float(r[h * kPer + e]);
+            const int64_t left = a.n - (j + h * kPer);
+            put_run<DT, kPer>(a, at + h * kPer, 1, v, left < 0 ? 0 : (int)left);
             continue;
         }
         float f[kPer];
@@ -755,9 +773,12 @@ mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ 
                 if constexpr (WIDE) {
                     if (l < a.m) put_row32<DT>(a, l, c0 + c, r);
                 } else if (l < a.n) {
+                    const int64_t left = a.m - (c0 + c);
+                    float v[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c0 + c + e < a.m) put<DT>(a, c0 + c + e, l, __uint_as_float(r[e]));
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+                    put_run<DT, 32>(a, (c0 + c) * a.stride + l, a.stride, v,
+                                    left < 32 ? (int)left : 32);
                 }
             }
             b ^= 1;
@@ -869,18 +890,19 @@ cudaError_t mm_go(const MxMatmulArgs &a, int sms, cudaStream_t s)
     sp.kt = (a.k + kMxCols - 1) / kMxCols;
     sp.tiles_n = (a.n + kMxRows - 1) / kMxRows;
     const int64_t tiles = sp.tiles_n * ((a.m + NT - 1) / NT);
-    // halve the columns while there are places without a block (as many
-    // per SM as shared memory lets in) and each part keeps two records
+    // Halve the columns while the blocks still find places (as many per SM
+    // as shared memory lets in) and every part keeps two records.
     sp.splits = 1;
-    for (;;) {
-        const int64_t most = (sp.kt + sp.splits - 1) / sp.splits;
-        sp.stages = most < Tl::kStages ? (most > 0 ? (int)most : 1) : Tl::kStages;
-        const int64_t next = (most + 1) / 2;
-        const int st = next < Tl::kStages ? (int)next : Tl::kStages;
-        const int64_t places = (int64_t)sms * (kSmemSm / (Tl::smem(st > 0 ? st : 1) + 1024));
-        if (sp.splits == 8 || sp.kt < 4 * sp.splits || tiles * sp.splits * 2 > places) break;
+    auto stages = [&](int splits) {
+        const int64_t most = (sp.kt + splits - 1) / splits;
+        return most < 1 ? 1 : most < Tl::kStages ? (int)most : Tl::kStages;
+    };
+    while (sp.splits < 8 && sp.kt >= 4 * sp.splits) {
+        const int64_t per_sm = kSmemSm / (Tl::smem(stages(2 * sp.splits)) + 1024);
+        if (tiles * sp.splits * 2 > sms * per_sm) break;
         sp.splits *= 2;
     }
+    sp.stages = stages(sp.splits);
     const int64_t blocks = tiles * sp.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
@@ -902,14 +924,19 @@ cudaError_t mm_go(const MxMatmulArgs &a, int sms, cudaStream_t s)
 
 template <int DT> cudaError_t mm_pick(const MxMatmulArgs &a, int sms, cudaStream_t s)
 {
-    const int64_t pairs = ((a.n + 255) / 256) * ((a.m + 255) / 256);
+    // Few rows, or no more tiles of 128 by 128 than SMs: the single blocks, whose
+    // columns can be split (4096 x 4096 by 512 rows, 128 tiles: 7.5 us against the
+    // pairs' 10.2).  Beyond that the pairs (768 rows, 192 tiles: 10.5 us against
+    // 13.6).
+    const int64_t tiles = ((a.n + 127) / 128) * ((a.m + 127) / 128);
     int64_t la, lb;
-    if (a.k > 0 && pairs >= sms / 4 && pair_lines(a, la, lb)) {
+    if (a.k > 0 && a.m > 64 && tiles > sms && pair_lines(a, la, lb)) {
         const int es = DT == F32 ? 4 : 2;
         const bool wide = ((uintptr_t)a.out & 31) == 0 && a.stride * es % 32 == 0;
         return wide ? pair_go<DT, true>(a, sms, s) : pair_go<DT, false>(a, sms, s);
     }
     return a.m <= 16 ? mm_go<DT, 16>(a, sms, s)
+           : a.m <= 32 ? mm_go<DT, 32>(a, sms, s)
            : a.m <= 64 ? mm_go<DT, 64>(a, sms, s) : mm_go<DT, 128>(a, sms, s);
 }
 

@@ -68,12 +68,17 @@ struct DropoutArgs {
     const void *x, *residual;
     void *out;
     int64_t n;
-    unsigned long long threshold;   // keep where the 32-bit word >= threshold
+    uint32_t threshold;             // keep where the word >= threshold,
+    int32_t any;                    // unless p = 1: 2^32 is no 32-bit threshold
     float up;                       // 1 / (1 - p)
-    uint32_t key0, key1, off0, off1;
+    uint32_t key0[10], key1[10];    // the rounds' keys
+    uint32_t off0, off1;
+    // What the first two rounds make of the offset alone, for counters below
+    // 2^32 (zero_dropout.cu)
+    uint32_t pre[4];
     unsigned long long first;       // counter of element 0 (first element / 4)
 };
-cudaError_t launch_dropout(int32_t dt, const DropoutArgs &a, int sms, cudaStream_t s);
+cudaError_t launch_dropout(int32_t dt, const DropoutArgs &a, cudaStream_t s);
 
 // ---- microscaled 4-bit matrices
 //

@@ -158,7 +158,7 @@ int zero_dropout(const void *x, const void *residual, void *out, int32_t dtype, 
                  double p, uint64_t seed, uint64_t offset, int64_t first, void *stream)
 {
     if (!valid_dtype(dtype)) return report(ZERO_EINVAL, "unknown element type %d", dtype);
-    if (n < 0 || n > (1ll << 60)) return report(ZERO_EINVAL, "%lld elements", (long long)n);
+    if (n < 0 || n > (1ll << 42)) return report(ZERO_EINVAL, "%lld elements", (long long)n);
     if (!(p >= 0.0 && p <= 1.0)) return report(ZERO_EINVAL, "p must be in [0, 1]");
     if (first < 0 || first % 4)
         return report(ZERO_EINVAL, "the first element must be a multiple of 4, not %lld",
@@ -168,21 +168,31 @@ int zero_dropout(const void *x, const void *residual, void *out, int32_t dtype, 
     if (!aligned(x, es) || !aligned(residual, es) || !aligned(out, es))
         return report(ZERO_EALIGN, "x, residual and out must be aligned to %d bytes", es);
     if (n == 0) return ZERO_OK;
-    const int sms = sm_count();
-    if (!sms) return ZERO_ECUDA;
     zgb::DropoutArgs a = {};
     a.x = x;
     a.residual = residual;
     a.out = out;
     a.n = n;
-    a.threshold = (unsigned long long)std::floor(p * 4294967296.0);
+    const double words = std::floor(p * 4294967296.0);
+    a.any = words < 4294967296.0;
+    a.threshold = a.any ? (uint32_t)words : 0;
     a.up = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.0f;
-    a.key0 = (uint32_t)seed;
-    a.key1 = (uint32_t)(seed >> 32);
+    for (uint32_t r = 0; r < 10; ++r) {
+        a.key0[r] = (uint32_t)seed + r * 0x9E3779B9u;
+        a.key1[r] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+    }
     a.off0 = (uint32_t)offset;
     a.off1 = (uint32_t)(offset >> 32);
     a.first = (unsigned long long)first / 4;
-    return launched(zgb::launch_dropout(dtype, a, sms, (cudaStream_t)stream), "dropout");
+    {   // round 1's product of off0, and round 2's of the word that it makes
+        const uint64_t p1 = (uint64_t)a.off0 * 0xCD9E8D57u;
+        const uint64_t p0 = (uint64_t)((uint32_t)(p1 >> 32) ^ a.key0[0]) * 0xD2511F53u;
+        a.pre[0] = a.off1 ^ a.key1[0];
+        a.pre[1] = (uint32_t)p1 ^ a.key0[1];
+        a.pre[2] = (uint32_t)(p0 >> 32) ^ a.key1[1];
+        a.pre[3] = (uint32_t)p0;
+    }
+    return launched(zgb::launch_dropout(dtype, a, (cudaStream_t)stream), "dropout");
 }
 
 int64_t zero_mx4_bytes(int64_t rows, int64_t cols)
