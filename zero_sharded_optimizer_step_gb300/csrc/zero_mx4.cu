@@ -90,13 +90,19 @@ __device__ __forceinline__ void load8(const void *x, int64_t at, int64_t c, int6
 }
 
 // ---- 16-bit types, two elements a word
-//
-// The largest magnitude of 16-bit floats is that of the words' halves as
-// whole numbers, two at a time; only the block's scale needs it as a float.
 
-__device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b)
+// The larger magnitudes of two words' elements; NaN where one is.
+template <int DT> __device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b)
 {
-    return __vmaxu2(a, b & 0x7fff7fffu);
+    if constexpr (DT == BF16) {
+        const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<__nv_bfloat162 *>(&a)),
+                                             __habs2(*reinterpret_cast<__nv_bfloat162 *>(&b)));
+        return *reinterpret_cast<const uint32_t *>(&m);
+    } else {
+        const __half2 m = __hmax2_nan(__habs2(*reinterpret_cast<__half2 *>(&a)),
+                                      __habs2(*reinterpret_cast<__half2 *>(&b)));
+        return *reinterpret_cast<const uint32_t *>(&m);
+    }
 }
 
 // The scale byte of a block whose largest magnitude has these 15 bits.
@@ -152,9 +158,9 @@ template <int DT>
 __device__ __forceinline__ void put_row16(unsigned char *rec, int r, uint4 v)
 {
     const int lane = threadIdx.x & 31;
-    uint32_t top = top2(top2(top2(top2(0, v.x), v.y), v.z), v.w);
-    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    uint32_t top = top2<DT>(top2<DT>(v.x, v.y), top2<DT>(v.z, v.w));
+    top = top2<DT>(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = top2<DT>(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const uint32_t scale = block_scale16<DT>(max(top & 0xffffu, top >> 16));
     const float inv = block_inverse(scale);
     float y[8];
@@ -171,8 +177,8 @@ __device__ __forceinline__ void put_row16(unsigned char *rec, int r, uint4 v)
     if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(rec + scale_at(r, lane >> 2)) = w;
 }
 
-// R rows a warp, loaded before any is quantised.
-template <int DT, int E, int R>
+// Few rows: a warp a row.
+template <int DT, int E>
 __global__ void __launch_bounds__(kThreads)
 mx4_rows16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt)
 {
@@ -180,25 +186,18 @@ mx4_rows16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt)
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int64_t row0 = task / kt * R, t = task % kt;
-    if (row0 >= a.rows) return;
-    uint4 v[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-        v[j] = row0 + j < a.rows ? load_words<E>(a.x, (row0 + j) * a.stride,
-                                                 t * kMxCols + lane * 8, a.cols)
-                                 : make_uint4(0, 0, 0, 0);
-    unsigned char *rec = a.q + ((row0 / kMxRows) * kt + t) * kMxRecord;   // R divides 128
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-        put_row16<DT>(row0 + j < a.rows ? rec : nullptr, (int)(row0 % kMxRows) + j, v[j]);
+    const int64_t row = task / kt, t = task - row * kt;
+    if (row >= a.rows) return;
+    put_row16<DT>(a.q + ((row / kMxRows) * kt + t) * kMxRecord, (int)(row % kMxRows),
+                  load_words<E>(a.x, row * a.stride, t * kMxCols + lane * 8, a.cols));
 }
 
-// Both directions from one read: a block takes 64 rows by 256 columns.  The
-// rows are quantised from the registers that they were read into; through
-// shared memory every thread then takes 32 rows of two neighbouring columns,
-// which are two blocks of the transpose.  Past the matrix's last row the
-// transpose gets zeros, up to the end of its record.
+// Either direction, or both from one read: a block takes 64 rows by 256
+// columns through shared memory.  For q a thread takes 32 columns of a row, a
+// block of the matrix, twice; for qt 32 rows of two neighbouring columns, two blocks
+// of its transpose: neither needs another thread's elements for its scale.
+// Past the matrix's last row the transpose gets zeros, up to the end of its
+// record.
 template <int DT, int E>
 __global__ void __launch_bounds__(kThreads)
 mx4_both16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt)
@@ -208,23 +207,58 @@ mx4_both16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t ct = blockIdx.x % kt, r0 = (blockIdx.x / kt) * 64, c0 = ct * kMxCols;
-    uint4 v[8];
+    {
+        uint4 v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int64_t row = r0 + warp * 8 + j;
-        v[j] = row < a.rows ? load_words<E>(a.x, row * a.stride, c0 + lane * 8, a.cols)
-                            : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 8; ++j) {
+            const int64_t row = r0 + warp * 8 + j;
+            v[j] = row < a.rows ? load_words<E>(a.x, row * a.stride, c0 + lane * 8, a.cols)
+                                : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4 *>(&strip[warp * 8 + j][lane * 4]) = v[j];
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4 *>(&strip[warp * 8 + j][lane * 4]) = v[j];
     __syncthreads();
     if (a.q) {
         unsigned char *rec = a.q + ((r0 / kMxRows) * kt + ct) * kMxRecord;
+        // a thread's four 16-byte pieces start at another one in every second
+        // thread, so that eight threads' reads fall into different banks
+        const int blk = threadIdx.x & 7, turn = blk >> 1;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            put_row16<DT>(r0 + warp * 8 + j < a.rows ? rec : nullptr,
-                          (int)(r0 % kMxRows) + warp * 8 + j, v[j]);
+        for (int half = 0; half < 2; ++half) {
+            const int sr = half * 32 + (threadIdx.x >> 3);
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = *reinterpret_cast<const uint4 *>(
+                    &strip[sr][blk * 16 + ((j + turn) & 3) * 4]);
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                top = top2<DT>(top, top2<DT>(top2<DT>(v[j].x, v[j].y), top2<DT>(v[j].z, v[j].w)));
+            const uint32_t scale = block_scale16<DT>(max(top & 0xffffu, top >> 16));
+            const float inv = block_inverse(scale);
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float y[8];
+                scaled2<DT>(v[j].x, inv, inv, y[0], y[1]);
+                scaled2<DT>(v[j].y, inv, inv, y[2], y[3]);
+                scaled2<DT>(v[j].z, inv, inv, y[4], y[5]);
+                scaled2<DT>(v[j].w, inv, inv, y[6], y[7]);
+                w[j] = codes8(y);
+            }
+            // w[j] is piece (j + turn) & 3: turn them back
+            const uint32_t u0 = turn & 1 ? w[3] : w[0], u1 = turn & 1 ? w[0] : w[1];
+            const uint32_t u2 = turn & 1 ? w[1] : w[2], u3 = turn & 1 ? w[2] : w[3];
+            const uint4 out = turn & 2 ? make_uint4(u2, u3, u0, u1) : make_uint4(u0, u1, u2, u3);
+            if (r0 + sr < a.rows) {
+                const int r = (int)(r0 % kMxRows) + sr;
+                *reinterpret_cast<uint4 *>(rec + r * 128 + ((blk ^ (r & 7)) << 4)) = out;
+                rec[scale_at(r, blk)] = (unsigned char)scale;
+            }
+        }
     }
     const int pair = threadIdx.x & 127, half = threadIdx.x >> 7;
     const int64_t col = c0 + 2 * pair;
@@ -233,7 +267,7 @@ mx4_both16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         w[i] = strip[half * 32 + i][pair];
-        top = top2(top, w[i]);
+        top = top2<DT>(top, w[i]);
     }
     const uint32_t s0 = block_scale16<DT>(top & 0xffffu), s1 = block_scale16<DT>(top >> 16);
     const float inv0 = block_inverse(s0), inv1 = block_inverse(s1);
@@ -377,11 +411,8 @@ template <int DT, int E> cudaError_t quant_go(const MxQuantArgs &a, int sms, cud
     const int64_t kt = (a.cols + kMxCols - 1) / kMxCols;
     const int64_t ktt = (a.rows + kMxCols - 1) / kMxCols;
     const int64_t limit = 0x7fffffff;
-    if (!a.qt) {
-        // four rows a warp once that still gives every SM a block; before that
-        // a row and warp a block, for latency
-        const bool many = DT != F32 && a.rows * kt >= (int64_t)sms * 32;
-        const int64_t warps = (many ? (a.rows + 3) / 4 : a.rows) * kt;
+    if (!a.qt && (DT == F32 || a.rows * kt < (int64_t)sms * 32)) {
+        const int64_t warps = a.rows * kt;
         const int threads = warps <= 1024 ? 32 : kThreads;
         const int64_t blocks = (warps * 32 + threads - 1) / threads;
         if (blocks > limit) return cudaErrorInvalidValue;
@@ -389,8 +420,7 @@ template <int DT, int E> cudaError_t quant_go(const MxQuantArgs &a, int sms, cud
         if constexpr (DT == F32)
             return launch_dependent(mx4_rows_kernel<DT, E>, grid, block, 0, s, a, kt);
         else
-            return many ? launch_dependent(mx4_rows16_kernel<DT, E, 4>, grid, block, 0, s, a, kt)
-                        : launch_dependent(mx4_rows16_kernel<DT, E, 1>, grid, block, 0, s, a, kt);
+            return launch_dependent(mx4_rows16_kernel<DT, E>, grid, block, 0, s, a, kt);
     }
     const int64_t blocks = kt * ktt * (DT == F32 ? 2 : 4);
     if (blocks > limit) return cudaErrorInvalidValue;
@@ -430,7 +460,9 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t scale, float (&f)[8
     }
 }
 
-template <int DT, int E>
+// A warp takes R rows' 256 columns of a record, all read before any is
+// written; 8 elements of a row a lane.  R divides 128.
+template <int DT, int E, int R>
 __global__ void __launch_bounds__(kThreads)
 mx4_values_kernel(const __grid_constant__ MxDequantArgs a, int64_t kt)
 {
@@ -438,44 +470,60 @@ mx4_values_kernel(const __grid_constant__ MxDequantArgs a, int64_t kt)
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int64_t row = task / kt, t = task - row * kt;
-    if (row >= a.rows) return;
-    const unsigned char *rec = a.q + ((row / kMxRows) * kt + t) * kMxRecord;
-    const int r = (int)(row % kMxRows);
+    const int64_t row0 = task / kt * R, t = task % kt;
     const int64_t c = t * kMxCols + lane * 8;
-    if (c >= a.cols) return;
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(
-        rec + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-    float f[8];
-    values8(w, rec[scale_at(r, lane >> 2)], f);
+    if (row0 >= a.rows || c >= a.cols) return;
+    const unsigned char *rec = a.q + ((row0 / kMxRows) * kt + t) * kMxRecord;
+    const int r0 = (int)(row0 % kMxRows);
+    uint32_t w[R], scale[R];
 #pragma unroll
-    for (int j = 0; j < 8 / E; ++j) {
-        if (c + j * E >= a.cols) break;
-        elems::Raw<DT, E> o;
-        float g[E];
+    for (int j = 0; j < R; ++j) {
+        const int r = r0 + j;
+        if (row0 + j < a.rows) {
+            w[j] = *reinterpret_cast<const uint32_t *>(
+                rec + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+            scale[j] = rec[scale_at(r, lane >> 2)];
+        }
+    }
 #pragma unroll
-        for (int e = 0; e < E; ++e) g[e] = f[j * E + e];
-        o.set(g);
-        o.store(a.out, row * a.stride + c + j * E);
+    for (int j = 0; j < R; ++j) {
+        if (row0 + j >= a.rows) break;
+        float f[8];
+        values8(w[j], scale[j], f);
+        const int64_t at = (row0 + j) * a.stride + c;
+#pragma unroll
+        for (int i = 0; i < 8 / E; ++i) {
+            if (c + i * E >= a.cols) break;
+            elems::Raw<DT, E> o;
+            float g[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) g[e] = f[i * E + e];
+            o.set(g);
+            o.store(a.out, at + i * E);
+        }
     }
 }
 
-template <int DT, int E> cudaError_t dequant_go(const MxDequantArgs &a, cudaStream_t s)
+template <int DT, int E> cudaError_t dequant_go(const MxDequantArgs &a, int sms, cudaStream_t s)
 {
     const int64_t kt = (a.cols + kMxCols - 1) / kMxCols;
-    const int64_t warps = a.rows * kt;
+    // an fp32 row is long enough to keep its warp busy: 27 us against 34 of four
+    // rows for 8192 x 4096
+    const bool many = DT != F32 && a.rows * kt >= (int64_t)sms * 64;
+    const int64_t warps = (many ? (a.rows + 3) / 4 : a.rows) * kt;
     const int threads = warps <= 1024 ? 32 : kThreads;
     const int64_t blocks = (warps * 32 + threads - 1) / threads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_dependent(mx4_values_kernel<DT, E>, dim3((unsigned)blocks),
-                            dim3((unsigned)threads), 0, s, a, kt);
+    const dim3 grid((unsigned)blocks), block((unsigned)threads);
+    return many ? launch_dependent(mx4_values_kernel<DT, E, 4>, grid, block, 0, s, a, kt)
+                : launch_dependent(mx4_values_kernel<DT, E, 1>, grid, block, 0, s, a, kt);
 }
 
-template <int DT> cudaError_t dequant_pick(const MxDequantArgs &a, cudaStream_t s)
+template <int DT> cudaError_t dequant_pick(const MxDequantArgs &a, int sms, cudaStream_t s)
 {
     const int e = row_access(a.out, a.stride, DT == F32 ? 4 : 2, a.cols);
-    return e == 8 ? dequant_go<DT, 8>(a, s)
-                  : e == 2 ? dequant_go<DT, 2>(a, s) : dequant_go<DT, 1>(a, s);
+    return e == 8 ? dequant_go<DT, 8>(a, sms, s)
+                  : e == 2 ? dequant_go<DT, 2>(a, sms, s) : dequant_go<DT, 1>(a, sms, s);
 }
 
 }  // namespace
@@ -487,11 +535,11 @@ cudaError_t launch_mx4_quantize(int32_t dt, const MxQuantArgs &a, int sms, cudaS
                      : dt == BF16 ? quant_pick<BF16>(a, sms, s) : quant_pick<F16>(a, sms, s);
 }
 
-cudaError_t launch_mx4_dequantize(int32_t dt, const MxDequantArgs &a, cudaStream_t s)
+cudaError_t launch_mx4_dequantize(int32_t dt, const MxDequantArgs &a, int sms, cudaStream_t s)
 {
     if (a.rows <= 0 || a.cols <= 0) return cudaSuccess;
-    return dt == F32 ? dequant_pick<F32>(a, s) : dt == BF16 ? dequant_pick<BF16>(a, s)
-                                                            : dequant_pick<F16>(a, s);
+    return dt == F32 ? dequant_pick<F32>(a, sms, s) : dt == BF16 ? dequant_pick<BF16>(a, sms, s)
+                                                            : dequant_pick<F16>(a, sms, s);
 }
 
 }  // namespace zgb

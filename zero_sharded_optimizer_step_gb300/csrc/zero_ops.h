@@ -105,7 +105,7 @@ struct MxDequantArgs {
     int64_t rows, cols, stride;
     void *out;
 };
-cudaError_t launch_mx4_dequantize(int32_t dt, const MxDequantArgs &a, cudaStream_t s);
+cudaError_t launch_mx4_dequantize(int32_t dt, const MxDequantArgs &a, int sms, cudaStream_t s);
 
 struct MxMatmulArgs {
     const unsigned char *a, *b;  // [m, k] and [n, k]

@@ -224,8 +224,11 @@ int zero_mx4_dequantize(const void *q, int64_t rows, int64_t cols, void *out, in
     ZERO_TRY(check_records("q", q, rows, cols));
     ZERO_TRY(check_matrix("out", out, dtype, rows, cols, stride));
     if (rows == 0 || cols == 0) return ZERO_OK;
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
     zgb::MxDequantArgs a = {static_cast<const unsigned char *>(q), rows, cols, stride, out};
-    return launched(zgb::launch_mx4_dequantize(dtype, a, (cudaStream_t)stream), "the values");
+    return launched(zgb::launch_mx4_dequantize(dtype, a, sms, (cudaStream_t)stream),
+                    "the values");
 }
 
 int zero_mx4_matmul(const void *a, int64_t m, const void *b, int64_t n, int64_t k, float alpha,
