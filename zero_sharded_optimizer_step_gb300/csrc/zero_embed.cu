@@ -94,15 +94,31 @@ template <int DT> cudaError_t embed_pick(const EmbedArgs &a, cudaStream_t s)
 
 // ----------------------------------------------------------------- the sort
 //
-// A stable radix sort of (id, position) by 8-bit digits, lowest first; ids
-// that name no row sort behind all rows.  Up to kSmallTokens tokens one block
-// sorts in shared memory; beyond that every pass is two launches over
-// at most 256 blocks: digit counts per block, then each block adds up the
-// counts before its own and places its tokens.
+// (id, position) pairs in order of id, then position; ids that name no row
+// come last.  Three ways, by the number of tokens:
+//   up to kRankTokens     every token's place is counted outright, as the number of
+//                         pairs that come before its own: n^2 comparisons (3 ALU
+//                         operations each, 11 us for 8192 tokens), but no
+//                         step that waits for another
+//   up to kSmallTokens    a stable radix sort by 8-bit digits, lowest first, in one
+//                         launch: a cluster of up to 8 blocks with a token a thread,
+//                         whose digit counts and tokens go through
+//                         distributed shared memory
+//   more                  the same over up to 256 blocks, a launch a digit: a block
+//                         adds up the digit counts of the blocks before it,
+//                         places its tokens, and counts the next digit
+//                         where they land
 constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kRankTokens = 2048;
 constexpr int kSmallTokens = 8192;
-constexpr int kSortTile = 4096;
+constexpr int64_t kSmallRows = 1 << 19;      // id and position in one word
+constexpr int kSortTile = 2048;
 constexpr int kMaxSortBlocks = 256;
+
+bool sort_small(const EmbedGradArgs &a)
+{
+    return a.tok.n <= kSmallTokens && a.tok.rows < kSmallRows;
+}
 
 int sort_passes(int64_t rows)
 {
@@ -111,7 +127,7 @@ int sort_passes(int64_t rows)
     return p;
 }
 
-int64_t sort_chunk(int64_t n)   // tokens per block of the multi-block sort
+int64_t sort_chunk(int64_t n)   // tokens per block of the radix sort
 {
     const int64_t per = (n + kMaxSortBlocks - 1) / kMaxSortBlocks;
     return (per + kSortTile - 1) / kSortTile * kSortTile;
@@ -137,14 +153,14 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t d, bool live)
 
 // Exclusive prefix over the 32 warps of every digit's counts, in place; the
 // digits' totals go to total[256].
-__device__ __forceinline__ void prefix_warps(uint32_t (*count)[256], uint32_t *total)
+__device__ __forceinline__ void prefix_warps(unsigned short (*count)[256], uint32_t *total)
 {
     for (int d = threadIdx.x; d < 256; d += kSortThreads) {
         uint32_t run = 0;
 #pragma unroll 8
         for (int w = 0; w < kSortWarps; ++w) {
             const uint32_t v = count[w][d];
-            count[w][d] = run;
+            count[w][d] = (unsigned short)run;
             run += v;
         }
         total[d] = run;
@@ -176,147 +192,212 @@ __device__ __forceinline__ void prefix_digits(uint32_t *v)
     }
 }
 
-struct SmallSort {
-    uint32_t count[kSortWarps][256];
-    uint32_t total[256];
-    uint32_t key[2][kSmallTokens];
-    unsigned short idx[2][kSmallTokens];
-};
+// A gradient that is not added to has zeros in the rows that no token names.
+// The sort is bound by latency, so its launches have blocks of their own that
+// zero all rows meanwhile; the sums then write those again that a token names.
 
-// Zeroes rows of the gradient: `warps` warps of the grid, this one `warp`,
-// a row each in turn; with `used`, only the rows that no token names.
+// Rows lo .. hi, a row each in turn: this is warp `warp` of `warps`.
 template <int GT, int E>
-__device__ __forceinline__ void zero_rows(const EmbedGradArgs &a, const unsigned char *used,
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs &a, int64_t lo, int64_t hi,
                                           int64_t warp, int64_t warps)
 {
-    const int lane = threadIdx.x & 31;
     elems::Raw<GT, E> z;
     z.zero();
-    for (int64_t r = warp; r < a.tok.rows; r += warps) {
-        if (used && used[r]) continue;
-        for (int64_t c = (int64_t)lane * E; c < a.dim; c += 32 * E)
+    for (int64_t r = lo + warp; r < hi; r += warps)
+        for (int64_t c = (int64_t)(threadIdx.x & 31) * E; c < a.dim; c += 32 * E)
             z.store(a.grad, r * a.grad_stride + c);
-    }
 }
 
-// Block 0 sorts; the others zero the gradient meanwhile (unless it is added
-// to): the rows that tokens name are written again afterwards, at most
-// kSmallTokens of them, which costs less than the sort that it hides.
+// The first rank_blocks blocks place the tokens: 32 of them a block, one a
+// lane, each warp against an eighth of the list, which it reads from shared
+// memory four pairs at a time, the same for all lanes.
 template <int GT, int E>
-__global__ void __launch_bounds__(kSortThreads)
-embed_sort_small_kernel(const __grid_constant__ EmbedGradArgs a, int passes)
+__global__ void __launch_bounds__(kThreads)
+embed_rank_kernel(const __grid_constant__ EmbedGradArgs a, int rank_blocks)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    SmallSort &sm = *reinterpret_cast<SmallSort *>(raw);
+    __shared__ __align__(16) uint32_t pairs[kRankTokens];
+    __shared__ uint32_t part[8][32];
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (blockIdx.x != 0) {
-        zero_rows<GT, E>(a, nullptr, (int64_t)(blockIdx.x - 1) * kSortWarps + warp,
-                         (int64_t)(gridDim.x - 1) * kSortWarps);
+    if ((int)blockIdx.x >= rank_blocks) {
+        zero_rows<GT, E>(a, 0, a.tok.rows, (int64_t)(blockIdx.x - rank_blocks) * 8 + warp,
+                         (int64_t)(gridDim.x - rank_blocks) * 8);
         return;
     }
     const int n = (int)a.tok.n;
-    if (threadIdx.x == 0) *a.n_runs = 0;
-    const int iters = (n + kSortThreads - 1) / kSortThreads;     // <= 8
-    for (int i = threadIdx.x; i < n; i += kSortThreads) {
-        sm.key[0][i] = token_key(a.tok, i);
-        sm.idx[0][i] = (unsigned short)i;
-    }
-    int from = 0;
-    for (int p = 0; p < passes; ++p) {
-        for (int i = threadIdx.x; i < kSortWarps * 256; i += kSortThreads)
-            (&sm.count[0][0])[i] = 0;
-        __syncthreads();
-        uint32_t key[8], rank[8];
-        unsigned short idx[8];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_runs = 0;
+    // eight warps' whole rounds of 16, the last filled up with what comes after all
+    const int padded = (n + 127) / 128 * 128;
+    uint32_t k[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= iters) break;
-            const int i = (warp * iters + j) * 32 + lane;
-            const bool live = i < n;
-            key[j] = live ? sm.key[from][i] : kNone;
-            idx[j] = live ? sm.idx[from][i] : 0;
-            const uint32_t d = (key[j] >> (8 * p)) & 255u;
-            const uint32_t peers = same_digit(d, live);
-            uint32_t before = 0;
-            if (live) before = sm.count[warp][d];
-            __syncwarp();
-            rank[j] = before + __popc(peers & ((1u << lane) - 1));
-            if (live && (peers >> lane) == 1u) sm.count[warp][d] = before + __popc(peers);
-            __syncwarp();
-        }
-        __syncthreads();
-        prefix_warps(sm.count, sm.total);
-        __syncthreads();
-        prefix_digits(sm.total);
-        __syncthreads();
-        const int to = from ^ 1;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= iters) break;
-            const int i = (warp * iters + j) * 32 + lane;
-            if (i < n) {
-                const uint32_t d = (key[j] >> (8 * p)) & 255u;
-                const uint32_t at = sm.total[d] + sm.count[warp][d] + rank[j];
-                sm.key[to][at] = key[j];
-                sm.idx[to][at] = idx[j];
-            }
-        }
-        __syncthreads();
-        from = to;
+    for (int u = 0; u < 8; ++u) {
+        const int i = (int)threadIdx.x + u * kThreads;
+        k[u] = i < n ? token_key(a.tok, i) << 13 | (uint32_t)i : kNone;
     }
-    for (int i = threadIdx.x; i < n; i += kSortThreads) {
-        a.key[0][i] = sm.key[from][i];
-        a.idx[0][i] = sm.idx[from][i];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) pairs[threadIdx.x + u * kThreads] = k[u];
+    __syncthreads();
+    const int i = (int)blockIdx.x * 32 + lane;
+    const uint32_t own = i < n ? pairs[i] : 0u;
+    uint32_t before = 0;
+    const uint4 *v = reinterpret_cast<const uint4 *>(pairs) + warp * (padded / 32);
+    for (int j = 0; j < padded / 128; ++j, v += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint4 p = v[u];
+            before += (p.x < own) + (p.y < own) + (p.z < own) + (p.w < own);
+        }
+    }
+    part[warp][lane] = before;
+    __syncthreads();
+    if (warp == 0 && i < n) {
+        uint32_t at = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) at += part[w][lane];
+        a.key[0][at] = own >> 13;
+        a.idx[0][at] = (uint32_t)i;
     }
 }
 
-// Digit counts of a block's tokens.  The first pass reads the tokens
-// themselves, clears the map of used rows and the count of long runs.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_peer(const void *p, uint32_t rank, uint32_t v)
+{
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// The first cluster sorts, the other blocks zero rows.  A pair is one
+// word (id << 13 | position), a thread has one in every pass.
+template <int GT, int E>
 __global__ void __launch_bounds__(kSortThreads)
-embed_count_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int64_t chunk)
+embed_cluster_kernel(const __grid_constant__ EmbedGradArgs a, int passes, int blocks)
+{
+    __shared__ uint32_t list[2][kSortThreads];
+    __shared__ unsigned short count[kSortWarps][256];
+    __shared__ uint32_t total[256], hist[8][256], sum[256], before[256];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((int)blockIdx.x >= blocks) {
+        zero_rows<GT, E>(a, 0, a.tok.rows,
+                         (int64_t)(blockIdx.x - blocks) * kSortWarps + warp,
+                         (int64_t)(gridDim.x - blocks) * kSortWarps);
+        return;
+    }
+    const uint32_t rank = cluster_rank();
+    const int n = (int)a.tok.n, i = (int)rank * kSortThreads + (int)threadIdx.x;
+    const bool live = i < n;                  // the places 0 .. n are taken in every pass
+    if (i == 0) *a.n_runs = 0;
+    list[0][threadIdx.x] = live ? token_key(a.tok, i) << 13 | (uint32_t)i : kNone;
+    for (int p = 0; p < passes; ++p) {
+        for (int c = threadIdx.x; c < kSortWarps * 128; c += kSortThreads)
+            reinterpret_cast<uint32_t *>(&count[0][0])[c] = 0;
+        __syncthreads();
+        const uint32_t pair = list[p & 1][threadIdx.x], d = (pair >> (13 + 8 * p)) & 255u;
+        const uint32_t peers = same_digit(d, live);
+        if (live && (peers >> lane) == 1u) count[warp][d] = (unsigned short)__popc(peers);
+        __syncthreads();
+        prefix_warps(count, total);
+        __syncthreads();
+        // every block gets every block's counts
+        for (int c = threadIdx.x; c < 256 * blocks; c += kSortThreads)
+            store_peer(&hist[rank][c & 255], (uint32_t)c >> 8, total[c & 255]);
+        cluster_sync();
+        if (threadIdx.x < 256) {
+            uint32_t all = 0, mine = 0;
+            for (int q = 0; q < blocks; ++q) {
+                const uint32_t v = hist[q][threadIdx.x];
+                all += v;
+                mine += q < (int)rank ? v : 0u;
+            }
+            sum[threadIdx.x] = all;
+            before[threadIdx.x] = mine;
+        }
+        __syncthreads();
+        prefix_digits(sum);
+        __syncthreads();
+        if (live) {
+            const uint32_t at = sum[d] + before[d] + count[warp][d] +
+                                __popc(peers & ((1u << lane) - 1));
+            store_peer(&list[(p & 1) ^ 1][at & (kSortThreads - 1)], at / kSortThreads, pair);
+        }
+        cluster_sync();
+    }
+    if (live) {
+        const uint32_t pair = list[passes & 1][threadIdx.x];
+        a.key[0][i] = pair >> 13;
+        a.idx[0][i] = pair & 8191u;
+    }
+}
+
+// Counts of the first digit, a block at a time.  The later digits' counts and
+// the count of long runs are cleared here.
+__global__ void __launch_bounds__(kSortThreads)
+embed_count_kernel(const __grid_constant__ EmbedGradArgs a, int64_t chunk, int passes)
 {
     __shared__ uint32_t count[256];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t T = (int64_t)gridDim.x * kSortThreads;
     const int64_t t0 = (int64_t)blockIdx.x * kSortThreads + threadIdx.x;
-    if (pass == 0) {
-        if (t0 == 0) *a.n_runs = 0;
-        for (int64_t r = t0; r < a.tok.rows; r += T) a.used[r] = 0;
-    }
+    if (t0 == 0) *a.n_runs = 0;
+    for (int64_t i = t0; i < (int64_t)(passes - 1) * gridDim.x * 256; i += T)
+        a.hist[(int64_t)gridDim.x * 256 + i] = 0;
     if (threadIdx.x < 256) count[threadIdx.x] = 0;
     __syncthreads();
     const int64_t lo = (int64_t)blockIdx.x * chunk;
     const int64_t hi = lo + chunk < a.tok.n ? lo + chunk : a.tok.n;
-    const uint32_t *key = a.key[(pass & 1) ^ 1];
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
-        const uint32_t k = pass == 0 ? token_key(a.tok, i) : key[i];
-        atomicAdd(&count[(k >> (8 * pass)) & 255u], 1u);
-    }
+#pragma unroll 2
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads)
+        atomicAdd(&count[token_key(a.tok, i) & 255u], 1u);
     __syncthreads();
     if (threadIdx.x < 256) a.hist[blockIdx.x * 256 + threadIdx.x] = count[threadIdx.x];
 }
 
 // Pass `pass` reads side (pass & 1) ^ 1 (the tokens themselves at first) and
-// writes side pass & 1.
+// writes side pass & 1.  The blocks past sort_blocks zero rows.
+template <int GT, int E>
 __global__ void __launch_bounds__(kSortThreads)
-embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int64_t chunk)
+embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int passes, int64_t chunk,
+                   int sort_blocks)
 {
-    __shared__ uint32_t count[kSortWarps][256];
-    __shared__ uint32_t total[256], base[256], part[4][2][256];
+    __shared__ unsigned short count[kSortWarps][256];
+    __shared__ uint32_t total[256], base[256], local[256], part[4][2][256];
+    __shared__ uint32_t tile_key[kSortTile], tile_idx[kSortTile];
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((int)blockIdx.x >= sort_blocks) {
+        zero_rows<GT, E>(a, a.tok.rows * pass / passes, a.tok.rows * (pass + 1) / passes,
+                         (int64_t)(blockIdx.x - sort_blocks) * kSortWarps + warp,
+                         (int64_t)(gridDim.x - sort_blocks) * kSortWarps);
+        return;
+    }
+    const uint32_t *hist = a.hist + (int64_t)pass * sort_blocks * 256;
+    uint32_t *next = pass + 1 < passes ? a.hist + (int64_t)(pass + 1) * sort_blocks * 256 : nullptr;
     {   // tokens of each digit in all blocks, and in the blocks before this one
         const int d = threadIdx.x & 255, quarter = threadIdx.x >> 8;
         uint32_t all = 0, before = 0;
 #pragma unroll 8
-        for (unsigned b = quarter; b < gridDim.x; b += 4) {
-            const uint32_t v = a.hist[b * 256 + d];
+        for (int b = quarter; b < sort_blocks; b += 4) {
+            const uint32_t v = hist[b * 256 + d];
             all += v;
-            before += b < blockIdx.x ? v : 0u;
+            before += b < (int)blockIdx.x ? v : 0u;
         }
         part[quarter][0][d] = all;
         part[quarter][1][d] = before;
@@ -338,7 +419,8 @@ embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int64_t ch
     const int64_t hi = lo + chunk < a.tok.n ? lo + chunk : a.tok.n;
     constexpr int kIters = kSortTile / kSortThreads;
     for (int64_t tile = lo; tile < hi; tile += kSortTile) {
-        for (int i = threadIdx.x; i < kSortWarps * 256; i += kSortThreads) (&count[0][0])[i] = 0;
+        for (int i = threadIdx.x; i < kSortWarps * 128; i += kSortThreads)
+            reinterpret_cast<uint32_t *>(&count[0][0])[i] = 0;
         __syncthreads();
         uint32_t key[kIters], idx[kIters], rank[kIters];
 #pragma unroll
@@ -351,26 +433,49 @@ embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int64_t ch
 #pragma unroll
         for (int j = 0; j < kIters; ++j) {
             const bool live = tile + (warp * kIters + j) * 32 + lane < hi;
-            if (pass == 0 && live && key[j] < (uint32_t)a.tok.rows) a.used[key[j]] = 1;
             const uint32_t d = (key[j] >> (8 * pass)) & 255u;
             const uint32_t peers = same_digit(d, live);
             uint32_t before = 0;
             if (live) before = count[warp][d];
             __syncwarp();
             rank[j] = before + __popc(peers & ((1u << lane) - 1));
-            if (live && (peers >> lane) == 1u) count[warp][d] = before + __popc(peers);
+            if (live && (peers >> lane) == 1u)
+                count[warp][d] = (unsigned short)(before + __popc(peers));
             __syncwarp();
         }
         __syncthreads();
         prefix_warps(count, total);
         __syncthreads();
+        if (threadIdx.x < 256) local[threadIdx.x] = total[threadIdx.x];
+        __syncthreads();
+        prefix_digits(local);
+        __syncthreads();
+        // in order within the block first, so that neighbouring threads then write
+        // neighbouring places
 #pragma unroll
-        for (int j = 0; j < kIters; ++j) {
+        for (int j = 0; j < kIters; ++j)
             if (tile + (warp * kIters + j) * 32 + lane < hi) {
                 const uint32_t d = (key[j] >> (8 * pass)) & 255u;
-                const uint32_t at = base[d] + count[warp][d] + rank[j];
-                dkey[at] = key[j];
-                didx[at] = idx[j];
+                const uint32_t at = local[d] + count[warp][d] + rank[j];
+                tile_key[at] = key[j];
+                tile_idx[at] = idx[j];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kIters; ++j) {
+            const int i = j * kSortThreads + (int)threadIdx.x;
+            const bool live = tile + i < hi;
+            uint32_t cell = kNone;
+            if (live) {
+                const uint32_t k = tile_key[i], d = (k >> (8 * pass)) & 255u;
+                const uint32_t at = base[d] - local[d] + (uint32_t)i;
+                dkey[at] = k;
+                didx[at] = tile_idx[i];
+                cell = at / (uint32_t)chunk * 256 + ((k >> (8 * pass + 8)) & 255u);
+            }
+            if (next) {     // one addition for a warp's tokens of one cell: a frequent id has many
+                const uint32_t peers = __match_any_sync(0xffffffffu, cell);
+                if (live && (peers >> lane) == 1u) atomicAdd(&next[cell], (uint32_t)__popc(peers));
             }
         }
         __syncthreads();
@@ -382,17 +487,20 @@ embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int64_t ch
 //
 // The sorted list is cut into chunks of C positions.  A warp takes a chunk
 // and 256 columns, 8 a lane, and reads the chunk's rows of dy a few at a
-// time.  A run of one id that lies within the chunk is finished there; one
-// that passes an end of it leaves its fp32 part in the workspace (slot 0: the
-// run that the chunk begins in the middle of, slot 1: the run that passes
-// its end), and the chunk in which such a run begins enters it in a list
-// whose entries embed_runs_kernel finishes.
+// time.  A run of one id that lies within the chunk is finished there.  One that
+// passes an end of it leaves its fp32 part in the workspace (slot 0: the run
+// that the chunk begins in the middle of, slot 1: the run that passes its end),
+// and the chunk in which such a run begins enters it in a list whose entries
+// embed_runs_kernel finishes.  (Counting the parts, for whichever warp brings
+// the last one to add them up in the same launch, costs a fence a part: 207 us
+// against 103 for 131,071 tokens of 1600 columns.)
 constexpr int kCols = 256;
 
 int64_t sum_chunk(int64_t n)
 {
-    int64_t c = 8;
-    while (c < 256 && n > c * 4096) c *= 2;
+    if (n <= 2048) return 8;
+    int64_t c = 16;
+    while (c < 256 && n > c * 2048) c *= 2;
     return c;
 }
 
@@ -426,21 +534,14 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs &a, uint32_t row, in
 // element e of access j is column seg * 256 + j * 32 * E + lane * E + e.
 template <int YT, int GT, int E>
 __global__ void __launch_bounds__(kThreads)
-embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chunk, int segs,
-                 int64_t sum_blocks)
+embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chunk, int segs)
 {
     constexpr int J = 8 / E;
     constexpr int U = YT == F32 ? 4 : 8;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    if (blockIdx.x >= sum_blocks) {
-        zero_rows<GT, E>(a, a.used,
-                         ((int64_t)(blockIdx.x - sum_blocks) * kThreads + threadIdx.x) >> 5,
-                         ((int64_t)(gridDim.x - sum_blocks) * kThreads) >> 5);
-        return;
-    }
-    const int64_t task = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int64_t ck = task / segs;
     const int seg = (int)(task - ck * segs);
     const int64_t lo = ck * chunk;
@@ -448,13 +549,27 @@ embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chun
     const int64_t hi = lo + chunk < a.tok.n ? lo + chunk : a.tok.n;
     const uint32_t *key = a.key[side], *idx = a.idx[side];
     const uint32_t none = (uint32_t)a.tok.rows;
-    uint32_t cur = key[lo];
+    uint32_t mykey = none, myidx = 0;             // of position base + lane, base = lo at first
+    if (lo + lane < hi) {
+        mykey = key[lo + lane];
+        myidx = idx[lo + lane];
+    }
+    uint32_t edge = kNone;                        // the ids around the chunk's ends
+    if (lane == 0 && lo > 0) edge = key[lo - 1];
+    if (lane == 1 && hi < a.tok.n) edge = key[hi];
+    const uint32_t prev = __shfl_sync(0xffffffffu, edge, 0);
+    const uint32_t next = __shfl_sync(0xffffffffu, edge, 1);
+    uint32_t cur = __shfl_sync(0xffffffffu, mykey, 0);
     if (cur == none) return;                      // sorted: nothing but such ids follows
-    const uint32_t prev = lo > 0 ? key[lo - 1] : kNone;
-    const uint32_t next = hi < a.tok.n ? key[hi] : kNone;
     const int64_t c0 = (int64_t)seg * kCols + lane * E;
     float *part = a.part + ck * 2 * (int64_t)segs * kCols + (int64_t)seg * kCols + lane * 8;
     bool begun = prev != cur;                     // the current run began in this chunk
+    int64_t col[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int64_t c = c0 + (int64_t)j * 32 * E;
+        col[j] = c < a.dim ? c : a.dim - E;
+    }
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
@@ -472,21 +587,19 @@ embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chun
 
     for (int64_t base = lo; base < hi; base += 32) {
         const int m = (int)(hi - base < 32 ? hi - base : 32);
-        const uint32_t mykey = lane < m ? key[base + lane] : none;
-        const uint32_t myidx = lane < m ? idx[base + lane] : 0u;
+        if (base > lo) {
+            mykey = lane < m ? key[base + lane] : none;
+            myidx = lane < m ? idx[base + lane] : 0u;
+        }
         for (int u0 = 0; u0 < m; u0 += U) {
+            // every lane loads, whatever of it is used: position 0 and the row's
+            // last columns stand in for what is not there
             elems::Raw<YT, E> r[U][J];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint32_t k = __shfl_sync(0xffffffffu, mykey, (u0 + u) & 31);
-                const uint32_t i = __shfl_sync(0xffffffffu, myidx, (u0 + u) & 31);
-                const bool live = u0 + u < m && k != none;
+                const int64_t i = __shfl_sync(0xffffffffu, myidx, (u0 + u) & 31);
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int64_t c = c0 + (int64_t)j * 32 * E;
-                    r[u][j].zero();
-                    if (live && c < a.dim) r[u][j].load(a.dy, (int64_t)i * a.dy_stride + c);
-                }
+                for (int j = 0; j < J; ++j) r[u][j].load(a.dy, i * a.dy_stride + col[j]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -512,56 +625,108 @@ embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chun
     flush(next != cur);
 }
 
-// A block takes a listed run and 256 columns: its warps add up the parts
-// they come to in turn, and the eight sums join in the warps' order.
+// Adds the parts of chunks from, from + step, ... up to `last` to acc; chunk
+// `first` has its part in the second slot.
+__device__ __forceinline__ void add_parts(const float *p0, int64_t width, int64_t slot,
+                                          int64_t from, int64_t last, int64_t step,
+                                          int64_t first, float (&acc)[8])
+{
+#pragma unroll 4
+    for (int64_t c = from; c <= last; c += step) {
+        const float *p = p0 + c * width + (c == first ? slot : 0);
+        const float4 u = reinterpret_cast<const float4 *>(p)[0];
+        const float4 v = reinterpret_cast<const float4 *>(p)[1];
+        acc[0] = __fadd_rn(acc[0], u.x);
+        acc[1] = __fadd_rn(acc[1], u.y);
+        acc[2] = __fadd_rn(acc[2], u.z);
+        acc[3] = __fadd_rn(acc[3], u.w);
+        acc[4] = __fadd_rn(acc[4], v.x);
+        acc[5] = __fadd_rn(acc[5], v.y);
+        acc[6] = __fadd_rn(acc[6], v.z);
+        acc[7] = __fadd_rn(acc[7], v.w);
+    }
+}
+
+// A warp takes a listed run and 256 columns and adds up its chunks' parts in
+// their order.  Runs of more than kLongRun parts it leaves to its block, whose
+// warps then take every eighth part each; their eight sums join in the warps'
+// order.  Neighbouring tasks (a run's columns) go to different blocks, so that a
+// frequent id does not keep one block busy.
+constexpr int kLongRun = 24, kLongMost = 64;
+
 template <int YT, int GT, int E>
 __global__ void __launch_bounds__(kThreads)
 embed_runs_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chunk, int segs)
 {
     __shared__ float sums[8][kCols];
-    __shared__ int64_t last_sh;
+    __shared__ int64_t long_first[kLongMost], long_last[kLongMost];
+    __shared__ int long_seg[kLongMost], n_long;
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t tasks = (int64_t)*a.n_runs * segs;
     const uint32_t *key = a.key[side];
-    for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
+    const int64_t width = 2 * (int64_t)segs * kCols, slot = (int64_t)segs * kCols;
+    if (threadIdx.x == 0) n_long = 0;
+    __syncthreads();
+    for (int64_t t = blockIdx.x + (int64_t)gridDim.x * warp; t < tasks;
+         t += (int64_t)gridDim.x * 8) {
         const int64_t run = t / segs;
         const int seg = (int)(t - run * segs);
         const int64_t first = a.runs[run];
-        const uint32_t id = key[(first + 1) * chunk];
         // the last chunk whose first id is the run's: 32 chunks at a time
-        if (warp == 0) {
-            int64_t last = first + 1;
-            for (int64_t c = first + 1;; c += 32) {
-                const int64_t at = (c + lane) * chunk;
-                const uint32_t m = __ballot_sync(0xffffffffu, at < a.tok.n && key[at] == id);
-                last = c + (m == 0xffffffffu ? 31 : __ffs(~m) - 2);
-                if (m != 0xffffffffu) break;
-            }
-            if (lane == 0) last_sh = last;
+        uint32_t id = 0;
+        int64_t last = first;
+        for (int64_t c = first + 1;; c += 32) {
+            const int64_t at = (c + lane) * chunk;
+            const uint32_t k = at < a.tok.n ? key[at] : kNone;
+            if (c == first + 1) id = __shfl_sync(0xffffffffu, k, 0);
+            const uint32_t m = __ballot_sync(0xffffffffu, k == id);
+            last = c + (m == 0xffffffffu ? 31 : __ffs(~m) - 2);
+            if (m != 0xffffffffu) break;
         }
-        __syncthreads();
-        const int64_t last = last_sh;
-        const int64_t step = 2 * (int64_t)segs * kCols;
         const float *p0 = a.part + (int64_t)seg * kCols + lane * 8;
+        const bool is_long = last - first >= kLongRun;
+        if (is_long) {
+            int at = kLongMost;
+            if (lane == 0) at = atomicAdd(&n_long, 1);
+            at = __shfl_sync(0xffffffffu, at, 0);
+            if (at < kLongMost) {
+                if (lane == 0) {
+                    long_first[at] = first;
+                    long_last[at] = last;
+                    long_seg[at] = seg;
+                }
+                continue;
+            }
+        }
         float acc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-        for (int64_t c = first + warp; c <= last; c += 8) {
-            const float *p = p0 + c * step + (c == first ? (int64_t)segs * kCols : 0);
-            const float4 u = reinterpret_cast<const float4 *>(p)[0];
-            const float4 v = reinterpret_cast<const float4 *>(p)[1];
-            acc[0] = __fadd_rn(acc[0], u.x);
-            acc[1] = __fadd_rn(acc[1], u.y);
-            acc[2] = __fadd_rn(acc[2], u.z);
-            acc[3] = __fadd_rn(acc[3], u.w);
-            acc[4] = __fadd_rn(acc[4], v.x);
-            acc[5] = __fadd_rn(acc[5], v.y);
-            acc[6] = __fadd_rn(acc[6], v.z);
-            acc[7] = __fadd_rn(acc[7], v.w);
+        if (!is_long) {
+            add_parts(p0, width, slot, first, last, 1, first, acc);
+        } else {     // the block's list is full: the same sums, one after another
+            for (int w = 0; w < 8; ++w) {
+                float part[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part[e] = 0.0f;
+                add_parts(p0, width, slot, first + w, last, 8, first, part);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = w ? __fadd_rn(acc[e], part[e]) : part[e];
+            }
         }
+        put_row<YT, GT, E>(a, id, (int64_t)seg * kCols + lane * E, acc);
+    }
+    __syncthreads();
+    const int count = n_long < kLongMost ? n_long : kLongMost;
+    for (int i = 0; i < count; ++i) {
+        const int64_t first = long_first[i], last = long_last[i];
+        const int seg = long_seg[i];
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+        add_parts(a.part + (int64_t)seg * kCols + lane * 8, width, slot, first + warp, last, 8,
+                  first, acc);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sums[warp][lane * 8 + e] = acc[e];
         __syncthreads();
@@ -573,59 +738,77 @@ embed_runs_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chu
                 for (int w = 1; w < 8; ++w) s = __fadd_rn(s, sums[w][lane * 8 + e]);
                 acc[e] = s;
             }
-            put_row<YT, GT, E>(a, id, (int64_t)seg * kCols + lane * E, acc);
+            put_row<YT, GT, E>(a, key[(first + 1) * chunk], (int64_t)seg * kCols + lane * E, acc);
         }
         __syncthreads();
     }
+}
+
+template <int GT, int E>
+cudaError_t small_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
+{
+    const int64_t n = a.tok.n;
+    if (n == 0 && a.accumulate) return cudaSuccess;
+    if (n <= kRankTokens) {
+        const int blocks = (int)((n + 31) / 32), fill = a.accumulate ? 0 : 4 * sms;
+        return launch_dependent(embed_rank_kernel<GT, E>, dim3((unsigned)(blocks + fill)),
+                                dim3(kThreads), 0, s, a, blocks);
+    }
+    int blocks = 1;
+    while (blocks * kSortThreads < n) blocks *= 2;
+    const int fill = a.accumulate ? 0 : 2 * sms / blocks * blocks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks + fill));
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)blocks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, embed_cluster_kernel<GT, E>, a, sort_passes(a.tok.rows),
+                              blocks);
 }
 
 template <int YT, int GT, int E>
 cudaError_t grad_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
 {
     const int64_t n = a.tok.n;
-    const int passes = sort_passes(a.tok.rows);
-    const bool small = n <= kSmallTokens;
     int side = 0;
     cudaError_t e;
-    if (small) {
-        static int attr_device = -1;   // the attribute is per device
-        int dev = 0;
-        cudaGetDevice(&dev);
-        if (attr_device != dev) {
-            e = cudaFuncSetAttribute(embed_sort_small_kernel<GT, E>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)sizeof(SmallSort));
-            if (e != cudaSuccess) return e;
-            attr_device = dev;
-        }
-        const unsigned blocks = a.accumulate ? 1u : (unsigned)(sms > 1 ? sms : 2);
-        e = launch_dependent(embed_sort_small_kernel<GT, E>, dim3(blocks), dim3(kSortThreads),
-                             sizeof(SmallSort), s, a, passes);
-        if (e != cudaSuccess || n == 0) return e;
+    if (sort_small(a)) {
+        e = small_go<GT, E>(a, sms, s);
+        if (e != cudaSuccess) return e;
     } else {
+        const int passes = sort_passes(a.tok.rows);
         const int64_t chunk = sort_chunk(n);
-        const unsigned blocks = (unsigned)((n + chunk - 1) / chunk);
+        const int blocks = n ? (int)((n + chunk - 1) / chunk) : 1;
+        e = launch_dependent(embed_count_kernel, dim3((unsigned)blocks), dim3(kSortThreads), 0, s,
+                             a, chunk, passes);
+        if (e != cudaSuccess) return e;
+        const int fill = a.accumulate ? 0 : 2 * sms;
         for (int p = 0; p < passes; ++p) {
-            e = launch_dependent(embed_count_kernel, dim3(blocks), dim3(kSortThreads), 0, s, a, p,
-                                 chunk);
-            if (e != cudaSuccess) return e;
-            e = launch_dependent(embed_place_kernel, dim3(blocks), dim3(kSortThreads), 0, s, a, p,
-                                 chunk);
+            e = launch_dependent(embed_place_kernel<GT, E>, dim3((unsigned)(blocks + fill)),
+                                 dim3(kSortThreads), 0, s, a, p, passes, chunk, blocks);
             if (e != cudaSuccess) return e;
         }
         side = (passes - 1) & 1;
     }
+    if (n == 0) return cudaSuccess;
     const int64_t chunk = sum_chunk(n);
     const int segs = (int)((a.dim + kCols - 1) / kCols);
     const int64_t tasks = (n + chunk - 1) / chunk * segs;
-    const int64_t sum_blocks = (tasks * 32 + kThreads - 1) / kThreads;
-    const int64_t fill_blocks = !small && !a.accumulate ? (a.tok.rows + 63) / 64 : 0;
-    if (sum_blocks + fill_blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    e = launch_dependent(embed_sum_kernel<YT, GT, E>, dim3((unsigned)(sum_blocks + fill_blocks)),
-                         dim3(kThreads), 0, s, a, side, chunk, segs, sum_blocks);
+    const int threads = tasks <= 16 * (int64_t)sms ? 64 : kThreads;   // few tasks: spread them
+    const int64_t blocks = (tasks * 32 + threads - 1) / threads;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    e = launch_dependent(embed_sum_kernel<YT, GT, E>, dim3((unsigned)blocks),
+                         dim3((unsigned)threads), 0, s, a, side, chunk, segs);
     if (e != cudaSuccess) return e;
-    const int64_t most = (n + chunk - 1) / chunk * segs;
-    const int64_t grid = most < 4 * (int64_t)sms ? most : 4 * (int64_t)sms;
+    const int64_t most = (tasks + 7) / 8, grid = most < 8 * (int64_t)sms ? most : 8 * (int64_t)sms;
     return launch_dependent(embed_runs_kernel<YT, GT, E>, dim3((unsigned)grid), dim3(kThreads), 0,
                             s, a, side, chunk, segs);
 }
@@ -669,15 +852,13 @@ int64_t embed_grad_layout(EmbedGradArgs &a, char *base)
     const int64_t segs = (a.dim + kCols - 1) / kCols;
     a.n_runs = reinterpret_cast<uint32_t *>(take(4));
     a.runs = reinterpret_cast<uint32_t *>(take(4 * chunks));
+    const bool big = !sort_small(a);
     for (int i = 0; i < 2; ++i) {
-        // one block sorts a short list in shared memory: one side is enough
-        const int64_t len = i == 1 && n <= kSmallTokens ? 0 : n;
+        const int64_t len = i == 0 || big ? n : 0;
         a.key[i] = reinterpret_cast<uint32_t *>(take(4 * len));
         a.idx[i] = reinterpret_cast<uint32_t *>(take(4 * len));
     }
-    const bool big = n > kSmallTokens;
-    a.hist = reinterpret_cast<uint32_t *>(take(big ? 4 * 256 * kMaxSortBlocks : 0));
-    a.used = reinterpret_cast<unsigned char *>(take(big ? a.tok.rows : 0));
+    a.hist = reinterpret_cast<uint32_t *>(take(big ? 4ll * 4 * 256 * kMaxSortBlocks : 0));
     a.part = reinterpret_cast<float *>(take(chunks * 2 * segs * kCols * 4));
     return off > 0 ? off : 256;
 }

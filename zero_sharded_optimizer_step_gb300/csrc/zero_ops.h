@@ -50,8 +50,7 @@ struct EmbedGradArgs {
     int32_t accumulate;
     // workspace (embed_grad_layout)
     uint32_t *key[2], *idx[2];   // ids and positions, the sort's two sides
-    uint32_t *hist;              // [sort blocks][256]
-    unsigned char *used;         // per table row: some token names it
+    uint32_t *hist;              // [pass][sort blocks][256]
     uint32_t *n_runs;            // runs of one id that pass the end of a chunk
     uint32_t *runs;              // the chunk each begins in
     float *part;                 // [chunk][2][columns rounded up to 256]
