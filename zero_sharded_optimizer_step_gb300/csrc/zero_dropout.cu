@@ -51,7 +51,7 @@ __device__ __forceinline__ float drop(float x, uint32_t word, const DropoutArgs 
     return word >= a.threshold && a.any ? __fmul_rn(x, a.up) : 0.0f;
 }
 
-// VEC: kGroups groups of 8 elements a thread, on 16-byte boundaries, all loaded
+// VEC: kGroups groups of 8 elements a thread, on their boundaries, all loaded
 // before the words are made.  Otherwise (an unaligned buffer, and the ragged
 // end) 4 elements a thread, one by one.
 constexpr int kGroups = 2;
@@ -65,7 +65,7 @@ dropout_kernel(const __grid_constant__ DropoutArgs a)
     const int64_t groups = VEC ? a.n / 8 : 0;
     if (VEC) {
         const int64_t g0 = (int64_t)blockIdx.x * (kThreads * kGroups) + threadIdx.x;
-        elems::Raw<DT, 8> rx[kGroups], rr[kGroups];
+        elems::Raw<DT> rx[kGroups], rr[kGroups];
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
             const int64_t g = g0 + k * kThreads;
@@ -132,7 +132,8 @@ cudaError_t go(const DropoutArgs &a, cudaStream_t s)
 
 template <int DT> cudaError_t pick(const DropoutArgs &a, cudaStream_t s)
 {
-    const bool vec = (((uintptr_t)a.x | (uintptr_t)a.residual | (uintptr_t)a.out) & 15) == 0;
+    const bool vec = (((uintptr_t)a.x | (uintptr_t)a.residual | (uintptr_t)a.out) &
+                      (8 * elem_size(DT) - 1)) == 0;
     const bool low = a.first + (unsigned long long)a.n / 4 < 0xffffffffull;
     if (vec && low) return a.residual ? go<DT, true, true, true>(a, s) : go<DT, false, true, true>(a, s);
     if (vec) return a.residual ? go<DT, true, true, false>(a, s) : go<DT, false, true, false>(a, s);

@@ -25,11 +25,20 @@ __device__ __forceinline__ int64_t token_row(const TokenArgs &t, int64_t i)
 
 // ------------------------------------------------------------- the lookup
 //
-// A warp copies up to 4 accesses a lane of one output row, all in flight at
+// A warp copies up to 4 x 256 columns of one output row, all in flight at
 // once; a wide row takes several warps.
+constexpr int kCols = 256;          // columns a warp's lanes hold, 8 each
 constexpr int kEmbedFlight = 4;
 
-template <int DT, int E>
+template <int DT>
+__device__ __forceinline__ elems::Span span_of(const void *p, int64_t rows, int64_t stride,
+                                               int64_t cols)
+{
+    const char *lo = static_cast<const char *>(p);
+    return {lo, lo + ((rows - 1) * stride + cols) * elems::Raw<DT>::kSize};
+}
+
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 embed_kernel(const __grid_constant__ EmbedArgs a, int segs)
 {
@@ -46,50 +55,58 @@ embed_kernel(const __grid_constant__ EmbedArgs a, int segs)
                                       : (int64_t)static_cast<const int *>(a.tok.ids)[i];
         if (id != a.tok.pad) atomicAdd(a.bad, 1ull);
     }
-    const int64_t c0 = ((int64_t)seg * kEmbedFlight * 32 + lane) * E;
-    elems::Raw<DT, E> r[kEmbedFlight];
+    const int64_t c0 = (int64_t)seg * kEmbedFlight * kCols;
+    const elems::Span table = span_of<DT>(a.table, a.tok.rows, a.table_stride, a.dim);
+    const int64_t from = (row >= 0 ? row : 0) * a.table_stride;
+    constexpr int kSize = elems::Raw<DT>::kSize;
+    const bool inside = table.around((from + c0) * kSize, kEmbedFlight * kCols * kSize);
+    elems::Eight<DT, VEC> r[kEmbedFlight];
 #pragma unroll
     for (int j = 0; j < kEmbedFlight; ++j) {
-        const int64_t c = c0 + (int64_t)j * 32 * E;
-        r[j].zero();
-        if (row >= 0 && c < a.dim) r[j].load(a.table, row * a.table_stride + c);
+        const int64_t c = c0 + j * kCols + lane * 8;
+        if constexpr (VEC) {
+            r[j].r.zero();
+            if (row >= 0 && c < a.dim) r[j].r.load(a.table, from + c);
+        } else {
+            r[j].ask(a.table, from + c, table, inside);
+        }
     }
 #pragma unroll
     for (int j = 0; j < kEmbedFlight; ++j) {
-        const int64_t c = c0 + (int64_t)j * 32 * E;
-        if (c >= a.dim) continue;
-        if (row >= 0) {
-            float f[E];
-            r[j].get(f);
+        const int64_t first = c0 + j * kCols;
+        if (first >= a.dim) break;
+        float f[8];
+        elems::Raw<DT> w = r[j].take();
+        w.get(f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = __fmul_rn(f[e], a.scale);
-            r[j].set(f);
-        }
-        r[j].store(a.out, i * a.out_stride + c);
+        for (int e = 0; e < 8; ++e) f[e] = row >= 0 ? __fmul_rn(f[e], a.scale) : 0.0f;
+        w.set(f);
+        if (!VEC)
+            w.store_any(a.out, i * a.out_stride + first,
+                           a.dim - first < kCols ? (int)(a.dim - first) : kCols);
+        else if (first + lane * 8 < a.dim)
+            w.store(a.out, i * a.out_stride + first + lane * 8);
     }
 }
 
-template <int DT, int E> cudaError_t embed_go(const EmbedArgs &a, cudaStream_t s)
+template <int DT, bool VEC> cudaError_t embed_go(const EmbedArgs &a, cudaStream_t s)
 {
-    const int64_t per = (int64_t)32 * E * kEmbedFlight;
+    const int64_t per = kCols * kEmbedFlight;
     const int64_t segs = (a.dim + per - 1) / per;
     const int64_t warps = a.tok.n * segs;
     // few rows: one warp a block, so that they spread over the SMs
     const int threads = warps <= 1024 ? 32 : kThreads;
     const int64_t blocks = (warps * 32 + threads - 1) / threads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_dependent(embed_kernel<DT, E>, dim3((unsigned)blocks), dim3((unsigned)threads),
-                            0, s, a, (int)segs);
+    return launch_dependent(embed_kernel<DT, VEC>, dim3((unsigned)blocks),
+                            dim3((unsigned)threads), 0, s, a, (int)segs);
 }
 
 template <int DT> cudaError_t embed_pick(const EmbedArgs &a, cudaStream_t s)
 {
-    const int es = DT == F32 ? 4 : 2;
-    const int e0 = row_access(a.table, a.table_stride, es, a.dim);
-    const int e1 = row_access(a.out, a.out_stride, es, a.dim);
-    const int e = e0 < e1 ? e0 : e1;
-    return e == 8 ? embed_go<DT, 8>(a, s) : e == 2 ? embed_go<DT, 2>(a, s)
-                                                   : embed_go<DT, 1>(a, s);
+    const bool vec = rows_aligned(a.table, a.table_stride, DT, a.dim) &&
+                     rows_aligned(a.out, a.out_stride, DT, a.dim);
+    return vec ? embed_go<DT, true>(a, s) : embed_go<DT, false>(a, s);
 }
 
 // ----------------------------------------------------------------- the sort
@@ -197,21 +214,24 @@ __device__ __forceinline__ void prefix_digits(uint32_t *v)
 // zero all rows meanwhile; the sums then write those again that a token names.
 
 // Rows lo .. hi, a row each in turn: this is warp `warp` of `warps`.
-template <int GT, int E>
+template <int GT, bool VEC>
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs &a, int64_t lo, int64_t hi,
                                           int64_t warp, int64_t warps)
 {
-    elems::Raw<GT, E> z;
+    elems::Raw<GT> z;
     z.zero();
     for (int64_t r = lo + warp; r < hi; r += warps)
-        for (int64_t c = (int64_t)(threadIdx.x & 31) * E; c < a.dim; c += 32 * E)
-            z.store(a.grad, r * a.grad_stride + c);
+        for (int64_t c = 0; c < a.dim; c += kCols) {
+            const int64_t at = r * a.grad_stride + c;
+            if (!VEC) z.store_any(a.grad, at, a.dim - c < kCols ? (int)(a.dim - c) : kCols);
+            else if (c + (threadIdx.x & 31) * 8 < a.dim) z.store(a.grad, at + (threadIdx.x & 31) * 8);
+        }
 }
 
 // The first rank_blocks blocks place the tokens: 32 of them a block, one a
 // lane, each warp against an eighth of the list, which it reads from shared
 // memory four pairs at a time, the same for all lanes.
-template <int GT, int E>
+template <int GT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 embed_rank_kernel(const __grid_constant__ EmbedGradArgs a, int rank_blocks)
 {
@@ -221,7 +241,7 @@ embed_rank_kernel(const __grid_constant__ EmbedGradArgs a, int rank_blocks)
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((int)blockIdx.x >= rank_blocks) {
-        zero_rows<GT, E>(a, 0, a.tok.rows, (int64_t)(blockIdx.x - rank_blocks) * 8 + warp,
+        zero_rows<GT, VEC>(a, 0, a.tok.rows, (int64_t)(blockIdx.x - rank_blocks) * 8 + warp,
                          (int64_t)(gridDim.x - rank_blocks) * 8);
         return;
     }
@@ -283,7 +303,7 @@ __device__ __forceinline__ void store_peer(const void *p, uint32_t rank, uint32_
 
 // The first cluster sorts, the other blocks zero rows.  A pair is one
 // word (id << 13 | position), a thread has one in every pass.
-template <int GT, int E>
+template <int GT, bool VEC>
 __global__ void __launch_bounds__(kSortThreads)
 embed_cluster_kernel(const __grid_constant__ EmbedGradArgs a, int passes, int blocks)
 {
@@ -294,7 +314,7 @@ embed_cluster_kernel(const __grid_constant__ EmbedGradArgs a, int passes, int bl
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((int)blockIdx.x >= blocks) {
-        zero_rows<GT, E>(a, 0, a.tok.rows,
+        zero_rows<GT, VEC>(a, 0, a.tok.rows,
                          (int64_t)(blockIdx.x - blocks) * kSortWarps + warp,
                          (int64_t)(gridDim.x - blocks) * kSortWarps);
         return;
@@ -346,18 +366,26 @@ embed_cluster_kernel(const __grid_constant__ EmbedGradArgs a, int passes, int bl
 }
 
 // Counts of the first digit, a block at a time.  The later digits' counts and
-// the count of long runs are cleared here.
+// the count of long runs are cleared here; the blocks past sort_blocks zero rows.
+template <int GT, bool VEC>
 __global__ void __launch_bounds__(kSortThreads)
-embed_count_kernel(const __grid_constant__ EmbedGradArgs a, int64_t chunk, int passes)
+embed_count_kernel(const __grid_constant__ EmbedGradArgs a, int64_t chunk, int passes,
+                   int sort_blocks)
 {
     __shared__ uint32_t count[256];
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t T = (int64_t)gridDim.x * kSortThreads;
+    if ((int)blockIdx.x >= sort_blocks) {
+        zero_rows<GT, VEC>(a, 0, a.tok.rows / (passes + 1),
+                           (int64_t)(blockIdx.x - sort_blocks) * kSortWarps + (threadIdx.x >> 5),
+                           (int64_t)(gridDim.x - sort_blocks) * kSortWarps);
+        return;
+    }
+    const int64_t T = (int64_t)sort_blocks * kSortThreads;
     const int64_t t0 = (int64_t)blockIdx.x * kSortThreads + threadIdx.x;
     if (t0 == 0) *a.n_runs = 0;
-    for (int64_t i = t0; i < (int64_t)(passes - 1) * gridDim.x * 256; i += T)
-        a.hist[(int64_t)gridDim.x * 256 + i] = 0;
+    for (int64_t i = t0; i < (int64_t)(passes - 1) * sort_blocks * 256; i += T)
+        a.hist[(int64_t)sort_blocks * 256 + i] = 0;
     if (threadIdx.x < 256) count[threadIdx.x] = 0;
     __syncthreads();
     const int64_t lo = (int64_t)blockIdx.x * chunk;
@@ -371,7 +399,7 @@ embed_count_kernel(const __grid_constant__ EmbedGradArgs a, int64_t chunk, int p
 
 // Pass `pass` reads side (pass & 1) ^ 1 (the tokens themselves at first) and
 // writes side pass & 1.  The blocks past sort_blocks zero rows.
-template <int GT, int E>
+template <int GT, bool VEC>
 __global__ void __launch_bounds__(kSortThreads)
 embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int passes, int64_t chunk,
                    int sort_blocks)
@@ -383,7 +411,8 @@ embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int passes
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((int)blockIdx.x >= sort_blocks) {
-        zero_rows<GT, E>(a, a.tok.rows * pass / passes, a.tok.rows * (pass + 1) / passes,
+        zero_rows<GT, VEC>(a, a.tok.rows * (pass + 1) / (passes + 1),
+                         a.tok.rows * (pass + 2) / (passes + 1),
                          (int64_t)(blockIdx.x - sort_blocks) * kSortWarps + warp,
                          (int64_t)(gridDim.x - sort_blocks) * kSortWarps);
         return;
@@ -494,8 +523,6 @@ embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int passes
 // embed_runs_kernel finishes.  (Counting the parts, for whichever warp brings
 // the last one to add them up in the same launch, costs a fence a part: 207 us
 // against 103 for 131,071 tokens of 1600 columns.)
-constexpr int kCols = 256;
-
 int64_t sum_chunk(int64_t n)
 {
     if (n <= 2048) return 8;
@@ -504,40 +531,50 @@ int64_t sum_chunk(int64_t n)
     return c;
 }
 
-template <int YT, int GT, int E>
-__device__ __forceinline__ void put_row(const EmbedGradArgs &a, uint32_t row, int64_t c0,
-                                        const float (&acc)[8])
+// The 256 columns from c0 of a row of the gradient, as they are before.
+template <int GT, bool VEC>
+__device__ __forceinline__ void ask_row(const EmbedGradArgs &a, const elems::Span &grad,
+                                        uint32_t row, int64_t c0, elems::Eight<GT, VEC> &r)
 {
-    constexpr int J = 8 / E;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int64_t c = c0 + (int64_t)j * 32 * E;
-        if (c >= a.dim) continue;
-        const int64_t at = (int64_t)row * a.grad_stride + c;
-        float f[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = __fmul_rn(acc[j * E + e], a.scale);
-        elems::Raw<GT, E> r;
-        if (a.accumulate) {
-            float o[E];
-            r.load(a.grad, at);
-            r.get(o);
-#pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = __fadd_rn(o[e], f[e]);
-        }
-        r.set(f);
-        r.store(a.grad, at);
-    }
+    constexpr int kSize = elems::Raw<GT>::kSize;
+    const int64_t c = c0 + (threadIdx.x & 31) * 8, from = (int64_t)row * a.grad_stride;
+    r.ask(a.grad, from + (VEC && c >= a.dim ? a.dim - 8 : c), grad,
+          grad.around((from + c0) * kSize, kCols * kSize));
 }
 
-// Both accesses of dy and of the gradient take E elements; lane `lane`'s
-// element e of access j is column seg * 256 + j * 32 * E + lane * E + e.
-template <int YT, int GT, int E>
+// By the whole warp: the sums of 256 columns from c0 go to a row of the
+// gradient; ACC: are added to `old`.
+template <int GT, bool VEC, bool ACC>
+__device__ __forceinline__ void put_row(const EmbedGradArgs &a, uint32_t row, int64_t c0,
+                                        const float (&acc)[8], const elems::Raw<GT> &old)
+{
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(acc[e], a.scale);
+    if (ACC) {
+        float o[8];
+        old.get(o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __fadd_rn(o[e], f[e]);
+    }
+    elems::Raw<GT> r;
+    r.set(f);
+    const int64_t at = (int64_t)row * a.grad_stride + c0;
+    if (!VEC) r.store_any(a.grad, at, a.dim - c0 < kCols ? (int)(a.dim - c0) : kCols);
+    else if (c0 + (threadIdx.x & 31) * 8 < a.dim) r.store(a.grad, at + (threadIdx.x & 31) * 8);
+}
+
+__device__ __forceinline__ void put_part(float *p, const float (&acc)[8])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+}
+
+template <int YT, int GT, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kThreads)
 embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chunk, int segs)
 {
-    constexpr int J = 8 / E;
-    constexpr int U = YT == F32 ? 4 : 8;
+    constexpr int U = YT == F32 || ACC || !VEC ? 4 : 8;       // rows in flight
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -554,36 +591,26 @@ embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chun
         mykey = key[lo + lane];
         myidx = idx[lo + lane];
     }
-    uint32_t edge = kNone;                        // the ids around the chunk's ends
+    uint32_t edge = kNone;                        // the ids around the chunk
     if (lane == 0 && lo > 0) edge = key[lo - 1];
     if (lane == 1 && hi < a.tok.n) edge = key[hi];
     const uint32_t prev = __shfl_sync(0xffffffffu, edge, 0);
     const uint32_t next = __shfl_sync(0xffffffffu, edge, 1);
-    uint32_t cur = __shfl_sync(0xffffffffu, mykey, 0);
-    if (cur == none) return;                      // sorted: nothing but such ids follows
-    const int64_t c0 = (int64_t)seg * kCols + lane * E;
-    float *part = a.part + ck * 2 * (int64_t)segs * kCols + (int64_t)seg * kCols + lane * 8;
-    bool begun = prev != cur;                     // the current run began in this chunk
-    int64_t col[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int64_t c = c0 + (int64_t)j * 32 * E;
-        col[j] = c < a.dim ? c : a.dim - E;
-    }
+    const uint32_t first = __shfl_sync(0xffffffffu, mykey, 0);
+    if (first == none) return;                    // sorted: nothing but such ids follows
+    const elems::Span dy = span_of<YT>(a.dy, a.tok.n, a.dy_stride, a.dim);
+    const elems::Span grad = span_of<GT>(a.grad, a.tok.rows, a.grad_stride, a.dim);
+    constexpr int kSize = elems::Raw<YT>::kSize;
+    const int64_t c0 = (int64_t)seg * kCols;
+    // a lane past the row's end reads its last columns again (VEC), or what
+    // lies behind them in the matrix (ANY): neither is written
+    const int64_t col = c0 + lane * 8 < a.dim || !VEC ? c0 + lane * 8 : a.dim - 8;
+    float *part = a.part + ck * 2 * (int64_t)segs * kCols + c0 + lane * 8;
+    bool begun = prev != first;                   // the current run began in this chunk
+    bool open = false;                            // and has not ended
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-
-    auto flush = [&](bool ended) {
-        if (begun && ended) {
-            put_row<YT, GT, E>(a, cur, c0, acc);
-        } else {
-            float *p = part + (begun ? (int64_t)segs * kCols : 0);
-            reinterpret_cast<float4 *>(p)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            reinterpret_cast<float4 *>(p)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-            if (begun && seg == 0 && lane == 0) a.runs[atomicAdd(a.n_runs, 1u)] = (uint32_t)ck;
-        }
-    };
 
     for (int64_t base = lo; base < hi; base += 32) {
         const int m = (int)(hi - base < 32 ? hi - base : 32);
@@ -591,38 +618,55 @@ embed_sum_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chun
             mykey = lane < m ? key[base + lane] : none;
             myidx = lane < m ? idx[base + lane] : 0u;
         }
+        // which positions have a row, and which of them end their run
+        uint32_t after = __shfl_down_sync(0xffffffffu, mykey, 1);
+        if (lane == m - 1) after = base + m < hi ? key[base + m] : next;
+        const uint32_t live = __ballot_sync(0xffffffffu, lane < m && mykey != none);
+        const uint32_t ends = __ballot_sync(0xffffffffu, after != mykey) & live;
         for (int u0 = 0; u0 < m; u0 += U) {
-            // every lane loads, whatever of it is used: position 0 and the row's
-            // last columns stand in for what is not there
-            elems::Raw<YT, E> r[U][J];
+            // every lane loads, whatever of it is used: position 0 stands in for
+            // what is not there
+            elems::Eight<YT, VEC> r[U];
+            elems::Eight<GT, VEC> old[ACC ? U : 1];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t i = __shfl_sync(0xffffffffu, myidx, (u0 + u) & 31);
+                const int64_t i = __shfl_sync(0xffffffffu, myidx, u0 + u);
+                r[u].ask(a.dy, i * a.dy_stride + col, dy,
+                         dy.around((i * a.dy_stride + c0) * kSize, kCols * kSize));
+            }
+            if constexpr (ACC) {
 #pragma unroll
-                for (int j = 0; j < J; ++j) r[u][j].load(a.dy, i * a.dy_stride + col[j]);
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t k = __shfl_sync(0xffffffffu, mykey, u0 + u);
+                    if (ends >> (u0 + u) & 1) ask_row<GT, VEC>(a, grad, k, c0, old[u]);
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint32_t k = __shfl_sync(0xffffffffu, mykey, (u0 + u) & 31);
-                if (u0 + u >= m || k == none) continue;
-                if (k != cur) {
-                    flush(true);
-                    cur = k;
-                    begun = true;
+                if (!(live >> (u0 + u) & 1)) break;
+                float f[8];
+                r[u].take().get(f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+                for (int e = 0; e < 8; ++e) acc[e] = __fadd_rn(acc[e], f[e]);
+                open = true;
+                if (!(ends >> (u0 + u) & 1)) continue;
+                if (begun) {
+                    elems::Raw<GT> was;
+                    if (ACC) was = old[ACC ? u : 0].take();
+                    put_row<GT, VEC, ACC>(a, __shfl_sync(0xffffffffu, mykey, u0 + u), c0, acc, was);
+                } else {
+                    put_part(part, acc);
                 }
+                begun = true;
+                open = false;
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    float f[E];
-                    r[u][j].get(f);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[j * E + e] = __fadd_rn(acc[j * E + e], f[e]);
-                }
+                for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
             }
         }
     }
-    flush(next != cur);
+    if (!open) return;
+    put_part(part + (begun ? (int64_t)segs * kCols : 0), acc);
+    if (begun && seg == 0 && lane == 0) a.runs[atomicAdd(a.n_runs, 1u)] = (uint32_t)ck;
 }
 
 // Adds the parts of chunks from, from + step, ... up to `last` to acc; chunk
@@ -654,7 +698,7 @@ __device__ __forceinline__ void add_parts(const float *p0, int64_t width, int64_
 // frequent id does not keep one block busy.
 constexpr int kLongRun = 24, kLongMost = 64;
 
-template <int YT, int GT, int E>
+template <int GT, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kThreads)
 embed_runs_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chunk, int segs)
 {
@@ -667,6 +711,7 @@ embed_runs_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chu
     const int64_t tasks = (int64_t)*a.n_runs * segs;
     const uint32_t *key = a.key[side];
     const int64_t width = 2 * (int64_t)segs * kCols, slot = (int64_t)segs * kCols;
+    const elems::Span grad = span_of<GT>(a.grad, a.tok.rows, a.grad_stride, a.dim);
     if (threadIdx.x == 0) n_long = 0;
     __syncthreads();
     for (int64_t t = blockIdx.x + (int64_t)gridDim.x * warp; t < tasks;
@@ -700,6 +745,8 @@ embed_runs_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chu
                 continue;
             }
         }
+        elems::Eight<GT, VEC> old;
+        if (ACC) ask_row<GT, VEC>(a, grad, id, (int64_t)seg * kCols, old);
         float acc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
@@ -715,7 +762,9 @@ embed_runs_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chu
                 for (int e = 0; e < 8; ++e) acc[e] = w ? __fadd_rn(acc[e], part[e]) : part[e];
             }
         }
-        put_row<YT, GT, E>(a, id, (int64_t)seg * kCols + lane * E, acc);
+        elems::Raw<GT> was;
+        if (ACC) was = old.take();
+        put_row<GT, VEC, ACC>(a, id, (int64_t)seg * kCols, acc, was);
     }
     __syncthreads();
     const int count = n_long < kLongMost ? n_long : kLongMost;
@@ -738,20 +787,27 @@ embed_runs_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chu
                 for (int w = 1; w < 8; ++w) s = __fadd_rn(s, sums[w][lane * 8 + e]);
                 acc[e] = s;
             }
-            put_row<YT, GT, E>(a, key[(first + 1) * chunk], (int64_t)seg * kCols + lane * E, acc);
+            const uint32_t id = key[(first + 1) * chunk];
+            elems::Eight<GT, VEC> old;
+            elems::Raw<GT> was;
+            if (ACC) {
+                ask_row<GT, VEC>(a, grad, id, (int64_t)seg * kCols, old);
+                was = old.take();
+            }
+            put_row<GT, VEC, ACC>(a, id, (int64_t)seg * kCols, acc, was);
         }
         __syncthreads();
     }
 }
 
-template <int GT, int E>
+template <int GT, bool VEC>
 cudaError_t small_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
 {
     const int64_t n = a.tok.n;
     if (n == 0 && a.accumulate) return cudaSuccess;
     if (n <= kRankTokens) {
         const int blocks = (int)((n + 31) / 32), fill = a.accumulate ? 0 : 4 * sms;
-        return launch_dependent(embed_rank_kernel<GT, E>, dim3((unsigned)(blocks + fill)),
+        return launch_dependent(embed_rank_kernel<GT, VEC>, dim3((unsigned)(blocks + fill)),
                                 dim3(kThreads), 0, s, a, blocks);
     }
     int blocks = 1;
@@ -770,29 +826,29 @@ cudaError_t small_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, embed_cluster_kernel<GT, E>, a, sort_passes(a.tok.rows),
+    return cudaLaunchKernelEx(&cfg, embed_cluster_kernel<GT, VEC>, a, sort_passes(a.tok.rows),
                               blocks);
 }
 
-template <int YT, int GT, int E>
+template <int YT, int GT, bool VEC, bool ACC>
 cudaError_t grad_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
 {
     const int64_t n = a.tok.n;
     int side = 0;
     cudaError_t e;
     if (sort_small(a)) {
-        e = small_go<GT, E>(a, sms, s);
+        e = small_go<GT, VEC>(a, sms, s);
         if (e != cudaSuccess) return e;
     } else {
         const int passes = sort_passes(a.tok.rows);
         const int64_t chunk = sort_chunk(n);
         const int blocks = n ? (int)((n + chunk - 1) / chunk) : 1;
-        e = launch_dependent(embed_count_kernel, dim3((unsigned)blocks), dim3(kSortThreads), 0, s,
-                             a, chunk, passes);
+        const int fill = ACC ? 0 : 2 * sms;
+        e = launch_dependent(embed_count_kernel<GT, VEC>, dim3((unsigned)(blocks + fill)),
+                             dim3(kSortThreads), 0, s, a, chunk, passes, blocks);
         if (e != cudaSuccess) return e;
-        const int fill = a.accumulate ? 0 : 2 * sms;
         for (int p = 0; p < passes; ++p) {
-            e = launch_dependent(embed_place_kernel<GT, E>, dim3((unsigned)(blocks + fill)),
+            e = launch_dependent(embed_place_kernel<GT, VEC>, dim3((unsigned)(blocks + fill)),
                                  dim3(kSortThreads), 0, s, a, p, passes, chunk, blocks);
             if (e != cudaSuccess) return e;
         }
@@ -805,21 +861,21 @@ cudaError_t grad_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
     const int threads = tasks <= 16 * (int64_t)sms ? 64 : kThreads;   // few tasks: spread them
     const int64_t blocks = (tasks * 32 + threads - 1) / threads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    e = launch_dependent(embed_sum_kernel<YT, GT, E>, dim3((unsigned)blocks),
+    e = launch_dependent(embed_sum_kernel<YT, GT, VEC, ACC>, dim3((unsigned)blocks),
                          dim3((unsigned)threads), 0, s, a, side, chunk, segs);
     if (e != cudaSuccess) return e;
     const int64_t most = (tasks + 7) / 8, grid = most < 8 * (int64_t)sms ? most : 8 * (int64_t)sms;
-    return launch_dependent(embed_runs_kernel<YT, GT, E>, dim3((unsigned)grid), dim3(kThreads), 0,
+    return launch_dependent(embed_runs_kernel<GT, VEC, ACC>, dim3((unsigned)grid), dim3(kThreads), 0,
                             s, a, side, chunk, segs);
 }
 
 template <int YT, int GT> cudaError_t grad_pick(const EmbedGradArgs &a, int sms, cudaStream_t s)
 {
-    const int e0 = row_access(a.dy, a.dy_stride, YT == F32 ? 4 : 2, a.dim);
-    const int e1 = row_access(a.grad, a.grad_stride, GT == F32 ? 4 : 2, a.dim);
-    const int e = e0 < e1 ? e0 : e1;
-    return e == 8 ? grad_go<YT, GT, 8>(a, sms, s)
-                  : e == 2 ? grad_go<YT, GT, 2>(a, sms, s) : grad_go<YT, GT, 1>(a, sms, s);
+    const bool vec = rows_aligned(a.dy, a.dy_stride, YT, a.dim) &&
+                     rows_aligned(a.grad, a.grad_stride, GT, a.dim);
+    if (a.accumulate)
+        return vec ? grad_go<YT, GT, true, true>(a, sms, s) : grad_go<YT, GT, false, true>(a, sms, s);
+    return vec ? grad_go<YT, GT, true, false>(a, sms, s) : grad_go<YT, GT, false, false>(a, sms, s);
 }
 
 template <int YT>

@@ -65,28 +65,47 @@ __device__ __forceinline__ int64_t scale_at(int row, int block)
     return kMxCodes + (block >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4 + (block & 3);
 }
 
-// 8 consecutive elements from column c of a row, zeros past the row's end.
-template <int DT, int E>
-__device__ __forceinline__ void load8(const void *x, int64_t at, int64_t c, int64_t cols,
-                                      float (&f)[8])
+template <int DT> __device__ __forceinline__ elems::Span span_of(const MxQuantArgs &a)
 {
-    if constexpr (E == 8) {
-        elems::Raw<DT, 8> r;
-        r.zero();
-        if (c < cols) r.load(x, at + c);
-        r.get(f);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8 / E; ++j) {
-            elems::Raw<DT, E> r;
-            float g[E];
-            r.zero();
-            if (c + j * E < cols) r.load(x, at + c + j * E);
-            r.get(g);
-#pragma unroll
-            for (int e = 0; e < E; ++e) f[j * E + e] = g[e];
-        }
+    const char *lo = static_cast<const char *>(a.x);
+    return {lo, lo + ((a.rows - 1) * a.stride + a.cols) * elems::Raw<DT>::kSize};
+}
+
+// A lane's 8 of the 256 columns from c0 of a row: asked for, and later taken,
+// with zeros where the matrix has none.
+template <int DT, bool VEC>
+__device__ __forceinline__ void ask8(const MxQuantArgs &a, const elems::Span &m, int64_t row,
+                                     int64_t c0, elems::Eight<DT, VEC> &r)
+{
+    constexpr int kSize = elems::Raw<DT>::kSize;
+    const int64_t c = c0 + (threadIdx.x & 31) * 8;
+    if constexpr (VEC && DT != F32) {
+        r.r.zero();
+        if (row < a.rows && c < a.cols) r.r.load(a.x, row * a.stride + c);
+    } else {      // fp32: 34 us against 40 of a predicated load, for 8192 x 4096 both ways
+        const int64_t from = (row < a.rows ? row : 0) * a.stride;
+        r.ask(a.x, from + (VEC && c >= a.cols ? a.cols - 8 : c), m,
+              m.around((from + c0) * kSize, kMxCols * kSize));
     }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ elems::Raw<DT> take8(const MxQuantArgs &a, int64_t row, int64_t c0,
+                                                const elems::Eight<DT, VEC> &r)
+{
+    elems::Raw<DT> v = r.take();
+    if (VEC && DT != F32) return v;
+    const int64_t left = row < a.rows ? a.cols - c0 - (threadIdx.x & 31) * 8 : 0;
+    v.cut(left >= 8 ? 8 : left > 0 ? (int)left : 0);
+    return v;
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ elems::Raw<DT> load8(const MxQuantArgs &a, int64_t row, int64_t c0)
+{
+    elems::Eight<DT, VEC> r;
+    ask8<DT, VEC>(a, span_of<DT>(a), row, c0, r);
+    return take8<DT, VEC>(a, row, c0, r);
 }
 
 // ---- 16-bit types, two elements a word
@@ -132,26 +151,6 @@ __device__ __forceinline__ void scaled2(uint32_t w, float inv_lo, float inv_hi, 
     }
 }
 
-// 8 consecutive elements from column c of a row as words, zeros past its end.
-template <int E>
-__device__ __forceinline__ uint4 load_words(const void *x, int64_t at, int64_t c, int64_t cols)
-{
-    uint32_t w[4] = {0, 0, 0, 0};
-    const unsigned short *p = static_cast<const unsigned short *>(x) + at + c;
-    if constexpr (E == 8) {
-        if (c < cols) return *reinterpret_cast<const uint4 *>(p);
-    } else if constexpr (E == 2) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + 2 * j < cols) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < cols) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // A warp's row of 256 columns of a record, 8 elements a lane, a block over 4
 // lanes: the codes, and the scales (four blocks' are one word).
 template <int DT>
@@ -178,18 +177,17 @@ __device__ __forceinline__ void put_row16(unsigned char *rec, int r, uint4 v)
 }
 
 // Few rows: a warp a row.
-template <int DT, int E>
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 mx4_rows16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
     const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int64_t row = task / kt, t = task - row * kt;
     if (row >= a.rows) return;
     put_row16<DT>(a.q + ((row / kMxRows) * kt + t) * kMxRecord, (int)(row % kMxRows),
-                  load_words<E>(a.x, row * a.stride, t * kMxCols + lane * 8, a.cols));
+                  load8<DT, VEC>(a, row, t * kMxCols).v[0]);
 }
 
 // Either direction, or both from one read: a block takes 64 rows by 256
@@ -198,7 +196,7 @@ mx4_rows16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt)
 // of its transpose: neither needs another thread's elements for its scale.
 // Past the matrix's last row the transpose gets zeros, up to the end of its
 // record.
-template <int DT, int E>
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 mx4_both16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt)
 {
@@ -208,16 +206,14 @@ mx4_both16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t ct = blockIdx.x % kt, r0 = (blockIdx.x / kt) * 64, c0 = ct * kMxCols;
     {
-        uint4 v[8];
+        const elems::Span m = span_of<DT>(a);
+        elems::Eight<DT, VEC> v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t row = r0 + warp * 8 + j;
-            v[j] = row < a.rows ? load_words<E>(a.x, row * a.stride, c0 + lane * 8, a.cols)
-                                : make_uint4(0, 0, 0, 0);
-        }
+        for (int j = 0; j < 8; ++j) ask8<DT, VEC>(a, m, r0 + warp * 8 + j, c0, v[j]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4 *>(&strip[warp * 8 + j][lane * 4]) = v[j];
+            *reinterpret_cast<uint4 *>(&strip[warp * 8 + j][lane * 4]) =
+                take8<DT, VEC>(a, r0 + warp * 8 + j, c0, v[j]).v[0];
     }
     __syncthreads();
     if (a.q) {
@@ -295,7 +291,7 @@ mx4_both16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt
 
 // A warp quantises one row's 256 columns of a record: 8 elements a lane, a
 // block over 4 lanes.
-template <int DT, int E>
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 mx4_rows_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt)
 {
@@ -306,7 +302,7 @@ mx4_rows_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt)
     const int64_t row = task / kt, t = task - row * kt;
     if (row >= a.rows) return;
     float x[8];
-    load8<DT, E>(a.x, row * a.stride, t * kMxCols + lane * 8, a.cols, x);
+    load8<DT, VEC>(a, row, t * kMxCols).get(x);
     uint32_t top = top_of(x);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -327,12 +323,12 @@ mx4_rows_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt)
 // were read into; through shared memory every thread then takes one column,
 // whose 32 elements are a block of the transpose.  Past the matrix's last
 // row the transpose gets zeros, up to the end of its record.
-template <int DT, int E>
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 mx4_both_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt)
 {
-    using T = typename elems::El<DT>::T;
-    __shared__ __align__(16) T strip[32][kMxCols + 8];
+    static_assert(DT == F32, "16-bit types take mx4_both16_kernel");
+    __shared__ __align__(16) float strip[32][kMxCols + 8];
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -345,23 +341,23 @@ mx4_both_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt)
     const int tr = (int)(col % kMxRows);
     const int tb0 = (int)(r0 % kMxCols) / 32;     // first block of the record's columns
     uint32_t tscales = 0;
+    const elems::Span m = span_of<DT>(a);
     for (int s = 0; s < 4; ++s) {
         float x[4][8];
+        {
+            elems::Eight<DT, VEC> v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t row = r0 + s * 32 + warp * 4 + j;
-            if (row < a.rows) {
-                load8<DT, E>(a.x, row * a.stride, c0 + lane * 8, a.cols, x[j]);
-            } else {
+            for (int j = 0; j < 4; ++j)
+                ask8<DT, VEC>(a, m, r0 + s * 32 + warp * 4 + j, c0, v[j]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[j][e] = 0.0f;
-            }
+            for (int j = 0; j < 4; ++j)
+                take8<DT, VEC>(a, r0 + s * 32 + warp * 4 + j, c0, v[j]).get(x[j]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            elems::Raw<DT, 8> raw;
-            raw.set(x[j]);
-            raw.store(&strip[warp * 4 + j][0], lane * 8);
+            float4 *to = reinterpret_cast<float4 *>(&strip[warp * 4 + j][lane * 8]);
+            to[0] = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
+            to[1] = make_float4(x[j][4], x[j][5], x[j][6], x[j][7]);
             const int64_t row = r0 + s * 32 + warp * 4 + j;
             uint32_t top = top_of(x[j]);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -388,7 +384,7 @@ mx4_both_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt)
             for (int g = 0; g < 4; ++g) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    y[g][e] = elems::load1<DT>(&strip[g * 8 + e][0], threadIdx.x);
+                    y[g][e] = strip[g * 8 + e][threadIdx.x];
                 top = max(top, top_of(y[g]));
             }
             const uint32_t scale = block_scale(top);
@@ -406,7 +402,7 @@ mx4_both_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt)
     if (rect) *reinterpret_cast<uint32_t *>(rect + scale_at(tr, tb0)) = tscales;
 }
 
-template <int DT, int E> cudaError_t quant_go(const MxQuantArgs &a, int sms, cudaStream_t s)
+template <int DT, bool VEC> cudaError_t quant_go(const MxQuantArgs &a, int sms, cudaStream_t s)
 {
     const int64_t kt = (a.cols + kMxCols - 1) / kMxCols;
     const int64_t ktt = (a.rows + kMxCols - 1) / kMxCols;
@@ -418,25 +414,24 @@ template <int DT, int E> cudaError_t quant_go(const MxQuantArgs &a, int sms, cud
         if (blocks > limit) return cudaErrorInvalidValue;
         const dim3 grid((unsigned)blocks), block((unsigned)threads);
         if constexpr (DT == F32)
-            return launch_dependent(mx4_rows_kernel<DT, E>, grid, block, 0, s, a, kt);
+            return launch_dependent(mx4_rows_kernel<DT, VEC>, grid, block, 0, s, a, kt);
         else
-            return launch_dependent(mx4_rows16_kernel<DT, E>, grid, block, 0, s, a, kt);
+            return launch_dependent(mx4_rows16_kernel<DT, VEC>, grid, block, 0, s, a, kt);
     }
     const int64_t blocks = kt * ktt * (DT == F32 ? 2 : 4);
     if (blocks > limit) return cudaErrorInvalidValue;
     if constexpr (DT == F32)
-        return launch_dependent(mx4_both_kernel<DT, E>, dim3((unsigned)blocks), dim3(kThreads), 0,
+        return launch_dependent(mx4_both_kernel<DT, VEC>, dim3((unsigned)blocks), dim3(kThreads), 0,
                                 s, a, kt, ktt);
     else
-        return launch_dependent(mx4_both16_kernel<DT, E>, dim3((unsigned)blocks), dim3(kThreads),
+        return launch_dependent(mx4_both16_kernel<DT, VEC>, dim3((unsigned)blocks), dim3(kThreads),
                                 0, s, a, kt, ktt);
 }
 
 template <int DT> cudaError_t quant_pick(const MxQuantArgs &a, int sms, cudaStream_t s)
 {
-    const int e = row_access(a.x, a.stride, DT == F32 ? 4 : 2, a.cols);
-    return e == 8 ? quant_go<DT, 8>(a, sms, s)
-                  : e == 2 ? quant_go<DT, 2>(a, sms, s) : quant_go<DT, 1>(a, sms, s);
+    return rows_aligned(a.x, a.stride, DT, a.cols) ? quant_go<DT, true>(a, sms, s)
+                                                   : quant_go<DT, false>(a, sms, s);
 }
 
 // ---------------------------------------------------------------- to values
@@ -462,7 +457,7 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t scale, float (&f)[8
 
 // A warp takes R rows' 256 columns of a record, all read before any is
 // written; 8 elements of a row a lane.  R divides 128.
-template <int DT, int E, int R>
+template <int DT, bool VEC, int R>
 __global__ void __launch_bounds__(kThreads)
 mx4_values_kernel(const __grid_constant__ MxDequantArgs a, int64_t kt)
 {
@@ -471,8 +466,8 @@ mx4_values_kernel(const __grid_constant__ MxDequantArgs a, int64_t kt)
     const int lane = threadIdx.x & 31;
     const int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int64_t row0 = task / kt * R, t = task % kt;
-    const int64_t c = t * kMxCols + lane * 8;
-    if (row0 >= a.rows || c >= a.cols) return;
+    const int64_t c = t * kMxCols;
+    if (row0 >= a.rows) return;
     const unsigned char *rec = a.q + ((row0 / kMxRows) * kt + t) * kMxRecord;
     const int r0 = (int)(row0 % kMxRows);
     uint32_t w[R], scale[R];
@@ -491,20 +486,14 @@ mx4_values_kernel(const __grid_constant__ MxDequantArgs a, int64_t kt)
         float f[8];
         values8(w[j], scale[j], f);
         const int64_t at = (row0 + j) * a.stride + c;
-#pragma unroll
-        for (int i = 0; i < 8 / E; ++i) {
-            if (c + i * E >= a.cols) break;
-            elems::Raw<DT, E> o;
-            float g[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) g[e] = f[i * E + e];
-            o.set(g);
-            o.store(a.out, at + i * E);
-        }
+        elems::Raw<DT> o;
+        o.set(f);
+        if (!VEC) o.store_any(a.out, at, a.cols - c < kMxCols ? (int)(a.cols - c) : kMxCols);
+        else if (c + lane * 8 < a.cols) o.store(a.out, at + lane * 8);
     }
 }
 
-template <int DT, int E> cudaError_t dequant_go(const MxDequantArgs &a, int sms, cudaStream_t s)
+template <int DT, bool VEC> cudaError_t dequant_go(const MxDequantArgs &a, int sms, cudaStream_t s)
 {
     const int64_t kt = (a.cols + kMxCols - 1) / kMxCols;
     // an fp32 row is long enough to keep its warp busy: 27 us against 34 of four
@@ -515,15 +504,14 @@ template <int DT, int E> cudaError_t dequant_go(const MxDequantArgs &a, int sms,
     const int64_t blocks = (warps * 32 + threads - 1) / threads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks), block((unsigned)threads);
-    return many ? launch_dependent(mx4_values_kernel<DT, E, 4>, grid, block, 0, s, a, kt)
-                : launch_dependent(mx4_values_kernel<DT, E, 1>, grid, block, 0, s, a, kt);
+    return many ? launch_dependent(mx4_values_kernel<DT, VEC, 4>, grid, block, 0, s, a, kt)
+                : launch_dependent(mx4_values_kernel<DT, VEC, 1>, grid, block, 0, s, a, kt);
 }
 
 template <int DT> cudaError_t dequant_pick(const MxDequantArgs &a, int sms, cudaStream_t s)
 {
-    const int e = row_access(a.out, a.stride, DT == F32 ? 4 : 2, a.cols);
-    return e == 8 ? dequant_go<DT, 8>(a, sms, s)
-                  : e == 2 ? dequant_go<DT, 2>(a, sms, s) : dequant_go<DT, 1>(a, sms, s);
+    return rows_aligned(a.out, a.stride, DT, a.cols) ? dequant_go<DT, true>(a, sms, s)
+                                                     : dequant_go<DT, false>(a, sms, s);
 }
 
 }  // namespace

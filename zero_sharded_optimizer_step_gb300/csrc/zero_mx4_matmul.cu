@@ -582,7 +582,7 @@ __device__ __forceinline__ void put_row32(const MxMatmulArgs &a, int64_t i, int6
             float o[8];
 #pragma unroll
             for (int u = 0; u < kPer / 8; ++u) {
-                elems::Raw<DT, 8> old;
+                elems::Raw<DT> old;
                 old.load(a.out, at + h * kPer + u * 8);
                 old.get(o);
 #pragma unroll

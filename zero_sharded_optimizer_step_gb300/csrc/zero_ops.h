@@ -8,17 +8,12 @@
 
 namespace zgb {
 
-// Elements per memory access of a row-wise kernel: 8, 2 or 1, the widest that
-// every base address and row stride of the call allows (E elements on an
-// E * elem_size boundary, at most 16 bytes of it).
-inline int row_access(const void *p, int64_t stride, int es, int64_t width)
+// Whether all rows of a matrix begin on a boundary of 8 elements and hold whole
+// eights (zero_elems.cuh: VEC).
+inline bool rows_aligned(const void *p, int64_t stride, int32_t dt, int64_t width)
 {
-    for (int e : {8, 2}) {
-        const int64_t b = (int64_t)e * es < 16 ? (int64_t)e * es : 16;
-        if (((uintptr_t)p % (uintptr_t)b) == 0 && (stride * es) % b == 0 && width % e == 0)
-            return e;
-    }
-    return 1;
+    const int b = 8 * elem_size(dt);
+    return ((uintptr_t)p % (uintptr_t)b) == 0 && stride % 8 == 0 && width % 8 == 0;
 }
 
 // ---- embedding
