@@ -106,7 +106,10 @@ int report(int code, const char *fmt, ...)
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
+    try {
+        g_last_error = buf;
+    } catch (...) {       // no memory for the message: the code alone
+    }
     return code;
 }
 

@@ -450,26 +450,27 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
 // copies arrive at its barriers: a record is a tensor of 136 rows of 128 bytes
 // to the copy engine, because only tensor copies may signal the other block.
 //
-// The scales have a warp of their own, which copies them a stage ahead into
-// one of two sets of columns.  A thread that issues both the copies and the
+// The scales have a warp of their own, which copies them up to three stages
+// ahead into one of four sets of columns.  A thread that issues both the copies and the
 // products stands at its next barrier until the copies are done, and
 // the tensor cores run dry: 177 clocks a product of 256 x 256 x 64, against
 // 134 with two warps and 128 for the products alone.
 //
 // The blocks are persistent.  The accumulators of consecutive tiles lie at
-// columns 0 and 192 of the tensor memory (of 512, 48 hold the scales): they
-// overlap in 64 columns, which the result warps read first, so that the next
+// columns 0 and 160 of the tensor memory (of 512, 96 hold the scales): they
+// overlap in 96 columns, which the result warps read first, so that the next
 // tile's products start as soon as those are out and run while the other
-// 192 are read, converted and stored.
+// 160 are read, converted and stored.
 constexpr int kPairStages = 6;
 constexpr int kPairStage = kMxRecord + kMxCodes + 2 * kMxScales;
 constexpr int kPairSmem = kPairStages * kPairStage + 1024;
 constexpr int kPairThreads = 224;
-constexpr int kOverlap = 64;
+constexpr int kOverlap = 96;
+constexpr int kSets = 4;                                 // of scales in tensor memory
 constexpr uint32_t kPairAcc = 256 - kOverlap;            // the upper accumulator
-constexpr uint32_t kPairScales = 2 * 256 - kOverlap;     // two sets: 8 columns for B, 16 for A
+constexpr uint32_t kPairScales = 2 * 256 - kOverlap;     // a set: 8 columns for B, 16 for A
 static_assert(kPairSmem <= kSmemBlock, "one block's shared memory");
-static_assert(kPairScales + 48 <= 512, "the tensor memory's columns");
+static_assert(kPairScales + kSets * 24 <= 512, "the tensor memory's columns");
 
 constexpr int kMxLines = kMxRecord / 128;               // 128-byte lines of a record
 
@@ -613,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ MxPair g)
 {
     extern __shared__ unsigned char dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 5];
+    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 3 + kSets];
     __shared__ uint32_t tmem_base, failed;
     const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -623,11 +624,11 @@ mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ 
     auto empty = [&](int s) { return saddr(&bars[kPairStages + s]); };
     auto done = [&](int b) { return saddr(&bars[2 * kPairStages + b]); };
     auto scaled = [&](int b) { return saddr(&bars[2 * kPairStages + 2 + b]); };  // the first block's
-    const uint32_t drained = saddr(&bars[2 * kPairStages + 4]);             // the first block's
+    const uint32_t drained = saddr(&bars[2 * kPairStages + 2 + kSets]);             // the first block's
 
     if (warp == 4) {
         if (lane == 0) {
-            for (int s = 0; s < 2 * kPairStages + 4; ++s) bar_init(saddr(&bars[s]), 1);
+            for (int s = 0; s < 2 * kPairStages + 2 + kSets; ++s) bar_init(saddr(&bars[s]), 1);
             bar_init(drained, 8);
             failed = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -681,16 +682,16 @@ mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ 
         const bool one = elect_one();
         const uint32_t sets = tmem + kPairScales;
         const int64_t total = pair_stages(g, blockIdx.x / 2, step);
-        int s = 0, last = 0;                                 // the stage, and that of two before
+        int s = 0, last = 0;                                 // the stage, and that of kSets before
         uint32_t phase = 0, last_phase = 0;
         for (int64_t it = 0; it < total; ++it) {
-            // the products two stages before have read this set of columns
-            ok = it < 2 ? bar_wait(full(s), phase)
+            // the products kSets stages before have read this set of columns
+            ok = it < kSets ? bar_wait(full(s), phase)
                         : bar_wait_both(full(s), phase, empty(last), last_phase);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if (one) {
-                const uint32_t sb = sets + (uint32_t)(it & 1) * 24, sa = sb + 8;
+                const uint32_t sb = sets + (uint32_t)(it % kSets) * 24, sa = sb + 8;
                 const uint64_t db = scale_desc(ring + s * kPairStage + kMxCodes);
                 const uint64_t da = db + ((kMxScales + kMxCodes) >> 4);
 #pragma unroll
@@ -699,11 +700,11 @@ mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ 
                     copy_scales2(sa + 8 * h, da + h * (512 >> 4));
                     copy_scales2(sa + 8 * h + 4, da + ((kMxScales + h * 512) >> 4));
                 }
-                commit2_first(scaled((int)(it & 1)));
+                commit2_first(scaled((int)(it % kSets)));
             }
             __syncwarp();
             if (++s == kPairStages) s = 0, phase ^= 1;
-            if (it >= 2 && ++last == kPairStages) last = 0, last_phase ^= 1;
+            if (it >= kSets && ++last == kPairStages) last = 0, last_phase ^= 1;
         }
     } else if (warp == 5 && rank == 0) {                     // the products
         const bool one = elect_one();
@@ -712,7 +713,7 @@ mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ 
         const uint32_t sets = tmem + kPairScales;
         int s = 0;
         uint32_t phase = 0, scaled_phase = 0;
-        uint32_t i = 0, it = 0;                              // parities of the tile and the stage
+        uint32_t i = 0, it = 0;                              // the tile's parity, the set
         // the record's columns past k are zeros: their products are left out
         const int last_steps = (int)((a.k - (g.kt - 1) * kMxCols + 63) / 64);
         for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
@@ -743,8 +744,7 @@ mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ 
                 }
                 __syncwarp();
                 if (++s == kPairStages) s = 0, phase ^= 1;
-                it ^= 1;
-                if (it == 0) scaled_phase ^= 1;
+                if (++it == kSets) it = 0, scaled_phase ^= 1;
             }
             i ^= 1;
         }
@@ -841,22 +841,16 @@ bool pair_lines(const MxMatmulArgs &a, int64_t &la, int64_t &lb)
 
 template <int DT, bool WIDE> cudaError_t pair_go(const MxMatmulArgs &a, int sms, cudaStream_t s)
 {
-    static int attr_device = -1;   // the attribute is per device
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (attr_device != dev) {
-        cudaError_t r = cudaFuncSetAttribute(mx4_pair_kernel<DT, WIDE>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmemBlock);
-        if (r != cudaSuccess) return r;
-        attr_device = dev;
-    }
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(mx4_pair_kernel<DT, WIDE>),
+                                 kSmemBlock, done);
+    if (e != cudaSuccess) return e;
     MxPair g;
     int64_t lines_a = 0, lines_b = 0;
     pair_lines(a, lines_a, lines_b);
     const void *lanes = WIDE ? a.a : a.b, *cols = WIDE ? a.b : a.a;
     const int64_t lines_l = WIDE ? lines_a : lines_b, lines_c = WIDE ? lines_b : lines_a;
-    cudaError_t e = record_map(&g.lanes, lanes, lines_l, kMxLines);
+    e = record_map(&g.lanes, lanes, lines_l, kMxLines);
     if (e == cudaSuccess) e = record_map(&g.codes, cols, lines_c, kMxCodes / 128);
     if (e == cudaSuccess) e = record_map(&g.scales, cols, lines_c, kMxScales / 128);
     if (e != cudaSuccess) return e;
@@ -876,16 +870,10 @@ template <int DT, int NT>
 cudaError_t mm_go(const MxMatmulArgs &a, int sms, cudaStream_t s)
 {
     using Tl = Tile<NT>;
-    static int attr_device = -1;   // the attribute is per device
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (attr_device != dev) {
-        cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<DT, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Tl::smem(Tl::kStages));
-        if (e != cudaSuccess) return e;
-        attr_device = dev;
-    }
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(mx4_matmul_kernel<DT, NT>),
+                                 Tl::smem(Tl::kStages), done);
+    if (e != cudaSuccess) return e;
     MxSplit sp;
     sp.kt = (a.k + kMxCols - 1) / kMxCols;
     sp.tiles_n = (a.n + kMxRows - 1) / kMxRows;

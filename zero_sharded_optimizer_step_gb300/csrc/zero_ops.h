@@ -4,9 +4,25 @@
 // zero_internal.h; every launcher returns a cudaError_t and launches on `s`.
 #pragma once
 
+#include <atomic>
+
 #include "zero_internal.h"
 
 namespace zgb {
+
+// Lets `kernel` use so much dynamic shared memory, once a device: `done` has a
+// bit for each (of the first 64).
+inline cudaError_t allow_shared(const void *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Whether all rows of a matrix begin on a boundary of 8 elements and hold whole
 // eights (zero_elems.cuh: VEC).
