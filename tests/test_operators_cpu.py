@@ -123,3 +123,13 @@ def test_quantize_restatement_pins():
     assert scale.tolist() == [[0]] and R.values(codes, scale).tolist() == [[0, 0, 0]]
     x[0, 3] = np.inf
     assert R.quantize(x)[1].tolist() == [[255]]
+
+
+def test_layers_refuse_what_is_not_on_a_gpu(z):
+    import torch
+    t, tok = torch.zeros(4, 8), torch.zeros(3, dtype=torch.int64)
+    for bad in (lambda: z.embed(t, tok), lambda: z.embed_grad(t, tok, t),
+                lambda: z.dropout(t, 0.5, 1, 2), lambda: z.mx4_quantize(t),
+                lambda: z.Mx4Linear(t)):
+        with pytest.raises(ValueError):
+            bad()

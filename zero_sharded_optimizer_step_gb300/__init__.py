@@ -18,7 +18,7 @@ def dtype_code(torch_dtype) -> int:
 
 
 def __getattr__(name):
-    # the ZeroAdam facade imports torch; load it on first use
+    # ZeroAdam and the layers import torch; load them on first use
     if name == "ZeroAdam":
         from .optim import ZeroAdam
         return ZeroAdam
@@ -28,4 +28,8 @@ def __getattr__(name):
     if name in ("consolidate_state", "shard_state"):
         from . import optim
         return getattr(optim, name)
+    if name in ("embed", "embed_grad", "dropout", "Mx4Matrix", "mx4_quantize", "mx4_matmul",
+                "Mx4Linear"):
+        from . import layers
+        return getattr(layers, name)
     raise AttributeError(name)
