@@ -48,7 +48,7 @@ __device__ __forceinline__ void philox(const unsigned long long (&c)[N], const D
 
 __device__ __forceinline__ float drop(float x, uint32_t word, const DropoutArgs &a)
 {
-    return word >= a.threshold && a.any ? __fmul_rn(x, a.up) : 0.0f;
+    return word >= a.threshold ? __fmul_rn(x, a.up) : 0.0f;
 }
 
 // VEC: kGroups groups of 8 elements a thread, on their boundaries, all loaded
@@ -117,6 +117,19 @@ dropout_kernel(const __grid_constant__ DropoutArgs a)
     }
 }
 
+// p = 1: nothing is kept (2^32 is no 32-bit threshold), and x is not read.
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+dropout_all_kernel(const __grid_constant__ DropoutArgs a)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t T = (int64_t)gridDim.x * kThreads;
+    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < a.n; e += T)
+        elems::store1<DT>(a.out, e, a.residual ? __fadd_rn(0.0f, elems::load1<DT>(a.residual, e))
+                                               : 0.0f);
+}
+
 template <int DT, bool RES, bool VEC, bool LOW>
 cudaError_t go(const DropoutArgs &a, cudaStream_t s)
 {
@@ -132,6 +145,12 @@ cudaError_t go(const DropoutArgs &a, cudaStream_t s)
 
 template <int DT> cudaError_t pick(const DropoutArgs &a, cudaStream_t s)
 {
+    if (a.all) {
+        const int64_t blocks = (a.n + kThreads - 1) / kThreads;
+        return launch_dependent(dropout_all_kernel<DT>,
+                                dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)),
+                                dim3(kThreads), 0, s, a);
+    }
     const bool vec = (((uintptr_t)a.x | (uintptr_t)a.residual | (uintptr_t)a.out) &
                       (8 * elem_size(DT) - 1)) == 0;
     const bool low = a.first + (unsigned long long)a.n / 4 < 0xffffffffull;

@@ -78,8 +78,8 @@ struct DropoutArgs {
     const void *x, *residual;
     void *out;
     int64_t n;
-    uint32_t threshold;             // keep where the word >= threshold,
-    int32_t any;                    // unless p = 1: 2^32 is no 32-bit threshold
+    uint32_t threshold;             // keep where the word >= threshold
+    int32_t all;                    // p = 1: drop everything
     float up;                       // 1 / (1 - p)
     uint32_t key0[10], key1[10];    // the rounds' keys
     uint32_t off0, off1;

@@ -174,8 +174,8 @@ int zero_dropout(const void *x, const void *residual, void *out, int32_t dtype, 
     a.out = out;
     a.n = n;
     const double words = std::floor(p * 4294967296.0);
-    a.any = words < 4294967296.0;
-    a.threshold = a.any ? (uint32_t)words : 0;
+    a.all = words >= 4294967296.0;
+    a.threshold = a.all ? 0 : (uint32_t)words;
     a.up = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.0f;
     for (uint32_t r = 0; r < 10; ++r) {
         a.key0[r] = (uint32_t)seed + r * 0x9E3779B9u;
