@@ -125,7 +125,9 @@ template <int DT> cudaError_t embed_pick(const EmbedArgs &a, cudaStream_t s)
 //                         adds up the digit counts of the blocks before it,
 //                         places its tokens, and counts the next digit
 //                         where they land
+// Up to kFewTokens tokens are not sorted at all (embed_few_kernel).
 constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kFewTokens = 512;
 constexpr int kRankTokens = 2048;
 constexpr int kSmallTokens = 8192;
 constexpr int64_t kSmallRows = 1 << 19;      // id and position in one word
@@ -210,14 +212,44 @@ __device__ __forceinline__ void prefix_digits(uint32_t *v)
 }
 
 // A gradient that is not added to has zeros in the rows that no token names.
-// The sort is bound by latency, so its launches have blocks of their own that
-// zero all rows meanwhile; the sums then write those again that a token names.
+// All rows are zeroed while the tokens are sorted, which is bound by latency, and the
+// sums write those again that a token names.  A short list's kernel goes on
+// beside embed_zero_kernel: it starts once every block of that one runs, which
+// is after whatever came before has ended, and waits for its end only before
+// it writes to the gradient, or ends itself.  A long list's launches have
+// blocks of their own for it.
 
-// Rows lo .. hi, a row each in turn: this is warp `warp` of `warps`.
+// Bytes first .. last of p, 2 KB a warp in turn: this is warp `warp` of `warps`.
+__device__ __forceinline__ void zero_bytes(char *p, int64_t first, int64_t last, int64_t warp,
+                                           int64_t warps)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t rest = (16 - (int64_t)((uintptr_t)(p + first) & 15)) & 15;
+    const int64_t head = first + rest < last ? first + rest : last;
+    const int64_t whole = (last - head) / 16, tail = head + whole * 16;
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    uint4 *v = reinterpret_cast<uint4 *>(p + head);
+    for (int64_t i = warp * 128 + lane; i < whole; i += warps * 128) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u * 32 < whole) v[i + u * 32] = z;
+    }
+    if (warp != 0) return;
+    if (lane < head - first) p[first + lane] = 0;
+    if (lane < last - tail) p[tail + lane] = 0;
+}
+
+// Rows lo .. hi: this is warp `warp` of `warps`.
 template <int GT, bool VEC>
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs &a, int64_t lo, int64_t hi,
                                           int64_t warp, int64_t warps)
 {
+    constexpr int kSize = elems::Raw<GT>::kSize;
+    if (a.grad_stride == a.dim && !VEC) {   // one piece, whatever boundary the rows are on
+        zero_bytes(static_cast<char *>(a.grad), lo * a.dim * kSize, hi * a.dim * kSize,
+                   warp, warps);
+        return;
+    }
     elems::Raw<GT> z;
     z.zero();
     for (int64_t r = lo + warp; r < hi; r += warps)
@@ -228,35 +260,40 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs &a, int64_t lo, in
         }
 }
 
-// The first rank_blocks blocks place the tokens: 32 of them a block, one a
-// lane, each warp against an eighth of the list, which it reads from shared
-// memory four pairs at a time, the same for all lanes.
 template <int GT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-embed_rank_kernel(const __grid_constant__ EmbedGradArgs a, int rank_blocks)
+embed_zero_kernel(const __grid_constant__ EmbedGradArgs a)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    zero_rows<GT, VEC>(a, 0, a.tok.rows, (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5),
+                       (int64_t)gridDim.x * 8);
+}
+
+// 32 tokens a block, one a lane, each warp against an eighth of the list, which it
+// reads from shared memory four pairs at a time, the same for all lanes.
+// BESIDE (here and below): runs beside embed_zero_kernel.
+template <bool BESIDE>
+__global__ void __launch_bounds__(kThreads)
+embed_rank_kernel(const __grid_constant__ EmbedGradArgs a)
 {
     __shared__ __align__(16) uint32_t pairs[kRankTokens];
     __shared__ uint32_t part[8][32];
-    pdl_wait();
+    if (!BESIDE) pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)blockIdx.x >= rank_blocks) {
-        zero_rows<GT, VEC>(a, 0, a.tok.rows, (int64_t)(blockIdx.x - rank_blocks) * 8 + warp,
-                         (int64_t)(gridDim.x - rank_blocks) * 8);
-        return;
-    }
     const int n = (int)a.tok.n;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_runs = 0;
     // eight warps' whole rounds of 16, the last filled up with what comes after all
     const int padded = (n + 127) / 128 * 128;
-    uint32_t k[8];
+    uint32_t k[kRankTokens / kThreads];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < kRankTokens / kThreads; ++u) {
         const int i = (int)threadIdx.x + u * kThreads;
         k[u] = i < n ? token_key(a.tok, i) << 13 | (uint32_t)i : kNone;
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) pairs[threadIdx.x + u * kThreads] = k[u];
+    for (int u = 0; u < kRankTokens / kThreads; ++u) pairs[threadIdx.x + u * kThreads] = k[u];
     __syncthreads();
     const int i = (int)blockIdx.x * 32 + lane;
     const uint32_t own = i < n ? pairs[i] : 0u;
@@ -278,6 +315,7 @@ embed_rank_kernel(const __grid_constant__ EmbedGradArgs a, int rank_blocks)
         a.key[0][at] = own >> 13;
         a.idx[0][at] = (uint32_t)i;
     }
+    if (BESIDE) pdl_wait();
 }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -301,24 +339,18 @@ __device__ __forceinline__ void store_peer(const void *p, uint32_t rank, uint32_
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
-// The first cluster sorts, the other blocks zero rows.  A pair is one
-// word (id << 13 | position), a thread has one in every pass.
-template <int GT, bool VEC>
+// One cluster.  A pair is one word (id << 13 | position), a thread has one in
+// every pass.
+template <bool BESIDE>
 __global__ void __launch_bounds__(kSortThreads)
 embed_cluster_kernel(const __grid_constant__ EmbedGradArgs a, int passes, int blocks)
 {
     __shared__ uint32_t list[2][kSortThreads];
     __shared__ unsigned short count[kSortWarps][256];
     __shared__ uint32_t total[256], hist[8][256], sum[256], before[256];
-    pdl_wait();
+    if (!BESIDE) pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)blockIdx.x >= blocks) {
-        zero_rows<GT, VEC>(a, 0, a.tok.rows,
-                         (int64_t)(blockIdx.x - blocks) * kSortWarps + warp,
-                         (int64_t)(gridDim.x - blocks) * kSortWarps);
-        return;
-    }
     const uint32_t rank = cluster_rank();
     const int n = (int)a.tok.n, i = (int)rank * kSortThreads + (int)threadIdx.x;
     const bool live = i < n;                  // the places 0 .. n are taken in every pass
@@ -363,6 +395,7 @@ embed_cluster_kernel(const __grid_constant__ EmbedGradArgs a, int passes, int bl
         a.key[0][i] = pair >> 13;
         a.idx[0][i] = pair & 8191u;
     }
+    if (BESIDE) pdl_wait();
 }
 
 // Counts of the first digit, a block at a time.  The later digits' counts and
@@ -525,8 +558,7 @@ embed_place_kernel(const __grid_constant__ EmbedGradArgs a, int pass, int passes
 // against 103 for 131,071 tokens of 1600 columns.)
 int64_t sum_chunk(int64_t n)
 {
-    if (n <= 2048) return 8;
-    int64_t c = 16;
+    int64_t c = n <= kRankTokens ? 8 : 16;
     while (c < 256 && n > c * 2048) c *= 2;
     return c;
 }
@@ -568,6 +600,121 @@ __device__ __forceinline__ void put_part(float *p, const float (&acc)[8])
 {
     reinterpret_cast<float4 *>(p)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+}
+
+// Up to kFewTokens tokens, without a sort: a block takes a token, and ends at
+// once if an earlier one has its id.  Otherwise it lists the positions of that
+// id and adds up their rows, a warp 256 columns; of a narrow table, and of an
+// id with many positions, several warps share the columns and take the positions
+// in turn, and their sums join in the warps' order.
+template <int YT, int GT, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kThreads)
+embed_few_kernel(const __grid_constant__ EmbedGradArgs a, int segs, int least)
+{
+    constexpr int U = YT == F32 || !VEC ? 4 : 8;
+    __shared__ unsigned short list[kFewTokens];
+    __shared__ uint32_t found[kFewTokens / 32];
+    __shared__ int n_list;
+    __shared__ float sums[8][kCols];
+    if (ACC) pdl_wait();                      // else beside embed_zero_kernel
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = (int)a.tok.n, i = (int)blockIdx.x;
+    const int64_t id = token_row(a.tok, i);
+    bool again = false;
+    if (id >= 0) {
+        int64_t other[kFewTokens / kThreads];
+#pragma unroll
+        for (int u = 0; u < kFewTokens / kThreads; ++u) {
+            const int j = u * kThreads + (int)threadIdx.x;
+            other[u] = j < n ? token_row(a.tok, j) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kFewTokens / kThreads; ++u) {
+            const int j = u * kThreads + (int)threadIdx.x;
+            again |= other[u] == id && j < i;
+            const uint32_t m = __ballot_sync(0xffffffffu, other[u] == id);
+            if (lane == 0) found[u * 8 + warp] = m;
+        }
+    }
+    // nothing to do (the same for the whole block)
+    const bool idle = __syncthreads_or(again) || id < 0;
+    if (!idle) {
+        if (warp == 0) {
+            static_assert(kFewTokens % 64 == 0 && kFewTokens <= 2048, "two words a lane");
+            const bool has = lane < kFewTokens / 64;
+            const uint32_t m0 = has ? found[2 * lane] : 0u, m1 = has ? found[2 * lane + 1] : 0u;
+            const int own = __popc(m0) + __popc(m1);
+            int at = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += v;
+            }
+            if (lane == 31) n_list = at;
+            at -= own;
+            for (uint32_t m = m0; m; m &= m - 1)
+                list[at++] = (unsigned short)(lane * 64 + __ffs(m) - 1);
+            for (uint32_t m = m1; m; m &= m - 1)
+                list[at++] = (unsigned short)(lane * 64 + 32 + __ffs(m) - 1);
+        }
+        __syncthreads();
+        const int count = n_list, shares = count > 32 ? 8 : least;
+        const int share = warp % shares, lead = warp / shares * shares;
+        const elems::Span dy = span_of<YT>(a.dy, a.tok.n, a.dy_stride, a.dim);
+        const elems::Span grad = span_of<GT>(a.grad, a.tok.rows, a.grad_stride, a.dim);
+        constexpr int kSize = elems::Raw<YT>::kSize;
+        // the same number of rounds for every warp: they join through shared memory
+        for (int seg0 = 0; seg0 < segs; seg0 += 8 / shares) {
+            const int seg = seg0 + warp / shares;
+            const int64_t c0 = (int64_t)seg * kCols;
+            const int64_t col = c0 + lane * 8 < a.dim || !VEC ? c0 + lane * 8 : a.dim - 8;
+            elems::Eight<GT, VEC> old;
+            float acc[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+            if (seg < segs) {
+                if (ACC && share == 0) ask_row<GT, VEC>(a, grad, (uint32_t)id, c0, old);
+                for (int k = share; k < count; k += U * shares) {
+                    elems::Eight<YT, VEC> r[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int64_t p = list[k + u * shares < count ? k + u * shares : k];
+                        r[u].ask(a.dy, p * a.dy_stride + col, dy,
+                                 dy.around((p * a.dy_stride + c0) * kSize, kCols * kSize));
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (k + u * shares >= count) break;
+                        float f[8];
+                        r[u].take().get(f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[e] = __fadd_rn(acc[e], f[e]);
+                    }
+                }
+            }
+            if (shares > 1 && count > 1) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sums[warp][lane * 8 + e] = acc[e];
+                __syncthreads();
+                if (share == 0) {
+                    for (int w = 1; w < shares && w < count; ++w)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            acc[e] = __fadd_rn(acc[e], sums[lead + w][lane * 8 + e]);
+                }
+                __syncthreads();
+            }
+            if (!ACC && seg0 == 0) pdl_wait();
+            if (seg < segs && share == 0) {
+                elems::Raw<GT> was;
+                if (ACC) was = old.take();
+                put_row<GT, VEC, ACC>(a, (uint32_t)id, c0, acc, was);
+            }
+        }
+    } else if (!ACC) {
+        pdl_wait();
+    }
 }
 
 template <int YT, int GT, bool VEC, bool ACC>
@@ -800,21 +947,12 @@ embed_runs_kernel(const __grid_constant__ EmbedGradArgs a, int side, int64_t chu
     }
 }
 
-template <int GT, bool VEC>
-cudaError_t small_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
+cudaError_t cluster_go(const EmbedGradArgs &a, cudaStream_t s)
 {
-    const int64_t n = a.tok.n;
-    if (n == 0 && a.accumulate) return cudaSuccess;
-    if (n <= kRankTokens) {
-        const int blocks = (int)((n + 31) / 32), fill = a.accumulate ? 0 : 4 * sms;
-        return launch_dependent(embed_rank_kernel<GT, VEC>, dim3((unsigned)(blocks + fill)),
-                                dim3(kThreads), 0, s, a, blocks);
-    }
     int blocks = 1;
-    while (blocks * kSortThreads < n) blocks *= 2;
-    const int fill = a.accumulate ? 0 : 2 * sms / blocks * blocks;
+    while (blocks * kSortThreads < a.tok.n) blocks *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks + fill));
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kSortThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -826,23 +964,40 @@ cudaError_t small_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, embed_cluster_kernel<GT, VEC>, a, sort_passes(a.tok.rows),
-                              blocks);
+    return cudaLaunchKernelEx(&cfg, a.accumulate ? embed_cluster_kernel<false>
+                                                 : embed_cluster_kernel<true>,
+                              a, sort_passes(a.tok.rows), blocks);
 }
 
 template <int YT, int GT, bool VEC, bool ACC>
 cudaError_t grad_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
 {
     const int64_t n = a.tok.n;
+    const int segs = (int)((a.dim + kCols - 1) / kCols);
     int side = 0;
     cudaError_t e;
+    if (!ACC && (n <= kFewTokens || sort_small(a))) {
+        // one wave of blocks, so that the next kernel starts beside them
+        e = launch_dependent(embed_zero_kernel<GT, VEC>, dim3((unsigned)(4 * sms)),
+                             dim3(kThreads), 0, s, a);
+        if (e != cudaSuccess || n == 0) return e;
+    }
+    if (n <= kFewTokens) {
+        const int least = segs == 1 ? 8 : segs == 2 ? 4 : segs <= 4 ? 2 : 1;
+        return launch_dependent(embed_few_kernel<YT, GT, VEC, ACC>, dim3((unsigned)n),
+                                dim3(kThreads), 0, s, a, segs, least);
+    }
     if (sort_small(a)) {
-        e = small_go<GT, VEC>(a, sms, s);
+        e = n > kRankTokens ? cluster_go(a, s)
+                            : launch_dependent(ACC ? embed_rank_kernel<false>
+                                                   : embed_rank_kernel<true>,
+                                               dim3((unsigned)((n + 31) / 32)), dim3(kThreads), 0,
+                                               s, a);
         if (e != cudaSuccess) return e;
     } else {
         const int passes = sort_passes(a.tok.rows);
         const int64_t chunk = sort_chunk(n);
-        const int blocks = n ? (int)((n + chunk - 1) / chunk) : 1;
+        const int blocks = (int)((n + chunk - 1) / chunk);
         const int fill = ACC ? 0 : 2 * sms;
         e = launch_dependent(embed_count_kernel<GT, VEC>, dim3((unsigned)(blocks + fill)),
                              dim3(kSortThreads), 0, s, a, chunk, passes, blocks);
@@ -854,9 +1009,7 @@ cudaError_t grad_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
         }
         side = (passes - 1) & 1;
     }
-    if (n == 0) return cudaSuccess;
     const int64_t chunk = sum_chunk(n);
-    const int segs = (int)((a.dim + kCols - 1) / kCols);
     const int64_t tasks = (n + chunk - 1) / chunk * segs;
     const int threads = tasks <= 16 * (int64_t)sms ? 64 : kThreads;   // few tasks: spread them
     const int64_t blocks = (tasks * 32 + threads - 1) / threads;
@@ -897,7 +1050,8 @@ cudaError_t launch_embed(int32_t dt, const EmbedArgs &a, cudaStream_t s)
 
 int64_t embed_grad_layout(EmbedGradArgs &a, char *base)
 {
-    const int64_t n = a.tok.n;
+    // few tokens need no lists; the arrays then have no elements
+    const int64_t n = a.tok.n <= kFewTokens ? 0 : a.tok.n;
     int64_t off = 0;
     auto take = [&](int64_t bytes) {
         char *p = base + off;
@@ -908,7 +1062,7 @@ int64_t embed_grad_layout(EmbedGradArgs &a, char *base)
     const int64_t segs = (a.dim + kCols - 1) / kCols;
     a.n_runs = reinterpret_cast<uint32_t *>(take(4));
     a.runs = reinterpret_cast<uint32_t *>(take(4 * chunks));
-    const bool big = !sort_small(a);
+    const bool big = n > 0 && !sort_small(a);
     for (int i = 0; i < 2; ++i) {
         const int64_t len = i == 0 || big ? n : 0;
         a.key[i] = reinterpret_cast<uint32_t *>(take(4 * len));
