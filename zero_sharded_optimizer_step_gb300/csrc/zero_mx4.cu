@@ -10,6 +10,11 @@
 // elements far below the block's largest, correctly rounded) multiplication.
 // A block that holds an infinity or NaN gets the scale 255 (NaN): every
 // product with it is NaN.
+//
+// What bounds it: memory (2 bytes in, 17/32 out an element and direction) for
+// one direction, for both from one read the ALU beside it (14 instructions an
+// element).  Measured for 8192 x 11008 bf16: both ways 55 us (5.0 TB/s), rows
+// alone 43, back to values 35 (6.4 TB/s); fp32 both ways 85 us (5.4 TB/s).
 #include "zero_elems.cuh"
 #include "zero_ops.h"
 

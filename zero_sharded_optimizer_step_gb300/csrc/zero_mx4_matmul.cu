@@ -22,6 +22,12 @@
 //
 // Every wait on a barrier is bounded; one that runs out is counted and ends
 // the block without a store.
+//
+// What bounds it: with few rows of A the bytes of B and the latency of a launch
+// (one row by 11008 x 4096: 6.7 us for 24 MB; 768 x 768: 2.5 us), with many the
+// tensor cores, whose rate for this kind is 16,384 multiply-adds a clock and SM
+// (measured: 128 clocks for 128 x 256 x 64).  Large products take the pair
+// kernel: 8192^3 in 149 us, 7.4 PFLOP/s, the tensor pipe 84% busy.
 #include <atomic>
 
 #include <cuda.h>
