@@ -169,6 +169,22 @@ def test_embed_grad_lengths_and_runs(n, kind):
     check_embed_grad(dy, t, rows, 1.0, 100, got)
 
 
+@pytest.mark.parametrize("n", [511, 512, 513, 2047, 2048, 2049, 4097])
+@pytest.mark.parametrize("rows,dim", [(300, 8), (524_287, 24), (524_288, 33), (900, 1111)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_path_boundaries(n, rows, dim, accumulate):
+    """Lengths and table sizes at which another way of sorting takes over."""
+    g = gen(n + rows)
+    t = (torch.exp(torch.rand(n, generator=g, device=DEV) * 6).long() * 7919) % rows
+    t[::9] = torch.randint(0, rows, (len(t[::9]),), generator=g, device=DEV)
+    t[1], t[n - 2] = -7, rows
+    dy = randn(g, n, dim, dtype=torch.float16)
+    grad = randn(g, rows, dim) if accumulate else None
+    old = R.host(grad) if accumulate else None
+    got = embed_grad(dy, t, rows, 0.25, grad=grad, accumulate=accumulate)
+    check_embed_grad(dy, t, rows, 0.25, -1, got, old)
+
+
 @pytest.mark.parametrize("rows", [1, 255, 256, 65_535, 65_536, 16_777_217])
 @pytest.mark.parametrize("n", [100, 10_000])
 def test_embed_grad_digit_counts(rows, n):
@@ -561,6 +577,79 @@ def test_linear_layer_gradients_against_differences():
         up, down = w.clone(), w.clone()
         up[i + 5, c], down[i + 5, c] = 1.5, 0.5
         assert loss(x, up) - loss(x, down) == float(dw[i + 5, c])
+
+
+# ------------------------------------------------- more than 2^31 (2^32) elements
+
+def test_embed_grad_of_a_long_list():
+    """dy of more than 2^31 elements: rows that one token each names hold that
+    token's row, the last of them among them; one frequent row, of whole numbers,
+    the exact sum."""
+    n, dim, rows = 1_100_000, 2048, 3000
+    dy = torch.ones(n, dim, dtype=torch.bfloat16, device=DEV)
+    t = torch.full((n,), 7, dtype=torch.int32, device=DEV)
+    single = torch.tensor([0, 1, 65_536, n // 2, n - 2, n - 1], device=DEV)
+    t[single] = torch.arange(100, 106, device=DEV, dtype=torch.int32)
+    dy[single] = randn(gen(1), 6, dim, dtype=torch.bfloat16)
+    got = embed_grad(dy, t, rows)
+    assert torch.equal(got[100:106], dy[single].float())
+    assert bool((got[7] == n - 6).all())               # below 2^24: exact in any order
+    got[7], got[100:106] = 0, 0
+    assert not got.any()
+
+
+def test_embed_grad_into_a_large_table():
+    rows, dim = 1_100_000, 2048
+    grad = torch.zeros(rows, dim, dtype=torch.bfloat16, device=DEV)
+    t = torch.tensor([rows - 1, 5, rows - 2, 5], device=DEV)
+    dy = torch.ones(4, dim, dtype=torch.bfloat16, device=DEV)
+    embed_grad(dy, t, rows, grad=grad, accumulate=True)
+    assert bool((grad[-2:] == 1).all()) and bool((grad[5] == 2).all())
+    assert not grad[6:-2].any()
+    grad.fill_(3)
+    embed_grad(dy, t, rows, grad=grad)
+    assert bool((grad[-2:] == 1).all()) and bool((grad[5] == 2).all())
+    assert not grad[6:-2].any() and not grad[:5].any()
+
+
+def test_dropout_of_more_than_2_to_32_elements():
+    n = 2 ** 32 + 24
+    x = torch.ones(n, dtype=torch.float16, device=DEV)
+    dropout(x, 0.5, 3, 4, out=x)
+    for lo in (0, 2 ** 31 - 8, 2 ** 32 - 8, n - 24):
+        m = min(64, n - lo)
+        kept = R.keep(m, 0.5, 3, 4, lo)
+        assert np.array_equal(R.host(x[lo:lo + m]), kept * 2.0)
+
+
+def test_quantize_of_more_than_2_to_31_elements():
+    rows, cols = 70_000, 32_768
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[-300:, -600:] = randn(gen(2), 300, 600, dtype=torch.bfloat16)
+    q, qt = quantize(x, True, True)
+    out = torch.empty_like(x)
+    z.zero_mx4_dequantize(q, rows, cols, out, z.ZERO_BF16, cols)
+    part = R.host(x[-304:, -608:])                      # whole blocks of 32 columns
+    assert np.array_equal(R.host(out[-304:, -608:]), R.values(*R.quantize(part)))
+    assert not out[:-300].any()
+    back = torch.empty(cols, rows, dtype=torch.bfloat16, device=DEV)
+    z.zero_mx4_dequantize(qt, cols, rows, back, z.ZERO_BF16, rows)
+    part = R.host(x[69_664:, -608:]).T                  # 69,664 is a multiple of 32
+    assert np.array_equal(R.host(back[-608:, 69_664:]), R.values(*R.quantize(part)))
+    assert not back[:-600].any()
+
+
+@pytest.mark.parametrize("n,stride", [(46_400, 46_400), (46_401, 46_401)])
+def test_matmul_into_more_than_2_to_31_elements(n, stride):
+    m, k = 46_500, 64
+    g = gen(3)
+    x, w = randn(g, m, k), randn(g, n, k)
+    (a, _), (b, _) = quantize(x), quantize(w)
+    out = torch.full((m, stride), 5.0, dtype=torch.bfloat16, device=DEV)
+    matmul(a, m, b, n, k, out)
+    av, bv = R.values(*R.quantize(R.host(x))), R.values(*R.quantize(R.host(w)))
+    for rows in (slice(0, 3), slice(m // 2, m // 2 + 3), slice(m - 3, m)):
+        check_product(av[rows], bv, 1.0, out[rows])
 
 
 # ------------------------------------------------------------ streams, graphs

@@ -115,15 +115,15 @@ __device__ __forceinline__ elems::Raw<DT> load8(const MxQuantArgs &a, int64_t ro
 
 // ---- 16-bit types, two elements a word
 
-// The larger magnitudes of two words' elements; NaN where one is.
+// The larger of a's elements and of b's magnitudes; NaN where one is.
 template <int DT> __device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b)
 {
     if constexpr (DT == BF16) {
-        const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<__nv_bfloat162 *>(&a)),
+        const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a),
                                              __habs2(*reinterpret_cast<__nv_bfloat162 *>(&b)));
         return *reinterpret_cast<const uint32_t *>(&m);
     } else {
-        const __half2 m = __hmax2_nan(__habs2(*reinterpret_cast<__half2 *>(&a)),
+        const __half2 m = __hmax2_nan(*reinterpret_cast<__half2 *>(&a),
                                       __habs2(*reinterpret_cast<__half2 *>(&b)));
         return *reinterpret_cast<const uint32_t *>(&m);
     }
@@ -162,7 +162,7 @@ template <int DT>
 __device__ __forceinline__ void put_row16(unsigned char *rec, int r, uint4 v)
 {
     const int lane = threadIdx.x & 31;
-    uint32_t top = top2<DT>(top2<DT>(v.x, v.y), top2<DT>(v.z, v.w));
+    uint32_t top = top2<DT>(top2<DT>(top2<DT>(top2<DT>(0, v.x), v.y), v.z), v.w);
     top = top2<DT>(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = top2<DT>(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const uint32_t scale = block_scale16<DT>(max(top & 0xffffu, top >> 16));
@@ -237,7 +237,7 @@ mx4_both16_kernel(const __grid_constant__ MxQuantArgs a, int64_t kt, int64_t ktt
             uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                top = top2<DT>(top, top2<DT>(top2<DT>(v[j].x, v[j].y), top2<DT>(v[j].z, v[j].w)));
+                top = top2<DT>(top2<DT>(top2<DT>(top2<DT>(top, v[j].x), v[j].y), v[j].z), v[j].w);
             const uint32_t scale = block_scale16<DT>(max(top & 0xffffu, top >> 16));
             const float inv = block_inverse(scale);
             uint32_t w[4];
