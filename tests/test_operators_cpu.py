@@ -133,3 +133,79 @@ def test_layers_refuse_what_is_not_on_a_gpu(z):
                 lambda: z.Mx4Linear(t)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_calls_convert_or_refuse_their_arguments(z):
+    """The compiled marshalling: what is no pointer, whole number or number
+    raises, and nothing is called; what converts reaches the library's checks."""
+    from zero_sharded_optimizer_step_gb300 import _calls
+
+    class Tensor:
+        def __init__(self, at):
+            self.at = at
+
+        def data_ptr(self):
+            return self.at
+
+    class Broken:
+        def data_ptr(self):
+            raise KeyError("broken")
+
+    ok = [A, None, B, z.ZERO_F32, 0, 0.1, 3, 4, 0, 5]     # no elements: nothing is launched
+    z.zero_dropout(*ok)
+    z.zero_dropout(*edit(ok, 0, Tensor(A)))
+    z.zero_dropout(*edit(ok, 4, np.int64(0)))
+    z.zero_dropout(*edit(ok, 5, 0))
+    z.zero_dropout(*edit(ok, 6, (1 << 64) - 1))
+    z.zero_dropout(*edit(ok, 6, -1))                      # the seed's 64 bits
+    for i, v, error in [(0, "x", AttributeError), (0, Broken(), KeyError), (0, -1, OverflowError),
+                        (2, Tensor("x"), TypeError), (3, 1 << 31, OverflowError),
+                        (3, 0.5, TypeError), (4, 1 << 63, OverflowError), (4, None, TypeError),
+                        (5, "x", TypeError), (6, 0.5, TypeError), (8, 1.0, TypeError)]:
+        with pytest.raises(error):
+            z.zero_dropout(*edit(ok, i, v))
+    refused(z, z.ZERO_EINVAL, z.zero_dropout, *edit(ok, 0, Tensor(0))[:4], 4, *ok[5:])
+    for name, n in [("embed", 14), ("embed_grad", 17), ("dropout", 10), ("quantize", 8),
+                    ("dequantize", 7), ("matmul", 11), ("bind", 6)]:
+        for count in (0, n - 1, n + 1):
+            with pytest.raises(TypeError):
+                getattr(_calls, name)(*[0] * count)
+    with pytest.raises(TypeError):
+        z.zero_dropout(*ok[:4])
+
+
+def test_calls_pass_every_argument_in_its_place(tmp_path):
+    """A second copy of the module, loaded from its own file and bound to callbacks
+    that write down what they are given."""
+    import ctypes as c
+    import importlib.util
+    import shutil
+
+    import __graft_entry__
+    path = str(tmp_path / "_calls.so")
+    shutil.copy(__graft_entry__._library_builder().build_calls(), path)
+    spec = importlib.util.spec_from_file_location("_calls", path)
+    calls = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(calls)
+    with pytest.raises(RuntimeError):
+        calls.matmul(*[0] * 11)
+    p, i, l, f, d, u = c.c_void_p, c.c_int32, c.c_int64, c.c_float, c.c_double, c.c_uint64
+    signatures = {
+        "embed": [p, i, l, l, l, p, i, l, l, f, p, l, p, p],
+        "embed_grad": [p, i, l, p, i, l, l, f, p, i, l, l, l, i, p, l, p],
+        "dropout": [p, p, p, i, l, d, u, u, l, p],
+        "quantize": [p, i, l, l, l, p, p, p],
+        "dequantize": [p, l, l, p, i, l, p],
+        "matmul": [p, l, p, l, l, f, i, p, i, l, p]}
+    seen, kept = [], []
+    for types in signatures.values():
+        kept.append(c.CFUNCTYPE(c.c_int, *types)(lambda *a: seen.append(a) or len(a)))
+    calls.bind(*(c.cast(k, p).value for k in kept))
+    big = {p: 1 << 63, l: -(1 << 62), i: -(1 << 30), f: 0.5, d: 1 / 3, u: (1 << 64) - 9}
+    truth = {"embed_grad": 13, "matmul": 6}
+    for name, types in signatures.items():
+        given = [big[t] + k if t not in (f, d) else big[t] + k for k, t in enumerate(types)]
+        if name in truth:
+            given[truth[name]] = True
+        assert getattr(calls, name)(*given) == len(types)
+        assert list(seen.pop()) == given

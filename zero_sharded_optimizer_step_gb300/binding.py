@@ -511,11 +511,27 @@ def zero_step_noalloc(ctx, grads, lr: float, beta1: float, beta2: float, eps: fl
 
 # ------------------------------------------------------- training operators
 
+# Called many times a step, on small tensors too: their arguments go through a
+# compiled module (csrc/zero_calls.c) instead of ctypes.
+
+try:
+    from . import _calls
+except ImportError as e:
+    raise ImportError("_calls.so is not built (run __graft_entry__.build() or "
+                      "python zero_sharded_optimizer_step_gb300/build.py): %s" % e) from e
+
+_calls.bind(*(ctypes.cast(getattr(_L, _name), _vp).value for _name in (
+    "zero_embed", "zero_embed_grad", "zero_dropout", "zero_mx4_quantize", "zero_mx4_dequantize",
+    "zero_mx4_matmul")))
+
+
 def zero_embed(table, dtype: int, rows: int, dim: int, table_stride: int, tokens,
                token_bytes: int, n: int, pad: int, scale: float, out, out_stride: int, bad=None,
                stream=None) -> None:
-    _check(_L.zero_embed(_ptr(table), dtype, rows, dim, table_stride, _ptr(tokens), token_bytes,
-                         n, pad, scale, _ptr(out), out_stride, _ptr(bad), _stream(stream)))
+    rc = _calls.embed(table, dtype, rows, dim, table_stride, tokens, token_bytes, n, pad, scale,
+                      out, out_stride, bad, stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_embed_grad_workspace(rows: int, dim: int, n: int) -> int:
@@ -526,16 +542,19 @@ def zero_embed_grad(dy, dy_dtype: int, dy_stride: int, tokens, token_bytes: int,
                     pad: int, scale: float, dtable, grad_dtype: int, rows: int, dim: int,
                     dtable_stride: int, accumulate: bool, workspace, workspace_bytes: int,
                     stream=None) -> None:
-    _check(_L.zero_embed_grad(_ptr(dy), dy_dtype, dy_stride, _ptr(tokens), token_bytes, n, pad,
-                              scale, _ptr(dtable), grad_dtype, rows, dim, dtable_stride,
-                              int(accumulate), _ptr(workspace), workspace_bytes,
-                              _stream(stream)))
+    rc = _calls.embed_grad(dy, dy_dtype, dy_stride, tokens, token_bytes, n, pad, scale, dtable,
+                           grad_dtype, rows, dim, dtable_stride, accumulate, workspace,
+                           workspace_bytes, stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_dropout(x, residual, out, dtype: int, n: int, p: float, seed: int, offset: int,
                  first: int = 0, stream=None) -> None:
-    _check(_L.zero_dropout(_ptr(x), _ptr(residual), _ptr(out), dtype, n, p, seed, offset, first,
-                           _stream(stream)))
+    rc = _calls.dropout(x, residual, out, dtype, n, p, seed, offset, first,
+                        stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_mx4_bytes(rows: int, cols: int) -> int:
@@ -544,20 +563,26 @@ def zero_mx4_bytes(rows: int, cols: int) -> int:
 
 def zero_mx4_quantize(x, dtype: int, rows: int, cols: int, stride: int, q, qt=None,
                       stream=None) -> None:
-    _check(_L.zero_mx4_quantize(_ptr(x), dtype, rows, cols, stride, _ptr(q), _ptr(qt),
-                                _stream(stream)))
+    rc = _calls.quantize(x, dtype, rows, cols, stride, q, qt,
+                         stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_mx4_dequantize(q, rows: int, cols: int, out, dtype: int, stride: int,
                         stream=None) -> None:
-    _check(_L.zero_mx4_dequantize(_ptr(q), rows, cols, _ptr(out), dtype, stride,
-                                  _stream(stream)))
+    rc = _calls.dequantize(q, rows, cols, out, dtype, stride,
+                           stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_mx4_matmul(a, m: int, b, n: int, k: int, alpha: float, accumulate: bool, out,
                     dtype: int, stride: int, stream=None) -> None:
-    _check(_L.zero_mx4_matmul(_ptr(a), m, _ptr(b), n, k, alpha, int(accumulate), _ptr(out),
-                              dtype, stride, _stream(stream)))
+    rc = _calls.matmul(a, m, b, n, k, alpha, accumulate, out, dtype, stride,
+                       stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_mx4_timeouts() -> int:

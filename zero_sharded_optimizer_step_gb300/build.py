@@ -1,4 +1,5 @@
-"""Build libzero.so, the CUDA library behind the binding, for sm_103a.
+"""Build libzero.so, the CUDA library behind the binding, for sm_103a, and
+_calls.so, the module that marshals its most frequent calls.
 
 Each translation unit is compiled in parallel with nvcc, then linked into a
 shared library next to this file (in-tree, so the binding finds it).  No
@@ -11,14 +12,17 @@ import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzero.so")
+CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ["zero_abi.cu", "zero_step_kernels.cu", "zero_gather.cu", "zero_advance.cu",
            "zero_embed.cu", "zero_dropout.cu", "zero_mx4.cu", "zero_mx4_matmul.cu",
            "zero_ops_abi.cu"]
+INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 HEADERS = ["zero_internal.h", "zero_ops.h", "zero_row_copy.cuh", "zero_elems.cuh", os.path.join("..", "..", "include", "zero.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -32,7 +36,22 @@ def _newest_input() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def build_calls(force: bool = False) -> str:
+    """The CPython module of csrc/zero_calls.c (host code only)."""
+    src = os.path.join(CSRC, "zero_calls.c")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "zero.h"),
+                                               os.path.abspath(__file__)))
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return CALLS
+    tmp = CALLS + ".tmp.%d" % os.getpid()
+    subprocess.run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE,
+                    "-I", sysconfig.get_paths()["include"], src, "-o", tmp], check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_calls(force)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -13,8 +13,8 @@
 //
 // What bounds it: memory (2 bytes in, 17/32 out an element and direction) for
 // one direction, for both from one read the ALU beside it (14 instructions an
-// element).  Measured for 8192 x 11008 bf16: both ways 55 us (5.0 TB/s), rows
-// alone 43, back to values 35 (6.4 TB/s); fp32 both ways 85 us (5.4 TB/s).
+// element).  Measured for 8192 x 11008 bf16: both ways 54 us (5.1 TB/s), rows
+// alone 42, back to values 35 (6.4 TB/s); fp32 both ways 85 us (5.4 TB/s).
 #include "zero_elems.cuh"
 #include "zero_ops.h"
 
