@@ -337,10 +337,20 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
-__device__ __forceinline__ void cluster_sync()
+__device__ __forceinline__ void cluster_arrive()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    cluster_arrive();
+    cluster_wait();
 }
 
 __device__ __forceinline__ void store_peer(const void *p, uint32_t rank, uint32_t v)
@@ -369,6 +379,9 @@ embed_cluster_kernel(const __grid_constant__ EmbedGradArgs a, int passes, int bl
                            (int64_t)(gridDim.x - blocks) * kSortWarps);
         return;
     }
+    // A block's shared memory may be written to once it is known to run: each
+    // arrives here, and waits for the others before its first store to them.
+    cluster_arrive();
     const uint32_t rank = cluster_rank();
     const int n = (int)a.tok.n, i = (int)rank * kSortThreads + (int)threadIdx.x;
     const bool live = i < n;                  // the places 0 .. n are taken in every pass
@@ -384,6 +397,7 @@ embed_cluster_kernel(const __grid_constant__ EmbedGradArgs a, int passes, int bl
         __syncthreads();
         prefix_warps(count, total);
         __syncthreads();
+        if (p == 0) cluster_wait();
         // every block gets every block's counts
         for (int c = threadIdx.x; c < 256 * blocks; c += kSortThreads)
             store_peer(&hist[rank][c & 255], (uint32_t)c >> 8, total[c & 255]);
