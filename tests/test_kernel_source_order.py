@@ -49,3 +49,14 @@ def test_a_cluster_barrier_comes_before_a_peers_shared_memory(kernel):
     first = re.search(PEER, body).start()
     barrier = re.search(r"\bcluster_(sync|wait)\(\)", body)
     assert barrier and barrier.start() < first, (file, name)
+
+
+@pytest.mark.parametrize("kernel", [k for k in ALL if "pdl_wait()" in k[2]], ids=lambda k: k[1])
+def test_a_kernel_waits_for_the_one_before_whatever_its_form(kernel):
+    """pdl_wait() is what makes an earlier kernel's writes visible, to the grid that
+    calls it: no template argument or flag may leave it out or put it off.  (A warp
+    with a task of its own may have a wait of its own.)"""
+    file, name, body = kernel
+    assert not re.search(r"\bif\s*\([^;{}]*\)\s*pdl_wait\(\)", body), (file, name)
+    for m in re.finditer(r"\bif\s*\(([^{};]*)\)\s*\{\s*pdl_wait\(\)", body):
+        assert "warp" in m.group(1), (file, name)

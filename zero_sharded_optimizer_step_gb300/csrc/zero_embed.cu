@@ -265,19 +265,6 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs &a, int64_t lo, in
         }
 }
 
-// For embed_few_kernel, which goes on beside it: that one starts once every
-// block of this one runs, which is after whatever came before has ended, and
-// waits for this one's end before it writes to the gradient.
-template <int GT, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-embed_zero_kernel(const __grid_constant__ EmbedGradArgs a)
-{
-    pdl_wait();
-    pdl_launch_dependents();
-    zero_rows<GT, VEC>(a, 0, a.tok.rows, (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5),
-                       (int64_t)gridDim.x * 8);
-}
-
 // The first rank_blocks blocks place 32 tokens each, one a lane, each warp against
 // an eighth of the list, which it reads from shared memory four pairs at a
 // time, the same for all lanes.  The others zero rows.
@@ -639,7 +626,48 @@ __device__ __forceinline__ void put_part(float *p, const float (&acc)[8])
 // once if an earlier one has its id.  Otherwise it lists the positions of that
 // id and adds up their rows, a warp 256 columns; of a narrow table, and of an
 // id with many positions, several warps share the columns and take the positions
-// in turn, and their sums join in the warps' order.
+// in turn, and their sums join in the warps' order.  Without ACC the blocks past
+// the tokens' zero the rows that no token names, a slice of the table each: they
+// mark the named rows of kMarkRows rows at a time and write what lies between
+// them, so that no row is written twice and one launch does (512 tokens into
+// 50,257 x 768 bf16: 14.9 us, against 24.4 with the zeroes in a launch before).
+constexpr int kMarkRows = 8192;
+
+template <int GT, bool VEC>
+__device__ __forceinline__ void zero_unnamed(const EmbedGradArgs &a, int64_t slice, int64_t slices)
+{
+    __shared__ uint32_t mark[kMarkRows / 32];
+    static_assert(kMarkRows / 32 == kThreads, "a word a thread");
+    const int warp = threadIdx.x >> 5;
+    int64_t row[kFewTokens / kThreads];
+#pragma unroll
+    for (int u = 0; u < kFewTokens / kThreads; ++u) {
+        const int j = u * kThreads + (int)threadIdx.x;
+        row[u] = j < (int)a.tok.n ? token_row(a.tok, j) : -1;
+    }
+    const int64_t end = a.tok.rows * (slice + 1) / slices;
+    for (int64_t lo = a.tok.rows * slice / slices; lo < end; lo += kMarkRows) {
+        const int m = (int)(end - lo < kMarkRows ? end - lo : kMarkRows);
+        __syncthreads();
+        mark[threadIdx.x] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kFewTokens / kThreads; ++u)
+            if (row[u] >= lo && row[u] < lo + m)
+                atomicOr(&mark[(row[u] - lo) >> 5], 1u << ((row[u] - lo) & 31));
+        __syncthreads();
+        for (int r = 0; r < m;) {
+            // the next named row from r on, the same for every thread
+            int w = r >> 5;
+            uint32_t bits = mark[w] & (0xffffffffu << (r & 31));
+            while (!bits && (w + 1) * 32 < m) bits = mark[++w];
+            const int next = bits ? w * 32 + __ffs(bits) - 1 : m;
+            if (next > r) zero_rows<GT, VEC>(a, lo + r, lo + next, warp, kThreads / 32);
+            r = next + 1;
+        }
+    }
+}
+
 template <int YT, int GT, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kThreads)
 embed_few_kernel(const __grid_constant__ EmbedGradArgs a, int segs, int least)
@@ -649,10 +677,14 @@ embed_few_kernel(const __grid_constant__ EmbedGradArgs a, int segs, int least)
     __shared__ uint32_t found[kFewTokens / 32];
     __shared__ int n_list;
     __shared__ float sums[8][kCols];
-    if (ACC) pdl_wait();                      // else beside embed_zero_kernel
+    pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n = (int)a.tok.n, i = (int)blockIdx.x;
+    if (!ACC && i >= n) {
+        zero_unnamed<GT, VEC>(a, i - n, (int64_t)gridDim.x - n);
+        return;
+    }
     const int64_t id = token_row(a.tok, i);
     bool again = false;
     if (id >= 0) {
@@ -738,15 +770,12 @@ embed_few_kernel(const __grid_constant__ EmbedGradArgs a, int segs, int least)
                 }
                 __syncthreads();
             }
-            if (!ACC && seg0 == 0) pdl_wait();
             if (seg < segs && share == 0) {
                 elems::Raw<GT> was;
                 if (ACC) was = old.take();
                 put_row<GT, VEC, ACC>(a, (uint32_t)id, c0, acc, was);
             }
         }
-    } else if (!ACC) {
-        pdl_wait();
     }
 }
 
@@ -1016,15 +1045,10 @@ cudaError_t grad_go(const EmbedGradArgs &a, int sms, cudaStream_t s)
     int side = 0;
     cudaError_t e;
     if (n <= kFewTokens) {
-        if (!ACC) {
-            // one wave of blocks, so that the next kernel starts beside them
-            e = launch_dependent(embed_zero_kernel<GT, VEC>, dim3((unsigned)(4 * sms)),
-                                 dim3(kThreads), 0, s, a);
-            if (e != cudaSuccess || n == 0) return e;
-        }
         const int least = segs == 1 ? 8 : segs == 2 ? 4 : segs <= 4 ? 2 : 1;
-        return launch_dependent(embed_few_kernel<YT, GT, VEC, ACC>, dim3((unsigned)n),
-                                dim3(kThreads), 0, s, a, segs, least);
+        return launch_dependent(embed_few_kernel<YT, GT, VEC, ACC>,
+                                dim3((unsigned)(n + (ACC ? 0 : 4 * sms))), dim3(kThreads), 0, s, a,
+                                segs, least);
     }
     if (sort_small(a)) {
         e = small_go<GT, VEC>(a, sms, s);
