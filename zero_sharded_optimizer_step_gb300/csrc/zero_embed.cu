@@ -38,8 +38,9 @@ template <int DT>
 __device__ __forceinline__ elems::Span span_of(const void *p, int64_t rows, int64_t stride,
                                                int64_t cols)
 {
+    // a table without rows has no bytes, whatever its stride (and may be null)
     const char *lo = static_cast<const char *>(p);
-    return {lo, lo + ((rows - 1) * stride + cols) * elems::Raw<DT>::kSize};
+    return {lo, rows > 0 ? lo + ((rows - 1) * stride + cols) * elems::Raw<DT>::kSize : lo};
 }
 
 template <int DT, bool VEC>
