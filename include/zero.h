@@ -672,7 +672,8 @@ int zero_step_noalloc(zero_ctx *ctx, const void *const *grads, int32_t n_grads, 
  * `dtype`, the product rounded once to it.  tokens: token_bytes is 4 or 8
  * (signed ids).  A token equal to `pad` (-1: none) gives a row of zeros; so
  * does one outside [0, rows), and it is counted: *bad (device memory, may be
- * NULL) grows by the number of such tokens. */
+ * NULL) grows by the number of such tokens.  With pad = -1 a token of -1 is
+ * counted too; a padding token is not, wherever it lies. */
 int zero_embed(const void *table, int32_t dtype, int64_t rows, int64_t dim, int64_t table_stride,
                const void *tokens, int32_t token_bytes, int64_t n, int64_t pad, float scale,
                void *out, int64_t out_stride, uint64_t *bad, void *stream);

@@ -58,7 +58,8 @@ embed_kernel(const __grid_constant__ EmbedArgs a, int segs)
     if (row < 0 && a.bad && lane == 0 && seg == 0) {
         const int64_t id = a.tok.wide ? static_cast<const long long *>(a.tok.ids)[i]
                                       : (int64_t)static_cast<const int *>(a.tok.ids)[i];
-        if (id != a.tok.pad) atomicAdd(a.bad, 1ull);
+        // a padding token is no wrong id, but -1 as such stands for none
+        if (id != a.tok.pad || id == -1) atomicAdd(a.bad, 1ull);
     }
     const int64_t c0 = (int64_t)seg * kEmbedFlight * kCols;
     const elems::Span table = span_of<DT>(a.table, a.tok.rows, a.table_stride, a.dim);

@@ -48,7 +48,7 @@ struct EmbedArgs {
     int64_t dim, table_stride, out_stride;
     float scale;
     void *out;
-    unsigned long long *bad;     // += ids outside the table that are not `pad` (or null)
+    unsigned long long *bad;     // += ids outside the table that are not `pad`, -1 always (or null)
 };
 cudaError_t launch_embed(int32_t dt, const EmbedArgs &a, cudaStream_t s);
 
