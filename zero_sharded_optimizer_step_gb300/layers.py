@@ -25,6 +25,19 @@ from . import binding as z
 _DT = {torch.float32: z.ZERO_F32, torch.bfloat16: z.ZERO_BF16, torch.float16: z.ZERO_F16}
 
 
+def _rows_apart(x: torch.Tensor) -> bool:
+    """Whether x's rows are runs of consecutive elements that do not overlap."""
+    return not (x.shape[1] > 1 and x.stride(1) != 1 or
+                x.shape[0] > 1 and x.stride(0) < x.shape[1])
+
+
+def _gradient(dy: torch.Tensor) -> torch.Tensor:
+    """An output's gradient as the library can take it.  torch hands on what the
+    next operation's gradient looks like: expanded over the rows after a sum
+    over them, say."""
+    return dy if _rows_apart(dy) else dy.contiguous()
+
+
 def _matrix(name: str, x: torch.Tensor) -> torch.Tensor:
     """x itself if the library can take it as rows of elements."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
@@ -33,7 +46,7 @@ def _matrix(name: str, x: torch.Tensor) -> torch.Tensor:
         raise ValueError("%s must be fp32, bf16 or fp16, not %s" % (name, x.dtype))
     if x.dim() != 2:
         raise ValueError("%s must have two dimensions, not %d" % (name, x.dim()))
-    if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+    if not _rows_apart(x):
         raise ValueError("%s must have consecutive elements in its rows" % name)
     return x
 
@@ -95,8 +108,8 @@ class _Embed(torch.autograd.Function):
         (flat,) = ctx.saved_tensors
         table = ctx.like
         grad = torch.empty(table.shape, dtype=table.dtype, device=table.device)
-        dy = dy.reshape(flat.numel(), table.shape[1])
-        embed_grad(dy if dy.stride(-1) == 1 else dy.contiguous(), flat, grad, ctx.scale, ctx.pad)
+        dy = _gradient(dy.reshape(flat.numel(), table.shape[1]))
+        embed_grad(dy, flat, grad, ctx.scale, ctx.pad)
         return grad, None, None, None, None
 
 
@@ -212,8 +225,7 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         dx = dw = None
-        if dy.stride(-1) != 1:
-            dy = dy.contiguous()
+        dy = _gradient(dy)
         q, qt = mx4_quantize(dy, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
         if q is not None:
             dx = mx4_matmul(q, ctx.wt, ctx.dtype)
