@@ -7,7 +7,8 @@ the binding on the current stream.  Outputs and workspaces come from torch's
 allocator.  A model's parameters are the optimizer's (ZeroAdam's views of
 its flat buffer, say); the gradients that backward() leaves in `.grad` go into
 a rank's gradient buffer, or `embed_grad` and `Mx4Linear.weight_grad` write them
-there directly.
+there directly.  The lookup and dropout can be differentiated any number of
+times, the linear layer once: an attempt at more raises.
 
     h = embed(table, tokens, pad=0)
     h = dropout(h, 0.1, seed, offset)
@@ -106,11 +107,23 @@ class _Embed(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         (flat,) = ctx.saved_tensors
-        table = ctx.like
-        grad = torch.empty(table.shape, dtype=table.dtype, device=table.device)
-        dy = _gradient(dy.reshape(flat.numel(), table.shape[1]))
-        embed_grad(dy, flat, grad, ctx.scale, ctx.pad)
-        return grad, None, None, None, None
+        dy = dy.reshape(flat.numel(), ctx.like.shape[1])
+        return _EmbedGrad.apply(dy, flat, ctx.like, ctx.scale, ctx.pad), None, None, None, None
+
+
+class _EmbedGrad(torch.autograd.Function):
+    """The lookup's transpose; its own gradient is the lookup again."""
+    @staticmethod
+    def forward(ctx, dy, flat, like, scale, pad):
+        ctx.save_for_backward(flat)
+        ctx.scale, ctx.pad = scale, pad
+        grad = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return embed_grad(_gradient(dy), flat, grad, scale, pad)
+
+    @staticmethod
+    def backward(ctx, g):
+        (flat,) = ctx.saved_tensors
+        return _Embed.apply(_gradient(g), flat, ctx.scale, ctx.pad, None), None, None, None, None
 
 
 def embed(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0, pad: int = -1,
@@ -141,7 +154,8 @@ class _Dropout(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        dx = _drop(dy, None, *ctx.args) if ctx.needs_input_grad[0] else None
+        # the same map of dy, and as such differentiable again
+        dx = _Dropout.apply(dy, None, *ctx.args) if ctx.needs_input_grad[0] else None
         return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
 
 
@@ -212,25 +226,47 @@ def mx4_matmul(a: Mx4Matrix, b: Mx4Matrix, dtype: torch.dtype = torch.bfloat16,
     return out
 
 
+class _Once(torch.autograd.Function):
+    """A gradient that depends on what `links` do and cannot be differentiated.
+    (torch's once_differentiable does not tie it to them: a derivative with
+    respect to given inputs would leave it out and say nothing.)"""
+    @staticmethod
+    def forward(ctx, grad, *links):
+        return grad.clone()
+
+    @staticmethod
+    def backward(ctx, g):
+        raise RuntimeError("Mx4Linear can be differentiated once: its gradients have none")
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, layer):
+        ctx.set_materialize_grads(False)
         ctx.layer, ctx.dtype = layer, x.dtype
         want = ctx.needs_input_grad[1]
         q, ctx.xt = mx4_quantize(x, True, want)
         # the weight as it was quantised for this forward pass
         ctx.wt = layer.wt if ctx.needs_input_grad[0] else None
-        return mx4_matmul(q, layer.w, x.dtype)
+        link = x.new_empty(0)            # leads back to x and the weight, and holds neither
+        ctx.save_for_backward(link)
+        return mx4_matmul(q, layer.w, x.dtype), link
 
     @staticmethod
-    def backward(ctx, dy):
+    def backward(ctx, dy, _):
         dx = dw = None
-        dy = _gradient(dy)
-        q, qt = mx4_quantize(dy, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
-        if q is not None:
-            dx = mx4_matmul(q, ctx.wt, ctx.dtype)
-        if qt is not None:
-            dw = mx4_matmul(qt, ctx.xt, ctx.layer.weight.dtype)
+        if dy is None:
+            return None, None, None
+        with torch.no_grad():
+            d = _gradient(dy)
+            q, qt = mx4_quantize(d, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+            if q is not None:
+                dx = mx4_matmul(q, ctx.wt, ctx.dtype)
+            if qt is not None:
+                dw = mx4_matmul(qt, ctx.xt, ctx.layer.weight.dtype)
+        if torch.is_grad_enabled():      # a graph of the gradients is wanted
+            (link,) = ctx.saved_tensors
+            dx, dw = (None if g is None else _Once.apply(g, dy, link) for g in (dx, dw))
         return dx, dw, None
 
 
@@ -257,7 +293,7 @@ class Mx4Linear:
             raise ValueError("x must have rows of %d elements on %s" % (k, self.weight.device))
         rows = x.reshape(-1, k)
         _matrix("x", rows)
-        return _Linear.apply(rows, self.weight, self).view(*x.shape[:-1], n)
+        return _Linear.apply(rows, self.weight, self)[0].view(*x.shape[:-1], n)
 
     def weight_grad(self, x: torch.Tensor, dy: torch.Tensor, grad: torch.Tensor,
                     accumulate: bool = False) -> torch.Tensor:
