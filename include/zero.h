@@ -742,9 +742,11 @@ int zero_mx4_dequantize(const void *q, int64_t rows, int64_t cols, void *out, in
  *   zero_mx4_matmul(x's q, m, W's q, n, k)         -> y
  *   zero_mx4_matmul(dy's q, m, W's qt, k, n)       -> dx
  *   zero_mx4_matmul(dy's qt, n, x's qt, k, m)      -> dW
- * The kernel's waits are bounded; zero_mx4_timeouts() (which synchronizes)
- * returns ZERO_ETIMEOUT and the count once one has run out in this process:
- * the results of the products since then are not to be used. */
+ * The kernel's waits are bounded, and a block whose wait runs out ends without
+ * storing its results.  zero_mx4_timeouts() waits for all work of the current
+ * device, whatever its stream, and returns ZERO_ETIMEOUT and the count once a
+ * wait has run out in this process on that device: the results of the products
+ * since then are not to be used. */
 int zero_mx4_matmul(const void *a, int64_t m, const void *b, int64_t n, int64_t k, float alpha,
                     int32_t accumulate, void *out, int32_t dtype, int64_t stride, void *stream);
 int zero_mx4_timeouts(uint32_t *count);

@@ -62,6 +62,13 @@ def batch(model: TokenModel, n: int, generator: torch.Generator):
     return tokens, targets
 
 
+def check_products() -> None:
+    """Raises if a 4-bit product gave up on the device (and stored nothing)."""
+    n = z.zero_mx4_timeouts()
+    if n:
+        raise RuntimeError("%d waits of the 4-bit products ran out" % n)
+
+
 def train(steps: int = 200, world: int = 2, n: int = 1024, lr: float = 3e-3, seed: int = 0,
           report=None):
     """The mean loss over the ranks, step by step."""
@@ -85,7 +92,9 @@ def train(steps: int = 200, world: int = 2, n: int = 1024, lr: float = 3e-3, see
         model.refresh()
         losses.append(total)
         if report and step % 20 == 19:
+            check_products()
             report("step %4d  loss %.4f" % (step + 1, float(total)))
+    check_products()
     return [float(v) for v in losses]
 
 

@@ -586,7 +586,8 @@ def zero_mx4_matmul(a, m: int, b, n: int, k: int, alpha: float, accumulate: bool
 
 
 def zero_mx4_timeouts() -> int:
-    """Waits of the product kernel that ran out (0 when all is well)."""
+    """Waits of the product kernel that ran out on the current device, once all
+    its work has ended (0 when all is well)."""
     n = ctypes.c_uint32()
     rc = _L.zero_mx4_timeouts(ctypes.byref(n))
     if rc != ZERO_ETIMEOUT:

@@ -950,6 +950,10 @@ cudaError_t launch_mx4_matmul(int32_t dt, const MxMatmulArgs &a, int sms, cudaSt
 
 cudaError_t mx4_timeouts(unsigned int *count)
 {
+    // the copy alone would not wait for streams that do not synchronise with the
+    // default one
+    const cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return e;
     return cudaMemcpyFromSymbol(count, g_mx4_timeouts, sizeof(unsigned int));
 }
 

@@ -10,6 +10,10 @@ a rank's gradient buffer, or `embed_grad` and `Mx4Linear.weight_grad` write them
 there directly.  The lookup and dropout can be differentiated any number of
 times, the linear layer once: an attempt at more raises.
 
+A 4-bit product whose waits on the device run out stores nothing, and its call
+has long returned: where a program reads its losses it also asks for the count
+(`zero_mx4_timeouts()`, 0 when all is well), which waits for the device.
+
     h = embed(table, tokens, pad=0)
     h = dropout(h, 0.1, seed, offset)
     y = layer(h)                     # layer = Mx4Linear(weight)
