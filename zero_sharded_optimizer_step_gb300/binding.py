@@ -514,15 +514,26 @@ def zero_step_noalloc(ctx, grads, lr: float, beta1: float, beta2: float, eps: fl
 # Called many times a step, on small tensors too: their arguments go through a
 # compiled module (csrc/zero_calls.c) instead of ctypes.
 
+class _NoCalls:
+    """Stands in for the module where it is not built: a call says so."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError("the _calls module is not built for this interpreter (run "
+                          "__graft_entry__.build() or python "
+                          "zero_sharded_optimizer_step_gb300/build.py): %s" % self.why)
+
+
 try:
     from . import _calls
 except ImportError as e:
-    raise ImportError("_calls.so is not built (run __graft_entry__.build() or "
-                      "python zero_sharded_optimizer_step_gb300/build.py): %s" % e) from e
-
-_calls.bind(*(ctypes.cast(getattr(_L, _name), _vp).value for _name in (
-    "zero_embed", "zero_embed_grad", "zero_dropout", "zero_mx4_quantize", "zero_mx4_dequantize",
-    "zero_mx4_matmul")))
+    _calls = _NoCalls(e)
+else:
+    _calls.bind(*(ctypes.cast(getattr(_L, _name), _vp).value for _name in (
+        "zero_embed", "zero_embed_grad", "zero_dropout", "zero_mx4_quantize",
+        "zero_mx4_dequantize", "zero_mx4_matmul")))
 
 
 def zero_embed(table, dtype: int, rows: int, dim: int, table_stride: int, tokens,

@@ -1,5 +1,5 @@
 """Build libzero.so, the CUDA library behind the binding, for sm_103a, and
-_calls.so, the module that marshals its most frequent calls.
+_calls, the CPython module that marshals its most frequent calls.
 
 Each translation unit is compiled in parallel with nvcc, then linked into a
 shared library next to this file (in-tree, so the binding finds it).  No
@@ -18,7 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzero.so")
-CALLS = os.path.join(HERE, "_calls.so")
+# named for the interpreter, so that another one does not load it
+CALLS = os.path.join(HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["zero_abi.cu", "zero_step_kernels.cu", "zero_gather.cu", "zero_advance.cu",
            "zero_embed.cu", "zero_dropout.cu", "zero_mx4.cu", "zero_mx4_matmul.cu",
            "zero_ops_abi.cu"]
@@ -37,15 +38,22 @@ def _newest_input() -> float:
 
 
 def build_calls(force: bool = False) -> str:
-    """The CPython module of csrc/zero_calls.c (host code only)."""
+    """The CPython module of csrc/zero_calls.c (host code only).  Without the
+    interpreter's headers it is left out: the training operators then raise where
+    they are called, and everything else works."""
     src = os.path.join(CSRC, "zero_calls.c")
     newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "zero.h"),
                                                os.path.abspath(__file__)))
     if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
         return CALLS
+    headers = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(headers, "Python.h")):
+        print("no Python.h under %s: %s is not built" % (headers, os.path.basename(CALLS)),
+              file=sys.stderr)
+        return CALLS
     tmp = CALLS + ".tmp.%d" % os.getpid()
     subprocess.run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE,
-                    "-I", sysconfig.get_paths()["include"], src, "-o", tmp], check=True)
+                    "-I", headers, src, "-o", tmp], check=True)
     os.replace(tmp, CALLS)
     return CALLS
 
