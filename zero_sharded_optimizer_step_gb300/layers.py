@@ -245,11 +245,12 @@ class _Once(torch.autograd.Function):
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, layer):
+    def forward(ctx, x, weight, layer, grads):
         ctx.set_materialize_grads(False)
         ctx.layer, ctx.dtype = layer, x.dtype
-        want = ctx.needs_input_grad[1]
-        q, ctx.xt = mx4_quantize(x, True, want)
+        # needs_input_grad tells what the tensors ask for, not whether a
+        # backward pass can follow (and here, inside, gradients are always off)
+        q, ctx.xt = mx4_quantize(x, True, grads and ctx.needs_input_grad[1])
         # the weight as it was quantised for this forward pass
         ctx.wt = layer.wt if ctx.needs_input_grad[0] else None
         link = x.new_empty(0)            # leads back to x and the weight, and holds neither
@@ -260,7 +261,7 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, dy, _):
         dx = dw = None
         if dy is None:
-            return None, None, None
+            return None, None, None, None
         with torch.no_grad():
             d = _gradient(dy)
             q, qt = mx4_quantize(d, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
@@ -271,7 +272,7 @@ class _Linear(torch.autograd.Function):
         if torch.is_grad_enabled():      # a graph of the gradients is wanted
             (link,) = ctx.saved_tensors
             dx, dw = (None if g is None else _Once.apply(g, dy, link) for g in (dx, dw))
-        return dx, dw, None
+        return dx, dw, None, None
 
 
 class Mx4Linear:
@@ -297,7 +298,8 @@ class Mx4Linear:
             raise ValueError("x must have rows of %d elements on %s" % (k, self.weight.device))
         rows = x.reshape(-1, k)
         _matrix("x", rows)
-        return _Linear.apply(rows, self.weight, self)[0].view(*x.shape[:-1], n)
+        return _Linear.apply(rows, self.weight, self, torch.is_grad_enabled())[0].view(
+            *x.shape[:-1], n)
 
     def weight_grad(self, x: torch.Tensor, dy: torch.Tensor, grad: torch.Tensor,
                     accumulate: bool = False) -> torch.Tensor:
