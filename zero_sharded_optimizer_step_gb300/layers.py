@@ -112,7 +112,14 @@ class _Embed(torch.autograd.Function):
     def backward(ctx, dy):
         (flat,) = ctx.saved_tensors
         dy = dy.reshape(flat.numel(), ctx.like.shape[1])
-        return _EmbedGrad.apply(dy, flat, ctx.like, ctx.scale, ctx.pad), None, None, None, None
+        grad = (_EmbedGrad.apply if torch.is_grad_enabled() else _table_grad)(
+            dy, flat, ctx.like, ctx.scale, ctx.pad)
+        return grad, None, None, None, None
+
+
+def _table_grad(dy, flat, like, scale, pad):
+    grad = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return embed_grad(_gradient(dy), flat, grad, scale, pad)
 
 
 class _EmbedGrad(torch.autograd.Function):
@@ -121,8 +128,7 @@ class _EmbedGrad(torch.autograd.Function):
     def forward(ctx, dy, flat, like, scale, pad):
         ctx.save_for_backward(flat)
         ctx.scale, ctx.pad = scale, pad
-        grad = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-        return embed_grad(_gradient(dy), flat, grad, scale, pad)
+        return _table_grad(dy, flat, like, scale, pad)
 
     @staticmethod
     def backward(ctx, g):
@@ -158,8 +164,10 @@ class _Dropout(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        # the same map of dy, and as such differentiable again
-        dx = _Dropout.apply(dy, None, *ctx.args) if ctx.needs_input_grad[0] else None
+        dx = None
+        if ctx.needs_input_grad[0]:
+            # the same map of dy; where a graph of it is wanted, differentiable again
+            dx = (_Dropout.apply if torch.is_grad_enabled() else _drop)(dy, None, *ctx.args)
         return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
 
 
@@ -253,25 +261,24 @@ class _Linear(torch.autograd.Function):
         q, ctx.xt = mx4_quantize(x, True, grads and ctx.needs_input_grad[1])
         # the weight as it was quantised for this forward pass
         ctx.wt = layer.wt if ctx.needs_input_grad[0] else None
-        link = x.new_empty(0)            # leads back to x and the weight, and holds neither
-        ctx.save_for_backward(link)
+        link = None
+        if grads:                        # leads back to x and the weight, and holds neither
+            link = x.new_empty(0)
+            ctx.save_for_backward(link)
         return mx4_matmul(q, layer.w, x.dtype), link
 
     @staticmethod
     def backward(ctx, dy, _):
         dx = dw = None
-        if dy is None:
-            return None, None, None, None
-        with torch.no_grad():
-            d = _gradient(dy)
-            q, qt = mx4_quantize(d, ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        if dy is not None:
+            q, qt = mx4_quantize(_gradient(dy), ctx.needs_input_grad[0], ctx.needs_input_grad[1])
             if q is not None:
                 dx = mx4_matmul(q, ctx.wt, ctx.dtype)
             if qt is not None:
                 dw = mx4_matmul(qt, ctx.xt, ctx.layer.weight.dtype)
-        if torch.is_grad_enabled():      # a graph of the gradients is wanted
-            (link,) = ctx.saved_tensors
-            dx, dw = (None if g is None else _Once.apply(g, dy, link) for g in (dx, dw))
+            if torch.is_grad_enabled():      # a graph of the gradients is wanted
+                (link,) = ctx.saved_tensors
+                dx, dw = (None if g is None else _Once.apply(g, dy, link) for g in (dx, dw))
         return dx, dw, None, None
 
 
