@@ -414,6 +414,8 @@ template <int DT, bool VEC> cudaError_t quant_go(const MxQuantArgs &a, int sms, 
     const int64_t limit = 0x7fffffff;
     if (!a.qt && (DT == F32 || a.rows * kt < (int64_t)sms * 32)) {
         const int64_t warps = a.rows * kt;
+        // one warp a block for few: 2.2 us a pass among others either way up to 1024
+        // warps, then slower (256 rows of 4096: 4.9 us against 2.2)
         const int threads = warps <= 1024 ? 32 : kThreads;
         const int64_t blocks = (warps * 32 + threads - 1) / threads;
         if (blocks > limit) return cudaErrorInvalidValue;
