@@ -751,6 +751,140 @@ int zero_mx4_matmul(const void *a, int64_t m, const void *b, int64_t n, int64_t 
                     int32_t accumulate, void *out, int32_t dtype, int64_t stride, void *stream);
 int zero_mx4_timeouts(uint32_t *count);
 
+/* ---- norm, linear layers and gated blocks in 16 bits, kept activations
+ *
+ * Calls of this part share these conventions.  `dtype` is the type of all
+ * matrices of a call that do not have one of their own.  An activation is one of
+ * enum zero_activation.  What a forward pass keeps for its backward pass goes
+ * into a matrix of `dtype`, or packed to 8 bits (zero_pack8) into a buffer of
+ * zero_pack8_bytes bytes, or nowhere (both NULL). */
+
+enum zero_activation {
+    ZERO_ACT_NONE = 0,
+    ZERO_ACT_RELU = 1,
+    ZERO_ACT_GELU = 2,      /* v times the normal distribution function of v */
+    ZERO_ACT_GELU_TANH = 3, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    ZERO_ACT_SILU = 4       /* v / (1 + exp(-v)) */
+};
+
+/* Rows kept in 8 bits: e4m3 elements (OCP FP8) under one power-of-two scale (E8M0)
+ * for every 32 consecutive elements of a row.  The scale 2^e is the smallest,
+ * not below 2^-127, with max|x| 2^-e <= 448; an element is x 2^-e rounded to the
+ * nearest e4m3 value, ties to the even code.  A block that holds an infinity or
+ * NaN gets the NaN scale.  A matrix of `rows` by `cols` takes
+ * zero_pack8_bytes(rows, cols) bytes (-1 on a bad argument), 16-byte aligned: rows of
+ * codes, each `cols` rounded up to a multiple of 32 long, then as many rows of
+ * scales (e + 127).  Codes past `cols` are zero.  zero_unpack8 gives the values,
+ * rounded once to `dtype`; one that the rounding would take past the
+ * type's largest finite value is that value. */
+int64_t zero_pack8_bytes(int64_t rows, int64_t cols);
+int zero_pack8(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride, void *q,
+               void *stream);
+int zero_unpack8(const void *q, int64_t rows, int64_t cols, void *out, int32_t dtype,
+                 int64_t stride, void *stream);
+
+/* The root-mean-square norm of rows, with the residual's addition:
+ *   sum[i] = x[i] + residual[i], rounded to `dtype`
+ *   rstd[i] = 1 / sqrt(mean of sum[i]^2 + eps),  y[i] = sum[i] * rstd[i] * weight
+ * residual may be NULL (sum is then x, and `sum` may be NULL too).  With a residual,
+ * sum may be NULL where only the norm is wanted; it may be x or residual itself.
+ * The norm goes to y (rounded once), to q (packed from fp32), or both;
+ * one of them is given.  rstd: fp32 [rows], NULL where no backward pass follows.
+ * Sums are in fp32.  eps >= 0. */
+int zero_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                  const void *weight, int32_t dtype, int64_t rows, int64_t dim, float eps,
+                  void *sum, int64_t sum_stride, void *y, int64_t y_stride, void *q, float *rstd,
+                  void *stream);
+
+/* Its gradient: with n = sum rstd,
+ *   dx[i] = dsum[i] + rstd[i] (weight dy[i] - n[i] mean(weight dy[i] n[i]))
+ *   dweight = sum over i of dy[i] n[i], or += that with accumulate != 0
+ * dx is the gradient of x and of residual; dsum, what reaches sum from its other
+ * uses, may be NULL (zero); dweight, of grad_dtype, may be NULL.  The sum
+ * over rows is in fp32, in an order that depends on the sizes alone.
+ * workspace: zero_rms_norm_grad_workspace(rows, dim) bytes (-1 on a bad
+ * argument), 16-byte aligned; not needed without dweight. */
+int64_t zero_rms_norm_grad_workspace(int64_t rows, int64_t dim);
+int zero_rms_norm_grad(const void *dy, int64_t dy_stride, const void *dsum, int64_t dsum_stride,
+                       const void *sum, int64_t sum_stride, const void *weight, const float *rstd,
+                       int32_t dtype, int64_t rows, int64_t dim, void *dx, int64_t dx_stride,
+                       void *dweight, int32_t grad_dtype, int32_t accumulate, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/* Products of 16-bit matrices (`dtype` ZERO_BF16 or ZERO_F16) with a linear layer's
+ * surroundings:
+ *   z = A B^T (+ A2 B2^T) + bias
+ *   out = activation(z) + residual, or out += activation(z) with accumulate != 0
+ * A is m by k, B n by k, out m by n of out_dtype (`dtype` or fp32).  a_cols != 0:
+ * `a` (and a2) lies as the transpose, k rows of m; b_cols likewise, k rows of n.
+ * a2 and b2 are both given or both NULL.  bias: [n] of `dtype`, or NULL;
+ * residual: m by n of out_dtype, or NULL (NULL with accumulate); it may be out itself.  z, before
+ * the activation, is kept in `kept` (`dtype`) or kept_q (packed from fp32).  A
+ * linear layer y = act(x W^T + b) and its gradients, dz being dy through the
+ * activation:
+ *   zero_matmul(x, 0, W, 0, m, n, k, b, act)   -> y
+ *   zero_matmul(dz, 0, W, 1, m, k, n)          -> dx
+ *   zero_matmul(dz, 1, x, 1, n, k, m)          -> dW
+ * Products are exact and summed in fp32 on the tensor cores; bias, activation and residual
+ * follow in fp32, and the result is rounded once.  workspace:
+ * zero_matmul_workspace(...) bytes of the same arguments (-1 on a bad one), 16-byte aligned; 0,
+ * and NULL will do, where the rows of a, b, a2 and b2 as they lie begin on 16-byte
+ * boundaries: others are copied there first.
+ *
+ * Waits are bounded as zero_mx4_matmul's are: a block whose wait runs out ends
+ * without storing its results, and zero_matmul_timeouts() reports it for
+ * zero_matmul and zero_gated as zero_mx4_timeouts() does for that call. */
+int64_t zero_matmul_workspace(const void *a, int32_t a_cols, int64_t a_stride, const void *b,
+                              int32_t b_cols, int64_t b_stride, const void *a2, int64_t a2_stride,
+                              const void *b2, int64_t b2_stride, int64_t m, int64_t n, int64_t k);
+int zero_matmul(const void *a, int32_t a_cols, int64_t a_stride, const void *b, int32_t b_cols,
+                int64_t b_stride, const void *a2, int64_t a2_stride, const void *b2,
+                int64_t b2_stride, int32_t dtype, int64_t m, int64_t n, int64_t k,
+                const void *bias, int32_t activation, const void *residual,
+                int64_t residual_stride, void *kept, int64_t kept_stride, void *kept_q, void *out,
+                int32_t out_dtype, int64_t out_stride, int32_t accumulate, void *workspace,
+                int64_t workspace_bytes, void *stream);
+
+/* A gated block's first half in one pass over x (m by k; w_gate and w_up n by k,
+ * h m by n, all 16-bit `dtype`):
+ *   gate = x w_gate^T,  up = x w_up^T,  h = activation(gate) * up
+ * gate and up are kept in `gate` and `up` (rows kept_stride apart), or packed
+ * in gate_q and up_q; both of either kind or none.  workspace as zero_matmul's, of
+ * zero_gated_workspace(...) bytes. */
+int64_t zero_gated_workspace(const void *x, int64_t x_stride, const void *w_gate,
+                             int64_t gate_stride, const void *w_up, int64_t up_stride, int64_t m,
+                             int64_t n, int64_t k);
+int zero_gated(const void *x, int64_t x_stride, const void *w_gate, int64_t gate_stride,
+               const void *w_up, int64_t up_stride, int32_t dtype, int64_t m, int64_t n, int64_t k,
+               int32_t activation, void *gate, void *up, int64_t kept_stride, void *gate_q,
+               void *up_q, void *h, int64_t h_stride, void *workspace, int64_t workspace_bytes,
+               void *stream);
+
+/* The gradient through an activation and of a bias:
+ *   dz = dy activation'(z),  dbias = sum over rows of dz (or += that)
+ * z is read from `kept` or kept_q (neither is needed for ZERO_ACT_NONE).  dz
+ * (`dtype`; it may be dy itself, with dy's stride) and dbias (bias_dtype) may be NULL, not both.  dbias sums dz
+ * before its rounding, in fp32, in an order that depends on the sizes alone.
+ * workspace: zero_activation_grad_workspace(rows, cols) bytes (-1 on a bad argument), 16-byte
+ * aligned; not needed without dbias. */
+int64_t zero_activation_grad_workspace(int64_t rows, int64_t cols);
+int zero_activation_grad(const void *dy, int64_t dy_stride, const void *kept, int64_t kept_stride,
+                         const void *kept_q, int32_t activation, int32_t dtype, int64_t rows,
+                         int64_t cols, void *dz, int64_t dz_stride, void *dbias,
+                         int32_t bias_dtype, int32_t accumulate, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/* The gradient through a gated block's product, from what zero_gated kept:
+ *   dgate = dh up activation'(gate),  dup = dh activation(gate)
+ * and, where h is not NULL, h = activation(gate) up again, for the gradient of the weight
+ * that it feeds.  The block's gradients follow by zero_matmul: dx from the pairs
+ * (dgate, w_gate) and (dup, w_up), the weights' from dgate and x, dup and x. */
+int zero_gated_grad(const void *dh, int64_t dh_stride, const void *gate, const void *up,
+                    int64_t kept_stride, const void *gate_q, const void *up_q, int32_t activation,
+                    int32_t dtype, int64_t rows, int64_t cols, void *dgate, void *dup,
+                    int64_t grad_stride, void *h, int64_t h_stride, void *stream);
+int zero_matmul_timeouts(uint32_t *count);
+
 #ifdef __cplusplus
 }
 #endif

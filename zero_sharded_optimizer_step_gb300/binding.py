@@ -19,6 +19,7 @@ ZERO_EINVAL, ZERO_ECUDA, ZERO_EALIGN, ZERO_ESTATE, ZERO_ETIMEOUT = -1, -2, -3, -
 ZERO_MAX_RANKS = 256
 ZERO_HYPER_BYTES = 128
 ZERO_GATHER_FAST, ZERO_GATHER_LEAN = 0, 1
+(ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_SILU) = range(5)
 
 
 class ZeroError(RuntimeError):
@@ -114,6 +115,28 @@ _SIGS = {
     "zero_mx4_matmul": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _f32, _i32, _vp, _i32, _i64,
                                        _vp]),
     "zero_mx4_timeouts": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
+    "zero_pack8_bytes": (_i64, [_i64, _i64]),
+    "zero_pack8": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp]),
+    "zero_unpack8": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i32, _i64, _vp]),
+    "zero_rms_norm": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _f32, _vp, _i64,
+                                     _vp, _i64, _vp, _vp, _vp]),
+    "zero_rms_norm_grad_workspace": (_i64, [_i64, _i64]),
+    "zero_rms_norm_grad": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i64,
+                                          _i64, _vp, _i64, _vp, _i32, _i32, _vp, _i64, _vp]),
+    "zero_matmul_workspace": (_i64, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i64, _vp, _i64, _i64,
+                                     _i64, _i64]),
+    "zero_matmul": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i64, _vp, _i64, _i32,
+                                   _i64, _i64, _i64, _vp, _i32, _vp, _i64, _vp, _i64, _vp, _vp,
+                                   _i32, _i64, _i32, _vp, _i64, _vp]),
+    "zero_gated_workspace": (_i64, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64]),
+    "zero_gated": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i32,
+                                  _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "zero_activation_grad_workspace": (_i64, [_i64, _i64]),
+    "zero_activation_grad": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i64, _i64,
+                                            _vp, _i64, _vp, _i32, _i32, _vp, _i64, _vp]),
+    "zero_gated_grad": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i64,
+                                       _i64, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "zero_matmul_timeouts": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_L, _name)
@@ -534,6 +557,10 @@ else:
     _calls.bind(*(ctypes.cast(getattr(_L, _name), _vp).value for _name in (
         "zero_embed", "zero_embed_grad", "zero_dropout", "zero_mx4_quantize",
         "zero_mx4_dequantize", "zero_mx4_matmul")))
+    _calls.bind_layers(*(ctypes.cast(getattr(_L, _name), _vp).value for _name in (
+        "zero_pack8", "zero_unpack8", "zero_rms_norm", "zero_rms_norm_grad",
+        "zero_matmul_workspace", "zero_matmul", "zero_gated_workspace", "zero_gated",
+        "zero_activation_grad", "zero_gated_grad")))
 
 
 def zero_embed(table, dtype: int, rows: int, dim: int, table_stride: int, tokens,
@@ -601,6 +628,120 @@ def zero_mx4_timeouts() -> int:
     its work has ended (0 when all is well)."""
     n = ctypes.c_uint32()
     rc = _L.zero_mx4_timeouts(ctypes.byref(n))
+    if rc != ZERO_ETIMEOUT:
+        _check(rc)
+    return int(n.value)
+
+
+def zero_pack8_bytes(rows: int, cols: int) -> int:
+    return _L.zero_pack8_bytes(rows, cols)
+
+
+def zero_pack8(x, dtype: int, rows: int, cols: int, stride: int, q, stream=None) -> None:
+    rc = _calls.pack8(x, dtype, rows, cols, stride, q,
+                      stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def zero_unpack8(q, rows: int, cols: int, out, dtype: int, stride: int, stream=None) -> None:
+    rc = _calls.unpack8(q, rows, cols, out, dtype, stride,
+                        stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def zero_rms_norm(x, x_stride: int, residual, residual_stride: int, weight, dtype: int,
+                  rows: int, dim: int, eps: float, sum, sum_stride: int, y, y_stride: int, q=None,
+                  rstd=None, stream=None) -> None:
+    rc = _calls.rms_norm(x, x_stride, residual, residual_stride, weight, dtype, rows, dim, eps,
+                         sum, sum_stride, y, y_stride, q, rstd,
+                         stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def zero_rms_norm_grad_workspace(rows: int, dim: int) -> int:
+    return _L.zero_rms_norm_grad_workspace(rows, dim)
+
+
+def zero_rms_norm_grad(dy, dy_stride: int, dsum, dsum_stride: int, sum, sum_stride: int, weight,
+                       rstd, dtype: int, rows: int, dim: int, dx, dx_stride: int, dweight,
+                       grad_dtype: int, accumulate: bool, workspace, workspace_bytes: int,
+                       stream=None) -> None:
+    rc = _calls.rms_norm_grad(dy, dy_stride, dsum, dsum_stride, sum, sum_stride, weight, rstd,
+                              dtype, rows, dim, dx, dx_stride, dweight, grad_dtype, accumulate,
+                              workspace, workspace_bytes,
+                              stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def zero_matmul_workspace(a, a_cols: bool, a_stride: int, b, b_cols: bool, b_stride: int, a2,
+                          a2_stride: int, b2, b2_stride: int, m: int, n: int, k: int) -> int:
+    return _calls.product_workspace(a, a_cols, a_stride, b, b_cols, b_stride, a2, a2_stride, b2,
+                                    b2_stride, m, n, k)
+
+
+def zero_matmul(a, a_cols: bool, a_stride: int, b, b_cols: bool, b_stride: int, a2,
+                a2_stride: int, b2, b2_stride: int, dtype: int, m: int, n: int, k: int, bias,
+                activation: int, residual, residual_stride: int, kept, kept_stride: int, kept_q,
+                out, out_dtype: int, out_stride: int, accumulate: bool, workspace=None,
+                workspace_bytes: int = 0, stream=None) -> None:
+    rc = _calls.product(a, a_cols, a_stride, b, b_cols, b_stride, a2, a2_stride, b2, b2_stride,
+                        dtype, m, n, k, bias, activation, residual, residual_stride, kept,
+                        kept_stride, kept_q, out, out_dtype, out_stride, accumulate, workspace,
+                        workspace_bytes, stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def zero_gated_workspace(x, x_stride: int, w_gate, gate_stride: int, w_up, up_stride: int, m: int,
+                         n: int, k: int) -> int:
+    return _calls.gated_workspace(x, x_stride, w_gate, gate_stride, w_up, up_stride, m, n, k)
+
+
+def zero_gated(x, x_stride: int, w_gate, gate_stride: int, w_up, up_stride: int, dtype: int,
+               m: int, n: int, k: int, activation: int, gate, up, kept_stride: int, gate_q, up_q,
+               h, h_stride: int, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    rc = _calls.gated(x, x_stride, w_gate, gate_stride, w_up, up_stride, dtype, m, n, k,
+                      activation, gate, up, kept_stride, gate_q, up_q, h, h_stride, workspace,
+                      workspace_bytes, stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def zero_activation_grad_workspace(rows: int, cols: int) -> int:
+    return _L.zero_activation_grad_workspace(rows, cols)
+
+
+def zero_activation_grad(dy, dy_stride: int, kept, kept_stride: int, kept_q, activation: int,
+                         dtype: int, rows: int, cols: int, dz, dz_stride: int, dbias,
+                         bias_dtype: int, accumulate: bool, workspace=None,
+                         workspace_bytes: int = 0, stream=None) -> None:
+    rc = _calls.activation_grad(dy, dy_stride, kept, kept_stride, kept_q, activation, dtype, rows,
+                                cols, dz, dz_stride, dbias, bias_dtype, accumulate, workspace,
+                                workspace_bytes,
+                                stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def zero_gated_grad(dh, dh_stride: int, gate, up, kept_stride: int, gate_q, up_q,
+                    activation: int, dtype: int, rows: int, cols: int, dgate, dup,
+                    grad_stride: int, h=None, h_stride: int = 0, stream=None) -> None:
+    rc = _calls.gated_grad(dh, dh_stride, gate, up, kept_stride, gate_q, up_q, activation, dtype,
+                           rows, cols, dgate, dup, grad_stride, h, h_stride,
+                           stream if type(stream) is int else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def zero_matmul_timeouts() -> int:
+    """Waits of zero_matmul's and zero_gated's kernels that ran out on the
+    current device, once all its work has ended (0 when all is well)."""
+    n = ctypes.c_uint32()
+    rc = _L.zero_matmul_timeouts(ctypes.byref(n))
     if rc != ZERO_ETIMEOUT:
         _check(rc)
     return int(n.value)

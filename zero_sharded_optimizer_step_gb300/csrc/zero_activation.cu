@@ -1,0 +1,368 @@
+// What a layer's backward pass does element by element: the gradients through
+// an activation and through a gated block's product, the bias's gradient, and
+// rows kept in 8 bits.
+//
+//   dz = dy act'(z), db = sum over rows of dz
+//   dg = dh u act'(g), du = dh act(g), h = act(g) u again for what it feeds
+//
+// z, g and u are read in the type or in 8 bits, straight from what the forward
+// pass kept.  Every matrix is read or written once, 256 columns of a row a warp.
+#include "zero_act.cuh"
+#include "zero_ops.h"
+#include "zero_pack8.cuh"
+#include "zero_rows.cuh"
+
+namespace zgb {
+namespace {
+
+constexpr int kWarps = kThreads / 32;
+
+// Values kept in the type or in 8 bits.
+template <int DT, bool VEC, bool PACKED> struct Kept {
+    rows::Eight<DT, VEC> e;
+    uint2 codes;
+    float up;
+
+    __device__ __forceinline__ void ask(const rows::In &m, const pack8::View &q, int64_t r,
+                                        int64_t c0, int64_t cols)
+    {
+        if constexpr (PACKED) {
+            const int64_t c = c0 + 8 * (threadIdx.x & 31);
+            codes = make_uint2(0, 0);
+            up = 0.0f;
+            if (c < q.wide) {
+                codes = *reinterpret_cast<const uint2 *>(q.codes + r * q.wide + c);
+                up = pack8::up(q.scales[r * (q.wide / pack8::kBlock) + c / pack8::kBlock]);
+            }
+        } else {
+            e.ask(m, r, c0, cols);
+        }
+    }
+
+    __device__ __forceinline__ void take(float (&f)[8]) const
+    {
+        if constexpr (PACKED) {
+            pack8::values4(codes.x, up, pack8::most<DT>(), f);
+            pack8::values4(codes.y, up, pack8::most<DT>(), f + 4);
+        } else {
+            e.take(f);
+        }
+    }
+};
+
+// ------------------------------------------------------- through an activation
+
+struct ActGrad {
+    rows::In dy, z;
+    pack8::View q;
+    int64_t n, cols;
+    int32_t act;
+    void *dz;
+    int64_t dz_stride;
+    float *parts;                                // [gridDim.y][cols], or null
+};
+
+// A block takes a strip of 256 columns and every gridDim.y-th eight of its rows.
+template <int DT, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(kThreads)
+activation_grad_kernel(const __grid_constant__ ActGrad a)
+{
+    __shared__ float joined[kWarps][256];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c0 = (int64_t)blockIdx.x * 256, step = (int64_t)gridDim.y * kWarps;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    constexpr int U = DT == F32 ? 1 : 2;         // rows on their way together
+    for (int64_t r0 = (int64_t)blockIdx.y * kWarps + warp; r0 < a.n; r0 += U * step) {
+        rows::Eight<DT, VEC> dye[U];
+        Kept<DT, VEC, PACKED> ze[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * step;
+            if (r >= a.n) break;
+            dye[u].ask(a.dy, r, c0, a.cols);
+            if (a.act != kActNone) ze[u].ask(a.z, a.q, r, c0, a.cols);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u * step;
+            if (r >= a.n) break;
+            float d[8];
+            dye[u].take(d);
+            if (a.act != kActNone) {
+                float z[8];
+                ze[u].take(z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float y, slope;
+                    act::both(z[e], a.act, y, slope);
+                    d[e] = __fmul_rn(d[e], slope);
+                }
+            }
+            if (a.dz) rows::put<DT, VEC>(a.dz, a.dz_stride, r, c0, a.cols, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] = __fadd_rn(sum[e], d[e]);
+        }
+    }
+    if (!a.parts) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) joined[warp][lane * 8 + e] = sum[e];
+    __syncthreads();
+    const int64_t c = c0 + threadIdx.x;
+    if (c < a.cols) {
+        float v = joined[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) v = __fadd_rn(v, joined[i][threadIdx.x]);
+        a.parts[(int64_t)blockIdx.y * a.cols + c] = v;
+    }
+}
+
+constexpr int64_t kBlocks = 152 * 8;             // about eight a SM
+
+int64_t act_parts(int64_t n, int64_t cols)
+{
+    const int64_t strips = (cols + 255) / 256, most = (n + kWarps - 1) / kWarps;
+    int64_t parts = (kBlocks + strips - 1) / strips;
+    parts = parts < most ? parts : most;
+    return parts < 1 ? 1 : parts < 65535 ? parts : 65535;
+}
+
+// ----------------------------------------------------- through a gated product
+
+struct GatedGrad {
+    rows::In dh, g, u;
+    pack8::View gq, uq;
+    int64_t n, cols, runs;
+    int32_t act;
+    void *dg, *du, *h;
+    int64_t grad_stride, h_stride;
+};
+
+template <int DT, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(kThreads)
+gated_grad_kernel(const __grid_constant__ GatedGrad a)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t r = w / a.runs, c0 = (w - r * a.runs) * 256;
+    if (r >= a.n) return;
+    rows::Eight<DT, VEC> dhe;
+    Kept<DT, VEC, PACKED> ge, ue;
+    dhe.ask(a.dh, r, c0, a.cols);
+    ge.ask(a.g, a.gq, r, c0, a.cols);
+    ue.ask(a.u, a.uq, r, c0, a.cols);
+    float dh[8], g[8], u[8], f[8], d[8];
+    dhe.take(dh);
+    ge.take(g);
+    ue.take(u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float slope;
+        act::both(g[e], a.act, f[e], slope);
+        d[e] = __fmul_rn(__fmul_rn(dh[e], u[e]), slope);
+        dh[e] = __fmul_rn(dh[e], f[e]);
+        f[e] = __fmul_rn(f[e], u[e]);
+    }
+    rows::put<DT, VEC>(a.dg, a.grad_stride, r, c0, a.cols, d);
+    rows::put<DT, VEC>(a.du, a.grad_stride, r, c0, a.cols, dh);
+    if (a.h) rows::put<DT, VEC>(a.h, a.h_stride, r, c0, a.cols, f);
+}
+
+// -------------------------------------------------------------- rows in 8 bits
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+pack8_kernel(const __grid_constant__ rows::In x, const __grid_constant__ pack8::View q,
+             int64_t n, int64_t cols, int64_t runs)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t r = w / runs, c0 = (w - r * runs) * 256;
+    if (r >= n) return;
+    rows::Eight<DT, VEC> e;
+    e.ask(x, r, c0, cols);
+    float f[8];
+    e.take(f);
+    const int64_t c = c0 + 8 * (threadIdx.x & 31);
+    pack8::put_eight(q, r, c, c < q.wide, f);
+}
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+unpack8_kernel(const __grid_constant__ pack8::View q, int64_t n, int64_t cols, int64_t runs,
+               void *out, int64_t stride)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t r = w / runs, c0 = (w - r * runs) * 256;
+    if (r >= n) return;
+    const int64_t c = c0 + 8 * (threadIdx.x & 31);
+    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (c < q.wide) pack8::get_eight<DT>(q, r, c, f);
+    rows::put<DT, VEC>(out, stride, r, c0, cols, f);
+}
+
+// ----------------------------------------------------------------- column sums
+
+// A block takes 32 columns, its warps every eighth of the partial rows, in order.
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+column_sums_kernel(const float *parts, int64_t n_parts, int64_t cols, void *out, int accumulate)
+{
+    __shared__ float joined[kWarps][32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float v = 0.0f;
+    if (c < cols) {
+        constexpr int U = 8;
+        for (int64_t p = warp; p < n_parts; p += U * kWarps) {
+            float f[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                f[u] = p + u * kWarps < n_parts ? parts[(p + u * kWarps) * cols + c] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) v = __fadd_rn(v, f[u]);
+        }
+    }
+    joined[warp][lane] = v;
+    __syncthreads();
+    if (warp || c >= cols) return;
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) v = __fadd_rn(v, joined[i][lane]);
+    if (accumulate) v = __fadd_rn(elems::load1<DT>(out, c), v);
+    elems::store1<DT>(out, c, v);
+}
+
+template <class F> cudaError_t by_type(int32_t dt, F f)
+{
+    return dt == F32 ? f(std::integral_constant<int, F32>{})
+           : dt == BF16 ? f(std::integral_constant<int, BF16>{})
+                        : f(std::integral_constant<int, F16>{});
+}
+
+// Blocks of eight warps for so many runs of 256 columns; 0 where there are too many.
+unsigned run_blocks(int64_t n, int64_t runs)
+{
+    const int64_t blocks = (n * runs + kWarps - 1) / kWarps;
+    return blocks > 0x7fffffff ? 0 : (unsigned)blocks;
+}
+
+}  // namespace
+
+cudaError_t launch_column_sums(int32_t dt, const float *parts, int64_t n_parts, int64_t cols,
+                               void *out, bool accumulate, cudaStream_t s)
+{
+    return by_type(dt, [&](auto t) {
+        return launch_dependent(column_sums_kernel<decltype(t)::value>,
+                                dim3((unsigned)((cols + 31) / 32)), dim3(kThreads), 0, s, parts,
+                                n_parts, cols, out, accumulate ? 1 : 0);
+    });
+}
+
+int64_t activation_grad_workspace(int64_t rows, int64_t cols)
+{
+    return act_parts(rows, cols) * cols * 4;
+}
+
+cudaError_t launch_activation_grad(int32_t dt, int32_t bdt, const ActGradArgs &a, float *workspace,
+                                   cudaStream_t s)
+{
+    if (a.cols <= 0) return cudaSuccess;
+    const int64_t parts = act_parts(a.rows, a.cols);
+    if (a.rows > 0) {
+        ActGrad g = {rows::in(a.dy, a.rows, a.cols, a.dy_stride, dt),
+                     rows::in(a.kept, a.rows, a.cols, a.kept_stride, dt),
+                     pack8::view(a.kept_q, a.rows, a.cols), a.rows, a.cols, a.act, a.dz,
+                     a.dz_stride, a.dbias ? workspace : nullptr};
+        const bool vec = rows_aligned(a.dy, a.dy_stride, dt, a.cols) &&
+                         (!a.kept || rows_aligned(a.kept, a.kept_stride, dt, a.cols)) &&
+                         (!a.dz || rows_aligned(a.dz, a.dz_stride, dt, a.cols));
+        const dim3 grid((unsigned)((a.cols + 255) / 256), (unsigned)parts);
+        const cudaError_t e = by_type(dt, [&](auto t) {
+            constexpr int DT = decltype(t)::value;
+            auto k = a.kept_q ? (vec ? activation_grad_kernel<DT, true, true>
+                                     : activation_grad_kernel<DT, false, true>)
+                              : (vec ? activation_grad_kernel<DT, true, false>
+                                     : activation_grad_kernel<DT, false, false>);
+            return launch_dependent(k, grid, dim3(kThreads), 0, s, g);
+        });
+        if (e != cudaSuccess) return e;
+    }
+    if (!a.dbias) return cudaSuccess;
+    return launch_column_sums(bdt, workspace, a.rows > 0 ? parts : 0, a.cols, a.dbias,
+                              a.accumulate, s);
+}
+
+cudaError_t launch_gated_grad(int32_t dt, const GatedGradArgs &a, cudaStream_t s)
+{
+    if (a.rows <= 0 || a.cols <= 0) return cudaSuccess;
+    const int64_t runs = (a.cols + 255) / 256;
+    GatedGrad g = {rows::in(a.dh, a.rows, a.cols, a.dh_stride, dt),
+                   rows::in(a.gate, a.rows, a.cols, a.kept_stride, dt),
+                   rows::in(a.up, a.rows, a.cols, a.kept_stride, dt),
+                   pack8::view(a.gate_q, a.rows, a.cols), pack8::view(a.up_q, a.rows, a.cols),
+                   a.rows, a.cols, runs, a.act, a.dgate, a.dup, a.h, a.grad_stride, a.h_stride};
+    const bool vec = rows_aligned(a.dh, a.dh_stride, dt, a.cols) &&
+                     (!a.gate || (rows_aligned(a.gate, a.kept_stride, dt, a.cols) &&
+                                  rows_aligned(a.up, a.kept_stride, dt, a.cols))) &&
+                     rows_aligned(a.dgate, a.grad_stride, dt, a.cols) &&
+                     rows_aligned(a.dup, a.grad_stride, dt, a.cols) &&
+                     (!a.h || rows_aligned(a.h, a.h_stride, dt, a.cols));
+    const unsigned blocks = run_blocks(a.rows, runs);
+    if (!blocks) return cudaErrorInvalidValue;
+    return by_type(dt, [&](auto t) {
+        constexpr int DT = decltype(t)::value;
+        auto k = a.gate_q ? (vec ? gated_grad_kernel<DT, true, true>
+                                 : gated_grad_kernel<DT, false, true>)
+                          : (vec ? gated_grad_kernel<DT, true, false>
+                                 : gated_grad_kernel<DT, false, false>);
+        return launch_dependent(k, dim3(blocks), dim3(kThreads), 0, s, g);
+    });
+}
+
+int64_t pack8_bytes(int64_t rows, int64_t cols)
+{
+    return rows * (pack8::pitch(cols) + pack8::pitch(cols) / pack8::kBlock);
+}
+
+cudaError_t launch_pack8(int32_t dt, const void *x, int64_t rows, int64_t cols, int64_t stride,
+                         unsigned char *q, cudaStream_t s)
+{
+    if (rows <= 0 || cols <= 0) return cudaSuccess;
+    const int64_t runs = (cols + 255) / 256;
+    const unsigned blocks = run_blocks(rows, runs);
+    if (!blocks) return cudaErrorInvalidValue;
+    const rows::In in = rows::in(x, rows, cols, stride, dt);
+    const bool vec = rows_aligned(x, stride, dt, cols);
+    return by_type(dt, [&](auto t) {
+        constexpr int DT = decltype(t)::value;
+        return launch_dependent(vec ? pack8_kernel<DT, true> : pack8_kernel<DT, false>,
+                                dim3(blocks), dim3(kThreads), 0, s, in,
+                                pack8::view(q, rows, cols), rows, cols, runs);
+    });
+}
+
+cudaError_t launch_unpack8(int32_t dt, const unsigned char *q, int64_t rows, int64_t cols,
+                           void *out, int64_t stride, cudaStream_t s)
+{
+    if (rows <= 0 || cols <= 0) return cudaSuccess;
+    const int64_t runs = (cols + 255) / 256;
+    const unsigned blocks = run_blocks(rows, runs);
+    if (!blocks) return cudaErrorInvalidValue;
+    const bool vec = rows_aligned(out, stride, dt, cols);
+    return by_type(dt, [&](auto t) {
+        constexpr int DT = decltype(t)::value;
+        return launch_dependent(vec ? unpack8_kernel<DT, true> : unpack8_kernel<DT, false>,
+                                dim3(blocks), dim3(kThreads), 0, s,
+                                pack8::view(const_cast<unsigned char *>(q), rows, cols), rows,
+                                cols, runs, out, stride);
+    });
+}
+
+}  // namespace zgb

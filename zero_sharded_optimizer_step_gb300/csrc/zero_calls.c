@@ -12,6 +12,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "zero.h"
 
@@ -237,11 +238,180 @@ static PyObject *bind(PyObject *self, PyObject *const *at, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
+/* ---- the norm, products, gated blocks and kept activations
+ *
+ * A call's signature is a letter an argument: p a pointer, i and l whole numbers of
+ * 32 and 64 bits, t a truth value (an int), f a float. */
+static struct {
+    __typeof__(&zero_pack8) pack8;
+    __typeof__(&zero_unpack8) unpack8;
+    __typeof__(&zero_rms_norm) rms_norm;
+    __typeof__(&zero_rms_norm_grad) rms_norm_grad;
+    __typeof__(&zero_matmul_workspace) product_workspace;
+    __typeof__(&zero_matmul) product;
+    __typeof__(&zero_gated_workspace) gated_workspace;
+    __typeof__(&zero_gated) gated;
+    __typeof__(&zero_activation_grad) activation_grad;
+    __typeof__(&zero_gated_grad) gated_grad;
+} layers;
+
+enum { LAYERS = 10, MOST = 28 };
+
+typedef union {
+    void *p;
+    int32_t i;
+    int64_t l;
+    float f;
+} slot;
+
+static int take(args_t *a, PyObject *const *at, Py_ssize_t n, const char *types, void *fn, slot *v)
+{
+    if (!begin(a, at, n, (Py_ssize_t)strlen(types), fn)) return 0;
+    for (int i = 0; types[i]; ++i)
+        switch (types[i]) {
+        case 'p': v[i].p = pointer(a, i); break;
+        case 'i': v[i].i = small(a, i); break;
+        case 'l': v[i].l = whole(a, i); break;
+        case 't': v[i].i = truth(a, i); break;
+        default: v[i].f = (float)real(a, i);
+        }
+    return !a->bad;
+}
+
+/* Host arithmetic alone: the GIL is kept. */
+#define SIZE(expression) return PyLong_FromLongLong(expression)
+
+static PyObject *pack8(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "pilllpp", (void *)layers.pack8, v)) return NULL;
+    CALL(layers.pack8(v[0].p, v[1].i, v[2].l, v[3].l, v[4].l, v[5].p, v[6].p));
+}
+
+static PyObject *unpack8(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "pllpilp", (void *)layers.unpack8, v)) return NULL;
+    CALL(layers.unpack8(v[0].p, v[1].l, v[2].l, v[3].p, v[4].i, v[5].l, v[6].p));
+}
+
+static PyObject *rms_norm(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "plplpillfplplppp", (void *)layers.rms_norm, v)) return NULL;
+    CALL(layers.rms_norm(v[0].p, v[1].l, v[2].p, v[3].l, v[4].p, v[5].i, v[6].l, v[7].l, v[8].f,
+                         v[9].p, v[10].l, v[11].p, v[12].l, v[13].p, v[14].p, v[15].p));
+}
+
+static PyObject *rms_norm_grad(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "plplplppillplpitplp", (void *)layers.rms_norm_grad, v)) return NULL;
+    CALL(layers.rms_norm_grad(v[0].p, v[1].l, v[2].p, v[3].l, v[4].p, v[5].l, v[6].p, v[7].p,
+                              v[8].i, v[9].l, v[10].l, v[11].p, v[12].l, v[13].p, v[14].i,
+                              v[15].i, v[16].p, v[17].l, v[18].p));
+}
+
+static PyObject *product_workspace(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "ptlptlplpllll", (void *)layers.product_workspace, v)) return NULL;
+    SIZE(layers.product_workspace(v[0].p, v[1].i, v[2].l, v[3].p, v[4].i, v[5].l, v[6].p, v[7].l,
+                                  v[8].p, v[9].l, v[10].l, v[11].l, v[12].l));
+}
+
+static PyObject *product(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "ptlptlplplilllpiplplppiltplp", (void *)layers.product, v)) return NULL;
+    CALL(layers.product(v[0].p, v[1].i, v[2].l, v[3].p, v[4].i, v[5].l, v[6].p, v[7].l, v[8].p,
+                        v[9].l, v[10].i, v[11].l, v[12].l, v[13].l, v[14].p, v[15].i, v[16].p,
+                        v[17].l, v[18].p, v[19].l, v[20].p, v[21].p, v[22].i, v[23].l, v[24].i,
+                        v[25].p, v[26].l, v[27].p));
+}
+
+static PyObject *gated_workspace(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "plplpllll", (void *)layers.gated_workspace, v)) return NULL;
+    SIZE(layers.gated_workspace(v[0].p, v[1].l, v[2].p, v[3].l, v[4].p, v[5].l, v[6].l, v[7].l,
+                                v[8].l));
+}
+
+static PyObject *gated(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "plplplilllipplppplplp", (void *)layers.gated, v)) return NULL;
+    CALL(layers.gated(v[0].p, v[1].l, v[2].p, v[3].l, v[4].p, v[5].l, v[6].i, v[7].l, v[8].l,
+                      v[9].l, v[10].i, v[11].p, v[12].p, v[13].l, v[14].p, v[15].p, v[16].p,
+                      v[17].l, v[18].p, v[19].l, v[20].p));
+}
+
+static PyObject *activation_grad(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "plplpiillplpitplp", (void *)layers.activation_grad, v)) return NULL;
+    CALL(layers.activation_grad(v[0].p, v[1].l, v[2].p, v[3].l, v[4].p, v[5].i, v[6].i, v[7].l,
+                                v[8].l, v[9].p, v[10].l, v[11].p, v[12].i, v[13].i, v[14].p,
+                                v[15].l, v[16].p));
+}
+
+static PyObject *gated_grad(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "plpplppiillpplplp", (void *)layers.gated_grad, v)) return NULL;
+    CALL(layers.gated_grad(v[0].p, v[1].l, v[2].p, v[3].p, v[4].l, v[5].p, v[6].p, v[7].i,
+                           v[8].i, v[9].l, v[10].l, v[11].p, v[12].p, v[13].l, v[14].p, v[15].l,
+                           v[16].p));
+}
+
+/* bind_layers(): the addresses of the functions above, in their order. */
+static PyObject *bind_layers(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    void *p[LAYERS];
+    if (!begin(&a, at, n, LAYERS, (void *)&layers)) return NULL;
+    for (int i = 0; i < LAYERS; ++i) p[i] = pointer(&a, i);
+    if (a.bad) return NULL;
+    layers.pack8 = (__typeof__(layers.pack8))p[0];
+    layers.unpack8 = (__typeof__(layers.unpack8))p[1];
+    layers.rms_norm = (__typeof__(layers.rms_norm))p[2];
+    layers.rms_norm_grad = (__typeof__(layers.rms_norm_grad))p[3];
+    layers.product_workspace = (__typeof__(layers.product_workspace))p[4];
+    layers.product = (__typeof__(layers.product))p[5];
+    layers.gated_workspace = (__typeof__(layers.gated_workspace))p[6];
+    layers.gated = (__typeof__(layers.gated))p[7];
+    layers.activation_grad = (__typeof__(layers.activation_grad))p[8];
+    layers.gated_grad = (__typeof__(layers.gated_grad))p[9];
+    Py_RETURN_NONE;
+}
+
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 
 static PyMethodDef methods[] = {METHOD(bind),     METHOD(embed),      METHOD(embed_grad),
                                 METHOD(dropout),  METHOD(quantize),   METHOD(dequantize),
-                                METHOD(matmul),   {NULL, NULL, 0, NULL}};
+                                METHOD(matmul),   METHOD(bind_layers),
+                                METHOD(pack8),
+                                METHOD(unpack8),
+                                METHOD(rms_norm),
+                                METHOD(rms_norm_grad),
+                                METHOD(product_workspace),
+                                METHOD(product),
+                                METHOD(gated_workspace),
+                                METHOD(gated),
+                                METHOD(activation_grad),
+                                METHOD(gated_grad),
+                                {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};

@@ -1,0 +1,979 @@
+// Products of 16-bit matrices on the tensor cores with what surrounds them in a
+// linear layer:
+//
+//   z[i, j] = sum over c of A[i, c] B[j, c] (+ of A2[i, c] B2[j, c]) + bias[j]
+//   out[i, j] = act(z[i, j]) (+ residual[i, j])
+//
+// and the gated block's first half, out = act(A B^T) * (A B2^T).  Either
+// operand may lie as its transpose: both orders are ones in which the tensor
+// cores read shared memory, so a layer's three products (y = x W^T, dx = dz W,
+// dW = dz^T x) need no transposed copy.  Products of two 16-bit numbers are exact in the
+// fp32 sums; bias, activation, residual follow in fp32, and the
+// result is rounded once.  What the backward pass needs of z is stored beside it,
+// rounded to the type or packed to 8 bits from the fp32 sum.
+//
+// Tensor copies (TMA) bring blocks of 64 columns c into shared memory, 128-byte lines
+// swizzled; what lies outside a matrix arrives as zeros.  They need 16-byte
+// boundaries: an operand whose rows are not on them is first copied to a
+// workspace whose rows are.
+#include <atomic>
+
+#include <cuda.h>
+
+#include "zero_act.cuh"
+#include "zero_elems.cuh"
+#include "zero_ops.h"
+#include "zero_pack8.cuh"
+#include "zero_tensor.cuh"
+
+namespace zgb {
+namespace {
+
+__device__ unsigned int g_matmul_timeouts;
+
+constexpr int kDepth = 64;                       // columns c of a stage: 128 bytes
+constexpr int kLine = 128;
+constexpr int kHalf = 128 * kLine;               // 128 rows of an operand in a stage
+
+// An operand's stage as the tensor cores read it.  Rows of c lie as lines of 128
+// bytes (64 c), eight lines a swizzle atom; the transpose as chunks of 64
+// rows of the operand, each 64 lines (one c each) of 128 bytes.
+struct Layout {
+    uint64_t desc;                               // without the address
+    uint32_t step;                               // 16 c further, in units of 16 bytes
+};
+
+__device__ __forceinline__ Layout layout_of(int32_t cols)
+{
+    const uint64_t fixed = ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    return cols ? Layout{fixed | ((uint64_t)(kDepth * kLine >> 4) << 16), 16 * kLine >> 4}
+                : Layout{fixed | (1ull << 16), 32 >> 4};
+}
+
+__device__ __forceinline__ uint64_t at(const Layout &l, uint32_t addr)
+{
+    return l.desc | ((addr & 0x3ffffu) >> 4);
+}
+
+// fp32 sums of 16-bit products, M lanes by N columns.
+template <int DT> __device__ __forceinline__ uint32_t shape_desc(int32_t a_cols, int32_t b_cols)
+{
+    constexpr uint32_t t = DT == BF16 ? 1u : 0u;
+    return (1u << 4) | (t << 7) | (t << 10) | ((uint32_t)(a_cols != 0) << 15) |
+           ((uint32_t)(b_cols != 0) << 16);
+}
+
+__device__ __forceinline__ void mma1(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                     uint32_t add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a),
+                 "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                     uint32_t add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a),
+                 "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+
+// A box of `map` from (x, y) into this block's shared memory, signalled here.
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, int32_t x,
+                                         int32_t y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile"
+                 ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+// The same, signalled at `bar` of the pair's first block.
+__device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap *map, int32_t x,
+                                            int32_t y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+                 ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+// ---------------------------------------------------------------- the results
+
+// Column j of row i, by a whole warp with 32 consecutive columns from a multiple
+// of 32 on; `in`: the column is one of the result's.  Every pointer that is
+// given is written or read by whole runs of the warp.
+template <int DT, int ODT, bool GATED>
+__device__ __forceinline__ void finish_lane(const ProductArgs &a, int64_t i, int64_t j, bool in,
+                                            float acc, float acc2, float bias)
+{
+    const float z = __fadd_rn(acc, bias);
+    if (a.kept && in) elems::store1<DT>(a.kept, i * a.kept_stride + j, z);
+    if (a.kept_q)
+        pack8::put_lane(pack8::view(a.kept_q, a.m, a.n), i, j - (threadIdx.x & 31), in ? z : 0.0f);
+    float y = act::value(z, a.act);
+    if constexpr (GATED) {
+        if (a.kept2 && in) elems::store1<DT>(a.kept2, i * a.kept_stride + j, acc2);
+        if (a.kept2_q)
+            pack8::put_lane(pack8::view(a.kept2_q, a.m, a.n), i, j - (threadIdx.x & 31),
+                            in ? acc2 : 0.0f);
+        y = __fmul_rn(y, acc2);
+    }
+    if (in) {
+        if (a.residual) y = __fadd_rn(y, elems::load1<ODT>(a.residual, i * a.residual_stride + j));
+        elems::store1<ODT>(a.out, i * a.stride + j, y);
+    }
+}
+
+// 16 columns of a row on 32-byte boundaries.
+template <int DT> __device__ __forceinline__ void load_run(const void *p, int64_t at, float *f)
+{
+    elems::Raw<DT> r;
+    float h[8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        r.load(p, at + 8 * u);
+        r.get(h);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[8 * u + e] = h[e];
+    }
+}
+
+template <int DT> __device__ __forceinline__ void store_run(void *p, int64_t at, const float *f)
+{
+    using T = typename elems::El<DT>::T;
+#pragma unroll
+    for (int u = 0; u < (DT == F32 ? 2 : 1); ++u) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (DT == F32) w[e] = __float_as_uint(f[8 * u + e]);
+            else w[e] = elems::narrow2<DT>(f[2 * e], f[2 * e + 1]);
+        }
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(
+                         static_cast<T *>(p) + at + 8 * u),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                     "r"(w[7]) : "memory");
+    }
+}
+
+// 32 columns of row i from j on, all the result's, by one thread.  z holds the
+// sums, z2 the second ones of a gated block.
+template <int DT, int ODT, bool GATED>
+__device__ __forceinline__ void finish_run(const ProductArgs &a, int64_t i, int64_t j,
+                                           float (&z)[32], float (&z2)[32])
+{
+    if (a.bias) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float b[16];
+            load_run<DT>(a.bias, j + 16 * h, b);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z[16 * h + e] = __fadd_rn(z[16 * h + e], b[e]);
+        }
+    }
+    if (a.kept) {
+        store_run<DT>(a.kept, i * a.kept_stride + j, z);
+        store_run<DT>(a.kept, i * a.kept_stride + j + 16, z + 16);
+        if constexpr (GATED) {
+            store_run<DT>(a.kept2, i * a.kept_stride + j, z2);
+            store_run<DT>(a.kept2, i * a.kept_stride + j + 16, z2 + 16);
+        }
+    }
+    if (a.kept_q) {
+        pack8::put_thread(pack8::view(a.kept_q, a.m, a.n), i, j, z);
+        if constexpr (GATED) pack8::put_thread(pack8::view(a.kept2_q, a.m, a.n), i, j, z2);
+    }
+    // one switch for the run: the activation's code is laid out once for each kind
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) z[e] = f(z[e]);
+    };
+    switch (a.act) {
+    case kActRelu: all([](float v) { return act::value(v, kActRelu); }); break;
+    case kActGelu: all([](float v) { return act::value(v, kActGelu); }); break;
+    case kActGeluTanh: all([](float v) { return act::value(v, kActGeluTanh); }); break;
+    case kActSilu: all([](float v) { return act::value(v, kActSilu); }); break;
+    default: break;
+    }
+    if constexpr (GATED) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) z[e] = __fmul_rn(z[e], z2[e]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (a.residual) {
+            float r[16];
+            load_run<ODT>(a.residual, i * a.residual_stride + j + 16 * h, r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z[16 * h + e] = __fadd_rn(z[16 * h + e], r[e]);
+        }
+        store_run<ODT>(a.out, i * a.stride + j + 16 * h, z + 16 * h);
+    }
+}
+
+// ------------------------------------------------- few rows, or few tiles
+//
+// The accumulator's 128 lanes are 128 rows of B (128 consecutive columns of
+// the result, so that a warp's stores are contiguous), its columns NT rows of
+// A: with few tokens the tile is as narrow as they are, and the product reads
+// the weights once.  A gated block has two accumulators, of the same lanes,
+// side by side.  One warp issues the copies, one the products, four write.
+// With fewer tiles than SMs the columns c are split over a cluster of up to 8
+// blocks, whose partial sums join through distributed shared memory in the blocks'
+// order.
+template <int NT, bool GATED, bool ACOLS> struct Tile {
+    static_assert(!ACOLS || NT >= 64, "a transposed chunk has 64 rows");
+    static constexpr int kWeights = GATED ? 2 : 1;
+    static constexpr int kStage = kWeights * kHalf + NT * kLine;
+    static constexpr int kCols = kWeights * NT;
+    static constexpr int kTmem = kCols <= 32 ? 32 : kCols;
+    static constexpr int kMost = (kSmemBlock - 1024) / kStage;
+    static constexpr int kStages = kMost < 8 ? kMost : 8;
+    static constexpr int kPart = kWeights * NT * 128 * 4;   // a split's partial sums
+    // A block's share of an SM's shared memory is at least its share of the tensor
+    // memory, so that no block waits for tensor memory that another one
+    // holds: two that wait for their cluster peers so would wait forever.
+    static constexpr int smem(int stages)
+    {
+        const int ring = stages * kStage > kPart ? stages * kStage : kPart;
+        const int share = (kSmemSm / (512 / kTmem) + 127) / 128 * 128;
+        return ring + 1024 > share ? ring + 1024 : share;
+    }
+    static_assert(kStage % 1024 == 0, "stages start on the swizzle's boundary");
+};
+
+constexpr int kOneThreads = 192;
+
+struct OneArgs {
+    CUtensorMap a, b, b2, a2;
+    int64_t kt1, kt, tiles_n;            // stages of the first pair of operands, of both
+    int32_t splits, stages;
+};
+
+__device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(addr, rank))
+                 : "memory");
+    return v;
+}
+
+// Adds up the SP splits' partial sums, [column][lane] in every block's shared
+// memory, in the blocks' order, and writes them: blocks and warps take 32 lanes
+// of a column each in turn.
+template <int DT, int ODT, bool GATED, int NT, int SP>
+__device__ __forceinline__ void join(const ProductArgs &a, const float *part, uint32_t rank,
+                                     int64_t i0, int64_t j0, int cols)
+{
+    constexpr int U = SP == 1 ? 4 : SP < 8 ? 2 : 1;    // runs on their way together
+    constexpr int kSums = GATED ? 2 : 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (a whole block's warp finds its own lanes' sums)
+#pragma unroll 1
+    for (int first = (int)rank * 4 + warp; first < cols * 4; first += U * SP * 4) {
+        float v[U][kSums][SP];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int run = first + u * SP * 4;
+            if (run >= cols * 4) break;
+#pragma unroll
+            for (int g = 0; g < kSums; ++g)
+#pragma unroll
+                for (int q = 0; q < SP; ++q)
+                    v[u][g][q] = SP == 1 ? part[g * NT * 128 + run * 32 + lane]
+                                         : load_peer(saddr(part + g * NT * 128 + run * 32 + lane),
+                                                     q);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int run = first + u * SP * 4;
+            if (run >= cols * 4) break;
+            float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int g = 0; g < kSums; ++g) {
+                sum[g] = v[u][g][0];
+#pragma unroll
+                for (int q = 1; q < SP; ++q) sum[g] = __fadd_rn(sum[g], v[u][g][q]);
+            }
+            const int64_t j = j0 + (run & 3) * 32 + lane;
+            if (j - lane >= a.n) continue;
+            const float bias = a.bias && j < a.n ? elems::load1<DT>(a.bias, j) : 0.0f;
+            finish_lane<DT, ODT, GATED>(a, i0 + (run >> 2), j, j < a.n, sum[0], sum[1], bias);
+        }
+    }
+}
+
+template <int DT, int ODT, bool GATED, int NT, bool ACOLS>
+__global__ void __launch_bounds__(kOneThreads, 2)
+matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ OneArgs g)
+{
+    using Tl = Tile<NT, GATED, ACOLS>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * Tl::kStages + 1];
+    __shared__ uint32_t tmem_base, failed;
+    const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = g.splits > 1 ? cluster_rank() : 0;
+    const int64_t tile = blockIdx.x / g.splits;
+    const int64_t tn = tile % g.tiles_n, tm = tile / g.tiles_n;
+    const int64_t k0 = g.kt * rank / g.splits, k1 = g.kt * (rank + 1) / g.splits;
+    const int rounds = (int)(k1 - k0);
+    const uint32_t done_bar = saddr(&bars[2 * Tl::kStages]);
+    auto full = [&](int s) { return saddr(&bars[s]); };
+    auto empty = [&](int s) { return saddr(&bars[Tl::kStages + s]); };
+
+    bool ok = true;
+    if (warp == 4) {                                         // the copies
+        const bool one = elect_one();
+        if (one) {
+            for (int s = 0; s < Tl::kStages; ++s) {
+                bar_init(full(s), 1);
+                bar_init(empty(s), 1);
+            }
+            bar_init(done_bar, 1);
+            failed = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+        pdl_wait();
+        const int32_t jx = (int32_t)(tn * 128), ix = (int32_t)(tm * NT);
+        auto weights = [&](uint32_t to, const CUtensorMap *map, int32_t c, uint32_t bar) {
+            if (a.b_cols) {
+                box_load(to, map, jx, c, bar);
+                box_load(to + kHalf / 2, map, jx + 64, c, bar);
+            } else {
+                box_load(to, map, c, jx, bar);
+            }
+        };
+        auto load = [&](int it, int s) {
+            const int64_t kt = k0 + it;
+            const bool second = kt >= g.kt1;
+            const int32_t c = (int32_t)((second ? kt - g.kt1 : kt) * kDepth);
+            const uint32_t st = ring + s * Tl::kStage, tok = st + Tl::kWeights * kHalf;
+            bar_expect(full(s), Tl::kStage);
+            weights(st, !GATED && second ? &g.b2 : &g.b, c, full(s));
+            if constexpr (GATED) weights(st + kHalf, &g.b2, c, full(s));
+            const CUtensorMap *map = second ? &g.a2 : &g.a;
+            if constexpr (ACOLS) {
+#pragma unroll
+                for (int h = 0; h < NT / 64; ++h)
+                    box_load(tok + h * (kHalf / 2), map, ix + 64 * h, c, full(s));
+            } else {
+                box_load(tok, map, c, ix, full(s));
+            }
+        };
+        // the first stages' copies need not wait for the other warps
+        const int ahead = rounds < g.stages ? rounds : g.stages;
+        for (int it = 0; it < ahead; ++it)
+            if (one) load(it, it);
+        __syncthreads();
+        int s = 0;
+        uint32_t phase = 0;
+        for (int it = ahead; it < rounds; ++it) {
+            ok = bar_wait(empty(s), phase);
+            if (!ok) break;
+            if (one) load(it, s);
+            __syncwarp();
+            if (++s == g.stages) s = 0, phase ^= 1;
+        }
+    } else if (warp == 5) {                                  // the products
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         saddr(&tmem_base)), "r"((uint32_t)Tl::kTmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncthreads();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const bool one = elect_one();
+        const uint32_t tmem = tmem_base;
+        const Layout lb = layout_of(a.b_cols), la = layout_of(ACOLS);
+        const uint32_t desc = shape_desc<DT>(a.b_cols, ACOLS) | ((uint32_t)(NT >> 3) << 17) |
+                              ((128u >> 4) << 24);
+        int s = 0;
+        uint32_t phase = 0;
+        for (int it = 0; it < rounds; ++it) {
+            ok = bar_wait(full(s), phase);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (one) {
+                const uint32_t st = ring + s * Tl::kStage;
+                const uint64_t db = at(lb, st), da = at(la, st + Tl::kWeights * kHalf);
+                // columns past k are zeros: their products are left out
+                const int64_t kt = k0 + it;
+                const int64_t left = a.k - (kt >= g.kt1 ? kt - g.kt1 : kt) * kDepth;
+                const int steps = left >= kDepth ? 4 : (int)((left + 15) / 16);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q >= steps) break;
+                    mma1(tmem, db + q * lb.step, da + q * la.step, desc, it > 0 || q > 0);
+                    if constexpr (GATED)
+                        mma1(tmem + NT, db + (kHalf >> 4) + q * lb.step, da + q * la.step, desc,
+                             it > 0 || q > 0);
+                }
+                commit(empty(s));
+            }
+            __syncwarp();
+            if (++s == g.stages) s = 0, phase ^= 1;
+        }
+        if (ok && one) commit(done_bar);
+        __syncwarp();
+    } else {                                                 // the results
+        pdl_wait();
+        __syncthreads();
+        pdl_launch_dependents();
+        ok = bar_wait(done_bar, 0);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    if (!ok) {
+        if (lane == 0) atomicAdd(&g_matmul_timeouts, 1u);
+        failed = 1;
+    }
+    const int64_t i0 = tm * NT;
+    const int cols = (int)(a.m - i0 < NT ? a.m - i0 : NT);
+    // The sums go where the stages were, [column][lane]: all copies have landed and
+    // all products have read them.  A split's blocks read each other's from there;
+    // a whole block's warps read their own, so that one piece of code, which is not laid
+    // out once for each register, writes the result.
+    float *part = reinterpret_cast<float *>(dyn + (ring - saddr(dyn)));
+    if (warp < 4 && ok) {
+        const uint32_t lanes = tmem_base + ((uint32_t)(warp * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < Tl::kWeights * NT; c += 16) {
+            if ((c & (NT - 1)) >= cols) continue;
+            float v[16];
+            load16(lanes + c, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                part[(c + e) * 128 + warp * 32 + lane] = g.kt == 0 ? 0.0f : v[e];  // empty sums
+        }
+    }
+    if (g.splits > 1) cluster_sync();
+    __syncwarp();
+    if (warp < 4 && ok) {
+        if (g.splits == 1) join<DT, ODT, GATED, NT, 1>(a, part, rank, i0, tn * 128, cols);
+        else if (g.splits == 2) join<DT, ODT, GATED, NT, 2>(a, part, rank, i0, tn * 128, cols);
+        else if (g.splits == 4) join<DT, ODT, GATED, NT, 4>(a, part, rank, i0, tn * 128, cols);
+        else join<DT, ODT, GATED, NT, 8>(a, part, rank, i0, tn * 128, cols);
+    }
+    if (g.splits > 1) cluster_sync();       // the peers have read this block's shared memory
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
+        for (int s = 0; s < g.stages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
+    __syncthreads();
+    if (warp == 5)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"((uint32_t)Tl::kTmem));
+}
+
+// ------------------------------------------------------------ the pair kernel
+//
+// Large products: two SMs share a tile of 256 rows of A by 256 rows of B, so that
+// either reads only its own 128 rows of both.  The first block's MMA
+// warp issues for both (cta_group::2), and both blocks' copies arrive at its
+// barriers.  Lanes are rows of A, so that a thread holds consecutive columns of a
+// row of the result.  A gated tile has 128 columns of the result: the first block
+// brings the gate's weights, the second the other ones, and the accumulator's
+// columns are 128 sums of either.  The last tile of a row of tiles is
+// as narrow as what is left, in steps of 32 columns.
+//
+// The blocks are persistent, with two accumulators of 256 columns (all of the
+// tensor memory): eight warps write one tile's result, in 32 columns at a time,
+// while the next tile's products run.
+constexpr int kPairStages = 6;
+constexpr int kPairStage = 2 * kHalf;
+constexpr int kPairWarps = 8;                            // of results
+constexpr int kPairThreads = (kPairWarps + 2) * 32;
+constexpr int kStagePad = 33;                            // floats of a staged row
+constexpr int kPairStaged = kPairWarps * 32 * kStagePad * 4;
+constexpr int kPairSmem = kPairStages * kPairStage + kPairStaged + 1024;
+static_assert(kPairSmem <= kSmemBlock, "one block's shared memory");
+
+struct PairArgs {
+    CUtensorMap a, b, b2, a2;
+    int64_t kt1, kt;                     // stages of the first pair of operands, of both
+    int64_t tiles_n, tiles_m;
+    int32_t vec;                         // finish_run's boundaries hold
+};
+
+// Tile t of the sweep: bands of 8 tiles of rows of A, so that the blocks at work
+// at one time share both operands in L2.
+__device__ __forceinline__ void pair_tile(const PairArgs &g, int64_t t, int64_t &tn, int64_t &tm)
+{
+    const int64_t band = t / (8 * g.tiles_n), in = t - band * 8 * g.tiles_n;
+    const int64_t wide = g.tiles_m - band * 8 < 8 ? g.tiles_m - band * 8 : 8;
+    tn = in / wide;
+    tm = band * 8 + in - tn * wide;
+}
+
+// Rows of B that either block brings for tile column tn.
+template <bool GATED> __device__ __forceinline__ int half_of(int64_t n, int64_t tn)
+{
+    if constexpr (GATED) {
+        const int64_t left = n - tn * 128;
+        return left >= 128 ? 128 : (int)((left + 15) / 16 * 16);
+    } else {
+        const int64_t left = n - tn * 256;
+        return left >= 256 ? 128 : (int)((left + 31) / 32 * 16);
+    }
+}
+
+template <int DT, int ODT, bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ PairArgs g)
+{
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * kPairStages + 4];
+    __shared__ uint32_t tmem_base, failed;
+    const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int64_t tiles = g.tiles_n * g.tiles_m, step = gridDim.x / 2;
+    auto full = [&](int s) { return saddr(&bars[s]); };                     // the first block's
+    auto empty = [&](int s) { return saddr(&bars[kPairStages + s]); };
+    auto done = [&](int b) { return saddr(&bars[2 * kPairStages + b]); };
+    auto drained = [&](int b) { return saddr(&bars[2 * kPairStages + 2 + b]); };  // the first's
+
+    if (warp == kPairWarps) {
+        if (lane == 0) {
+            for (int s = 0; s < 2 * kPairStages + 2; ++s) bar_init(saddr(&bars[s]), 1);
+            for (int b = 0; b < 2; ++b) bar_init(drained(b), 2 * kPairWarps);
+            failed = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+    } else if (warp == kPairWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         saddr(&tmem_base)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();             // both blocks' barriers and tensor memory are there
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_base;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    bool ok = true;
+    if (warp == kPairWarps) {                                // the copies
+        const bool one = elect_one();
+        int s = 0;
+        uint32_t phase = 1;                                  // the stages start empty
+        for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
+            int64_t tn, tm;
+            pair_tile(g, t, tn, tm);
+            const int32_t ix = (int32_t)(tm * 256 + rank * 128);
+            const int32_t jx = GATED ? (int32_t)(tn * 128)
+                                     : (int32_t)(tn * 256 + rank * half_of<GATED>(a.n, tn));
+            for (int64_t kt = 0; kt < g.kt; ++kt) {
+                ok = bar_wait(empty(s), phase);
+                if (!ok) break;
+                if (one) {
+                    const bool second = kt >= g.kt1;
+                    const int32_t c = (int32_t)((second ? kt - g.kt1 : kt) * kDepth);
+                    const CUtensorMap *ma = second ? &g.a2 : &g.a;
+                    const CUtensorMap *mb = (GATED ? rank != 0 : second) ? &g.b2 : &g.b;
+                    const uint32_t st = ring + s * kPairStage, bar = peer_addr(full(s), 0);
+                    if (rank == 0) bar_expect(full(s), 2 * kPairStage);
+                    if (a.a_cols) {
+                        tensor_load(st, ma, ix, c, bar);
+                        tensor_load(st + kHalf / 2, ma, ix + 64, c, bar);
+                    } else {
+                        tensor_load(st, ma, c, ix, bar);
+                    }
+                    if (a.b_cols) {
+                        tensor_load(st + kHalf, mb, jx, c, bar);
+                        tensor_load(st + kHalf + kHalf / 2, mb, jx + 64, c, bar);
+                    } else {
+                        tensor_load(st + kHalf, mb, c, jx, bar);
+                    }
+                }
+                __syncwarp();
+                if (++s == kPairStages) s = 0, phase ^= 1;
+            }
+        }
+    } else if (warp == kPairWarps + 1) {                     // the products
+        if (rank == 0) {
+            const bool one = elect_one();
+            const Layout la = layout_of(a.a_cols), lb = layout_of(a.b_cols);
+            const uint32_t shape = shape_desc<DT>(a.a_cols, a.b_cols) | ((256u >> 4) << 24);
+            const int last_steps = (int)((a.k - (g.kt1 - 1) * kDepth + 15) / 16);
+            int s = 0;
+            uint32_t phase = 0, i = 0, drained_phase = 1;    // the accumulators start drained
+            for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
+                int64_t tn, tm;
+                pair_tile(g, t, tn, tm);
+                const uint32_t desc = shape | ((uint32_t)(2 * half_of<GATED>(a.n, tn)) >> 3 << 17);
+                const uint32_t acc = tmem + i * 256;
+                ok = bar_wait(drained((int)i), drained_phase);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int64_t kt = 0; kt < g.kt; ++kt) {
+                    ok = bar_wait(full(s), phase);
+                    if (!ok) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (one) {
+                        const uint64_t da = at(la, ring + s * kPairStage);
+                        const uint64_t db = at(lb, ring + s * kPairStage + kHalf);
+                        const int steps = kt == g.kt1 - 1 || kt == g.kt - 1 ? last_steps : 4;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (q >= steps) break;
+                            mma2(acc, da + q * la.step, db + q * lb.step, desc, kt > 0 || q > 0);
+                        }
+                        commit2(empty(s));
+                        if (kt == g.kt - 1) commit2(done((int)i));
+                    }
+                    __syncwarp();
+                    if (++s == kPairStages) s = 0, phase ^= 1;
+                }
+                i ^= 1;
+                if (i == 0) drained_phase ^= 1;
+            }
+        }
+    } else {                                                 // the results
+        const int part = warp & 3, turn = warp >> 2;
+        const uint32_t lanes = (uint32_t)(part * 32) << 16;
+        float *staged = reinterpret_cast<float *>(dyn + (ring - saddr(dyn)) +
+                                                  kPairStages * kPairStage) +
+                        warp * 32 * kStagePad;
+        uint32_t b = 0, done_phase = 0;
+        for (int64_t t = blockIdx.x / 2; t < tiles; t += step) {
+            int64_t tn, tm;
+            pair_tile(g, t, tn, tm);
+            ok = bar_wait(done((int)b), done_phase);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const int half = half_of<GATED>(a.n, tn);
+            const int64_t i0 = tm * 256 + rank * 128 + part * 32;
+            const int64_t j0 = tn * (GATED ? 128 : 256);
+            const int wide = GATED ? half : 2 * half;        // columns of the result
+#pragma unroll 1
+            for (int c = turn * 32; c < wide; c += 64) {
+                const uint32_t from = tmem + lanes + b * 256 + c;
+                uint32_t r[32], r2[32];
+                load32(from, r);
+                if constexpr (GATED) load32(from + half, r2);
+                float z[32], z2[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    z[e] = __uint_as_float(r[e]);
+                    z2[e] = GATED ? __uint_as_float(r2[e]) : 0.0f;
+                }
+                const int64_t j = j0 + c;
+                if (g.vec && j + 32 <= a.n) {
+                    if (i0 + lane < a.m) finish_run<DT, ODT, GATED>(a, i0 + lane, j, z, z2);
+                    continue;
+                }
+                // rows off the boundaries, or a ragged end: through shared memory, so that
+                // a warp's accesses are consecutive
+                const float bias = a.bias && j + lane < a.n ? elems::load1<DT>(a.bias, j + lane)
+                                                            : 0.0f;
+                const int64_t rows = a.m - i0 < 32 ? a.m - i0 : 32;
+                float w2[32];
+                __syncwarp();
+                if constexpr (GATED) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) staged[lane * kStagePad + e] = z2[e];
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) w2[e] = staged[e * kStagePad + lane];
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) staged[lane * kStagePad + e] = z[e];
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e < rows)
+                        finish_lane<DT, ODT, GATED>(a, i0 + e, j + lane, j + lane < a.n,
+                                                    staged[e * kStagePad + lane],
+                                                    GATED ? w2[e] : 0.0f, bias);
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_first(drained((int)b));
+            b ^= 1;
+            if (b == 0) done_phase ^= 1;
+        }
+    }
+    if (!ok) {
+        if (lane == 0) atomicAdd(&g_matmul_timeouts, 1u);
+        failed = 1;
+    }
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    // copies still in flight land before either block ends
+    if (failed && threadIdx.x == 0 && rank == 0)
+        for (int s = 0; s < kPairStages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
+    __syncthreads();
+    cluster_sync();             // nothing of either block is still in use by the other
+    if (warp == kPairWarps + 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(512u));
+}
+
+// ------------------------------------------------------- rows onto boundaries
+//
+// A matrix whose rows do not begin on 16-byte boundaries, copied to one whose
+// rows do: a warp takes 256 elements of a row.
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+align_rows_kernel(const void *from, int64_t rows, int64_t cols, int64_t stride, void *to,
+                  int64_t to_stride, int64_t runs)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t r = w / runs, c0 = (w - r * runs) * 256;
+    if (r >= rows) return;
+    const elems::Span span = {static_cast<const char *>(from),
+                              static_cast<const char *>(from) +
+                                  ((rows - 1) * stride + cols) * 2};
+    const int64_t at = r * stride + c0;
+    const bool inside = span.around(at * 2, 512);
+    elems::Pieces<DT> p;
+    p.ask(from, at + 8 * lane, span, inside);
+    const elems::Raw<DT> v = p.take();
+    const int64_t c = c0 + 8 * lane;
+    // (the eights reach no further than the padded row: to_stride is cols rounded up to 8)
+    if (c < cols) v.store(to, r * to_stride + c);
+}
+
+cudaError_t align_rows(const void *from, int64_t rows, int64_t cols, int64_t stride, void *to,
+                       int64_t to_stride, cudaStream_t s)
+{
+    const int64_t runs = (cols + 255) / 256, blocks = (rows * runs + 7) / 8;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    // (16-bit elements are copied as they are: either type will do)
+    return launch_dependent(align_rows_kernel<BF16>, dim3((unsigned)blocks), dim3(kThreads), 0, s,
+                            from, rows, cols, stride, to, to_stride, runs);
+}
+
+// ------------------------------------------------------------------- the host
+
+using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                            const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                            const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encoder(Encode &f)
+{
+    static std::atomic<Encode> known{nullptr};
+    f = known.load(std::memory_order_relaxed);
+    if (f) return cudaSuccess;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                     cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (!p || found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    f = reinterpret_cast<Encode>(p);
+    known.store(f, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// `rows` rows of k elements, or (cols) their transpose; boxes of 64 c by
+// `box` rows, or of 64 rows by 64 c.
+cudaError_t operand_map(CUtensorMap *map, const void *p, int64_t rows, int64_t k, int64_t stride,
+                        int32_t cols, int box)
+{
+    Encode f;
+    const cudaError_t e = encoder(f);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[2] = {(cuuint64_t)(cols ? rows : k), (cuuint64_t)(cols ? k : rows)};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t boxes[2] = {64, (cuuint32_t)(cols ? 64 : box)}, one[2] = {1, 1};
+    const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(p), dims,
+                         strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The maps of one call's operands, `rows_a` rows of A and `rows_b` of B a box.
+template <class G>
+cudaError_t operand_maps(const ProductArgs &a, G &g, int rows_a, int rows_b)
+{
+    if (a.k == 0) return cudaSuccess;                   // nothing is read
+    cudaError_t e = operand_map(&g.a, a.a, a.m, a.k, a.a_stride, a.a_cols, rows_a);
+    if (e == cudaSuccess) e = operand_map(&g.b, a.b, a.n, a.k, a.b_stride, a.b_cols, rows_b);
+    if (e == cudaSuccess && a.b2)
+        e = operand_map(&g.b2, a.b2, a.n, a.k, a.b2_stride, a.b_cols, rows_b);
+    if (e == cudaSuccess && a.a2)
+        e = operand_map(&g.a2, a.a2, a.m, a.k, a.a2_stride, a.a_cols, rows_a);
+    return e;
+}
+
+template <int DT, int ODT, bool GATED>
+cudaError_t pair_go(const ProductArgs &a, int sms, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e =
+        allow_shared(reinterpret_cast<const void *>(matmul_pair_kernel<DT, ODT, GATED>),
+                     kSmemBlock, done);
+    if (e != cudaSuccess) return e;
+    PairArgs g;
+    e = operand_maps(a, g, 128, 128);
+    if (e != cudaSuccess) return e;
+    g.kt1 = (a.k + kDepth - 1) / kDepth;
+    g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
+    g.tiles_n = GATED ? (a.n + 127) / 128 : (a.n + 255) / 256;
+    g.tiles_m = (a.m + 255) / 256;
+    auto rows32 = [](const void *p, int64_t stride, int es) {
+        return !p || (((uintptr_t)p & 31) == 0 && stride * es % 32 == 0);
+    };
+    constexpr int os = ODT == F32 ? 4 : 2;
+    g.vec = rows32(a.out, a.stride, os) && rows32(a.residual, a.residual_stride, os) &&
+            rows32(a.kept, a.kept_stride, 2) && rows32(a.kept2, a.kept_stride, 2) &&
+            ((uintptr_t)a.bias & 15) == 0;
+    const int64_t tiles = g.tiles_n * g.tiles_m;
+    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    return launch_dependent(matmul_pair_kernel<DT, ODT, GATED>, dim3((unsigned)(2 * pairs)),
+                            dim3(kPairThreads), kSmemBlock, s, a, g);
+}
+
+template <int DT, int ODT, bool GATED, int NT, bool ACOLS>
+cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
+{
+    using Tl = Tile<NT, GATED, ACOLS>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e =
+        allow_shared(reinterpret_cast<const void *>(matmul_kernel<DT, ODT, GATED, NT, ACOLS>),
+                     Tl::smem(Tl::kStages), done);
+    if (e != cudaSuccess) return e;
+    OneArgs g;
+    e = operand_maps(a, g, NT, 128);
+    if (e != cudaSuccess) return e;
+    g.kt1 = (a.k + kDepth - 1) / kDepth;
+    g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
+    g.tiles_n = (a.n + 127) / 128;
+    const int64_t tiles = g.tiles_n * ((a.m + NT - 1) / NT);
+    // The split that leaves the fullest SM the fewest stages, a join counting
+    // as kJoin of them, as long as all blocks find a place at once.
+    constexpr int kJoin = 4;
+    auto stages = [&](int splits) {
+        const int64_t most = (g.kt + splits - 1) / splits;
+        return most < 1 ? 1 : most < Tl::kStages ? (int)most : Tl::kStages;
+    };
+    g.splits = 1;
+    int64_t least = (tiles + sms - 1) / sms * g.kt;
+    for (int n = 2; n <= 8 && g.kt >= 2 * n; n *= 2) {
+        const int64_t per_sm = (tiles * n + sms - 1) / sms;
+        if (per_sm > kSmemSm / (Tl::smem(stages(n)) + 1024)) break;
+        const int64_t cost = per_sm * ((g.kt + n - 1) / n) + kJoin;
+        if (cost < least) least = cost, g.splits = n;
+    }
+    g.stages = stages(g.splits);
+    const int64_t blocks = tiles * g.splits;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kOneThreads);
+    cfg.dynamicSmemBytes = Tl::smem(g.stages);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)g.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, matmul_kernel<DT, ODT, GATED, NT, ACOLS>, a, g);
+}
+
+template <int DT, int ODT, bool GATED>
+cudaError_t pick(const ProductArgs &a, int sms, cudaStream_t s)
+{
+    // Few rows, or no more tiles of 128 by 128 than SMs: the single blocks, whose
+    // columns c can be split.  Beyond that the pairs.
+    const int64_t tiles = ((a.n + 127) / 128) * ((a.m + 127) / 128);
+    if (a.k > 0 && a.m > 64 && tiles > sms) return pair_go<DT, ODT, GATED>(a, sms, s);
+    if constexpr (!GATED) {
+        if (a.a_cols)
+            return a.m <= 64 ? one_go<DT, ODT, GATED, 64, true>(a, sms, s)
+                             : one_go<DT, ODT, GATED, 128, true>(a, sms, s);
+    }
+    return a.m <= 16 ? one_go<DT, ODT, GATED, 16, false>(a, sms, s)
+           : a.m <= 64 ? one_go<DT, ODT, GATED, 64, false>(a, sms, s)
+                       : one_go<DT, ODT, GATED, 128, false>(a, sms, s);
+}
+
+// An operand's place in the workspace, if it needs one: bytes.
+struct Place {
+    int64_t rows, cols, stride;                       // as it lies
+    int64_t bytes() const
+    {
+        return (rows * ((cols + 7) / 8 * 8) * 2 + 127) / 128 * 128;
+    }
+};
+
+bool on_boundaries(const void *p, int64_t rows, int64_t stride)
+{
+    return ((uintptr_t)p & 15) == 0 && (rows <= 1 || stride % 8 == 0);
+}
+
+}  // namespace
+
+int64_t product_workspace(const ProductArgs &a)
+{
+    int64_t need = 0;
+    auto add = [&](const void *p, int64_t rows, int32_t cols, int64_t stride) {
+        const Place at = cols ? Place{a.k, rows, stride} : Place{rows, a.k, stride};
+        if (p && !on_boundaries(p, at.rows, stride)) need += at.bytes();
+    };
+    add(a.a, a.m, a.a_cols, a.a_stride);
+    add(a.b, a.n, a.b_cols, a.b_stride);
+    add(a.a2, a.m, a.a_cols, a.a2_stride);
+    add(a.b2, a.n, a.b_cols, a.b2_stride);
+    return need;
+}
+
+cudaError_t launch_product(int32_t dt, int32_t odt, ProductArgs a, void *workspace, int sms,
+                           cudaStream_t s)
+{
+    if (a.m <= 0 || a.n <= 0) return cudaSuccess;
+    if (a.k > 0) {
+        char *room = static_cast<char *>(workspace);
+        cudaError_t e = cudaSuccess;
+        auto settle = [&](const void *&p, int64_t rows, int32_t cols, int64_t &stride) {
+            if (!p || e != cudaSuccess) return;
+            const Place at = cols ? Place{a.k, rows, stride} : Place{rows, a.k, stride};
+            if (!on_boundaries(p, at.rows, stride)) {
+                const int64_t to = (at.cols + 7) / 8 * 8;
+                e = align_rows(p, at.rows, at.cols, stride, room, to, s);
+                p = room;
+                stride = to;
+                room += at.bytes();
+            } else if (at.rows <= 1) {
+                stride = (at.cols + 7) / 8 * 8;       // of no use, but it has to be a stride
+            }
+        };
+        settle(a.a, a.m, a.a_cols, a.a_stride);
+        settle(a.b, a.n, a.b_cols, a.b_stride);
+        settle(a.a2, a.m, a.a_cols, a.a2_stride);
+        settle(a.b2, a.n, a.b_cols, a.b2_stride);
+        if (e != cudaSuccess) return e;
+    }
+    if (a.gated)
+        return dt == BF16 ? pick<BF16, BF16, true>(a, sms, s) : pick<F16, F16, true>(a, sms, s);
+    if (dt == BF16)
+        return odt == F32 ? pick<BF16, F32, false>(a, sms, s) : pick<BF16, BF16, false>(a, sms, s);
+    return odt == F32 ? pick<F16, F32, false>(a, sms, s) : pick<F16, F16, false>(a, sms, s);
+}
+
+cudaError_t matmul_timeouts(unsigned int *count)
+{
+    // the copy alone would not wait for streams that do not synchronise with the
+    // default one
+    const cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return e;
+    return cudaMemcpyFromSymbol(count, g_matmul_timeouts, sizeof(unsigned int));
+}
+
+}  // namespace zgb

@@ -1,0 +1,468 @@
+// The root-mean-square norm with the residual's addition, and its gradient.
+//
+//   s = T(x + r), rstd = 1 / sqrt(mean of s^2 + eps), y = s rstd w
+//   dx = ds + rstd (w dy - n mean(w dy n)), dw = sum over rows of dy n, n = s rstd
+//
+// A row's elements stay in registers between the sum and the result, so that
+// every matrix is read or written once.  One to eight warps share a row; sums
+// are in fp32, in an order that depends on the sizes alone.
+#include "zero_ops.h"
+#include "zero_pack8.cuh"
+#include "zero_rows.cuh"
+
+namespace zgb {
+namespace {
+
+constexpr int kWarps = kThreads / 32;
+
+struct Norm {
+    rows::In x, residual, w;
+    int64_t n, dim;
+    float eps;
+    void *sum, *y;
+    int64_t sum_stride, y_stride;
+    unsigned char *q;
+    float *rstd;
+};
+
+// The sum over the W warps of a row, the same in all of them.
+template <int W> __device__ __forceinline__ float row_sum(float v, float *shared)
+{
+    v = rows::warp_sum(v);
+    if constexpr (W == 1) return v;
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();                             // the sum before has been read
+    if ((threadIdx.x & 31) == 0) shared[warp] = v;
+    __syncthreads();
+    const int first = warp / W * W;
+    v = shared[first];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v = __fadd_rn(v, shared[first + i]);
+    return v;
+}
+
+__device__ __forceinline__ float rstd_of(float squares, int64_t dim, float eps)
+{
+    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(squares, (float)dim), eps)));
+}
+
+// x + r rounded to the type, as it is kept.
+template <int DT, bool VEC>
+__device__ __forceinline__ void total(bool add, const rows::Eight<DT, VEC> &x,
+                                      const rows::Eight<DT, VEC> &r, float (&s)[8])
+{
+    x.take(s);
+    if (add) {
+        float f[8];
+        r.take(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = __fadd_rn(s[e], f[e]);
+        elems::Raw<DT> v;
+        v.set(s);
+        v.get(s);
+    }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void finish(const Norm &a, int64_t row, int64_t c0, float rstd,
+                                       const rows::Eight<DT, VEC> &weight, float (&s)[8])
+{
+    float w[8];
+    weight.take(w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = __fmul_rn(__fmul_rn(s[e], rstd), w[e]);
+    if (a.y) rows::put<DT, VEC>(a.y, a.y_stride, row, c0, a.dim, s);
+    if (a.q) {
+        const pack8::View q = pack8::view(a.q, a.n, a.dim);
+        const int64_t c = c0 + 8 * (threadIdx.x & 31);
+        pack8::put_eight(q, row, c, c < q.wide, s);
+    }
+}
+
+// Rows of up to W * G * 256 elements.
+template <int DT, int W, int G, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+norm_kernel(const __grid_constant__ Norm a)
+{
+    __shared__ float shared[kWarps];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * (kWarps / W) + warp / W;
+    const int64_t first = (int64_t)(warp % W) * (G * 256);
+    const bool live = row < a.n;
+    rows::Eight<DT, VEC> x[G], r[G], w[G];
+    if (live) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            x[g].ask(a.x, row, first + g * 256, a.dim);
+            if (a.residual.p) r[g].ask(a.residual, row, first + g * 256, a.dim);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) w[g].ask(a.w, 0, first + g * 256, a.dim);
+    }
+    float s[G][8], squares = 0.0f;
+    if (live) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            total<DT, VEC>(a.residual.p != nullptr, x[g], r[g], s[g]);
+            if (a.sum) rows::put<DT, VEC>(a.sum, a.sum_stride, row, first + g * 256, a.dim, s[g]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) squares = __fmaf_rn(s[g][e], s[g][e], squares);
+        }
+    }
+    const float rstd = rstd_of(row_sum<W>(squares, shared), a.dim, a.eps);
+    if (!live) return;
+    if (a.rstd && warp % W == 0 && (threadIdx.x & 31) == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int g = 0; g < G; ++g) finish<DT, VEC>(a, row, first + g * 256, rstd, w[g], s[g]);
+}
+
+// Longer rows, a block each: the elements are read again for the result.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+norm_long_kernel(const __grid_constant__ Norm a)
+{
+    __shared__ float shared[kWarps];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t row = blockIdx.x, first = (int64_t)(threadIdx.x >> 5) * 256;
+    float squares = 0.0f, s[8];
+    rows::Eight<DT, VEC> x, r, w;
+    for (int64_t c0 = first; c0 < a.dim; c0 += kWarps * 256) {
+        x.ask(a.x, row, c0, a.dim);
+        if (a.residual.p) r.ask(a.residual, row, c0, a.dim);
+        total<DT, VEC>(a.residual.p != nullptr, x, r, s);
+        // (sum may be residual: its rows are read again below from there)
+        if (a.sum) rows::put<DT, VEC>(a.sum, a.sum_stride, row, c0, a.dim, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) squares = __fmaf_rn(s[e], s[e], squares);
+    }
+    const float rstd = rstd_of(row_sum<kWarps>(squares, shared), a.dim, a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    __syncwarp();
+    const bool again = !a.sum && a.residual.p;   // the sum was not stored: it is made again
+    const rows::In from = !a.sum ? a.x : rows::In{
+        a.sum, a.sum_stride,
+        {static_cast<const char *>(a.sum),
+         static_cast<const char *>(a.sum) +
+             ((a.n - 1) * a.sum_stride + a.dim) * elems::Raw<DT>::kSize}};
+    for (int64_t c0 = first; c0 < a.dim; c0 += kWarps * 256) {
+        x.ask(from, row, c0, a.dim);
+        if (again) r.ask(a.residual, row, c0, a.dim);
+        w.ask(a.w, 0, c0, a.dim);
+        total<DT, VEC>(again, x, r, s);
+        finish<DT, VEC>(a, row, c0, rstd, w, s);
+    }
+}
+
+template <int DT, int W, int G, bool VEC> cudaError_t norm_go(const Norm &a, cudaStream_t s)
+{
+    const int64_t blocks = (a.n + kWarps / W - 1) / (kWarps / W);
+    return launch_dependent(norm_kernel<DT, W, G, VEC>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                            s, a);
+}
+
+// Rows that a warp holds go a warp each, as long as that fills the SMs; few or
+// longer ones a block each.
+template <int DT, bool VEC> cudaError_t norm_pick(const Norm &a, int sms, cudaStream_t s)
+{
+    if (a.dim > 8192)
+        return launch_dependent(norm_long_kernel<DT, VEC>, dim3((unsigned)a.n), dim3(kThreads), 0,
+                                s, a);
+    if (a.n >= (int64_t)sms * 16) {
+        if (a.dim <= 256) return norm_go<DT, 1, 1, VEC>(a, s);
+        if (a.dim <= 1024) return norm_go<DT, 1, 4, VEC>(a, s);
+        if (a.dim <= 4096 && a.dim > 2048) return norm_go<DT, 4, 4, VEC>(a, s);
+    }
+    if (a.dim <= 2048) return norm_go<DT, 8, 1, VEC>(a, s);
+    if (a.dim <= 4096) return norm_go<DT, 8, 2, VEC>(a, s);
+    return norm_go<DT, 8, 4, VEC>(a, s);
+}
+
+// ----------------------------------------------------------------- the gradient
+
+struct NormGrad {
+    rows::In dy, ds, s, w;
+    const float *rstd;
+    int64_t n, dim;
+    void *dx;
+    int64_t dx_stride;
+    float *parts;                                // [blocks][dim], or null
+};
+
+// Blocks stride over the rows; a thread adds up its columns' part of dw in
+// registers, and the block's row groups join theirs at the end.
+template <int DT, int W, int G, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+norm_grad_kernel(const __grid_constant__ NormGrad a)
+{
+    constexpr int kGroups = kWarps / W;
+    __shared__ float shared[kWarps];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = (int64_t)(warp % W) * (G * 256);
+    rows::Eight<DT, VEC> we[G];
+    float dw[G][8];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        we[g].ask(a.w, 0, first + g * 256, a.dim);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[g][e] = 0.0f;
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.n; r0 += (int64_t)gridDim.x * kGroups) {
+        const int64_t row = r0 + warp / W;
+        const bool live = row < a.n;
+        rows::Eight<DT, VEC> dye[G], se[G], dse[G];
+        float rstd = 0.0f, share = 0.0f;
+        if (live) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                dye[g].ask(a.dy, row, first + g * 256, a.dim);
+                se[g].ask(a.s, row, first + g * 256, a.dim);
+                if (a.ds.p) dse[g].ask(a.ds, row, first + g * 256, a.dim);
+            }
+            rstd = a.rstd[row];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float dy[8], n[8], w[8];
+                dye[g].take(dy);
+                se[g].take(n);
+                we[g].take(w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    n[e] = __fmul_rn(n[e], rstd);
+                    dw[g][e] = __fmaf_rn(dy[e], n[e], dw[g][e]);
+                    share = __fmaf_rn(__fmul_rn(dy[e], w[e]), n[e], share);
+                }
+            }
+        }
+        share = __fdiv_rn(row_sum<W>(share, shared), (float)a.dim);
+        if (live) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float dy[8], n[8], w[8], d[8];
+                dye[g].take(dy);
+                se[g].take(n);
+                we[g].take(w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    n[e] = __fmul_rn(n[e], rstd);
+                    d[e] = __fmul_rn(rstd, __fmaf_rn(-n[e], share, __fmul_rn(dy[e], w[e])));
+                }
+                if (a.ds.p) {
+                    float f[8];
+                    dse[g].take(f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[e] = __fadd_rn(d[e], f[e]);
+                }
+                rows::put<DT, VEC>(a.dx, a.dx_stride, row, first + g * 256, a.dim, d);
+            }
+        }
+    }
+    if (!a.parts) return;
+    float *part = a.parts + (int64_t)blockIdx.x * a.dim;
+    if constexpr (kGroups == 1) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t c = first + g * 256 + lane * 8 + e;
+                if (c < a.dim) part[c] = dw[g][e];
+            }
+    } else {
+        __shared__ float joined[kGroups * W * G * 256];
+        __syncthreads();
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                joined[(warp / W) * (W * G * 256) + (int)first + g * 256 + lane * 8 + e] = dw[g][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.dim; c += kThreads) {
+            float v = joined[c];
+#pragma unroll
+            for (int i = 1; i < kGroups; ++i) v = __fadd_rn(v, joined[i * (W * G * 256) + c]);
+            part[c] = v;
+        }
+    }
+}
+
+// Rows of more than 8192 elements: dx by a block a row, which reads it twice ...
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+norm_grad_long_kernel(const __grid_constant__ NormGrad a)
+{
+    __shared__ float shared[kWarps];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t row = blockIdx.x, first = (int64_t)(threadIdx.x >> 5) * 256;
+    const float rstd = a.rstd[row];
+    float share = 0.0f;
+    rows::Eight<DT, VEC> dye, se, we, dse;
+    float dy[8], n[8], w[8], d[8];
+    for (int64_t c0 = first; c0 < a.dim; c0 += kWarps * 256) {
+        dye.ask(a.dy, row, c0, a.dim);
+        se.ask(a.s, row, c0, a.dim);
+        we.ask(a.w, 0, c0, a.dim);
+        dye.take(dy);
+        se.take(n);
+        we.take(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            share = __fmaf_rn(__fmul_rn(dy[e], w[e]), __fmul_rn(n[e], rstd), share);
+    }
+    share = __fdiv_rn(row_sum<kWarps>(share, shared), (float)a.dim);
+    for (int64_t c0 = first; c0 < a.dim; c0 += kWarps * 256) {
+        dye.ask(a.dy, row, c0, a.dim);
+        se.ask(a.s, row, c0, a.dim);
+        we.ask(a.w, 0, c0, a.dim);
+        if (a.ds.p) dse.ask(a.ds, row, c0, a.dim);
+        dye.take(dy);
+        se.take(n);
+        we.take(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            n[e] = __fmul_rn(n[e], rstd);
+            d[e] = __fmul_rn(rstd, __fmaf_rn(-n[e], share, __fmul_rn(dy[e], w[e])));
+        }
+        if (a.ds.p) {
+            dse.take(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = __fadd_rn(d[e], w[e]);
+        }
+        rows::put<DT, VEC>(a.dx, a.dx_stride, row, c0, a.dim, d);
+    }
+}
+
+// ... and dw by strips of 256 columns, a share of the rows each block.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+norm_grad_strips_kernel(const __grid_constant__ NormGrad a)
+{
+    __shared__ float joined[kWarps][256];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c0 = (int64_t)blockIdx.x * 256;
+    float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int64_t r = (int64_t)blockIdx.y * kWarps + warp; r < a.n; r += (int64_t)gridDim.y * kWarps) {
+        rows::Eight<DT, VEC> dye, se;
+        float dy[8], n[8];
+        dye.ask(a.dy, r, c0, a.dim);
+        se.ask(a.s, r, c0, a.dim);
+        const float rstd = a.rstd[r];
+        dye.take(dy);
+        se.take(n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[e] = __fmaf_rn(dy[e], __fmul_rn(n[e], rstd), dw[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) joined[warp][lane * 8 + e] = dw[e];
+    __syncthreads();
+    const int64_t c = c0 + threadIdx.x;
+    if (c < a.dim) {
+        float v = joined[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) v = __fadd_rn(v, joined[i][threadIdx.x]);
+        a.parts[(int64_t)blockIdx.y * a.dim + c] = v;
+    }
+}
+
+constexpr int kMostBlocks = 608;                 // four on each of 152 SMs
+constexpr int kStripParts = 16;
+
+// Which of a row's forms a width takes: warps a row.
+int row_warps(int64_t dim) { return dim <= 1024 ? 1 : 8; }
+
+template <int DT, int W, int G, bool VEC>
+cudaError_t grad_go(const NormGrad &a, int64_t parts, cudaStream_t s)
+{
+    return launch_dependent(norm_grad_kernel<DT, W, G, VEC>, dim3((unsigned)parts), dim3(kThreads),
+                            0, s, a);
+}
+
+template <int DT, bool VEC>
+cudaError_t grad_pick(const NormGrad &a, int64_t parts, cudaStream_t s)
+{
+    if (a.dim > 8192) {
+        cudaError_t e = launch_dependent(norm_grad_long_kernel<DT, VEC>, dim3((unsigned)a.n),
+                                         dim3(kThreads), 0, s, a);
+        if (e != cudaSuccess || !a.parts) return e;
+        return launch_dependent(norm_grad_strips_kernel<DT, VEC>,
+                                dim3((unsigned)((a.dim + 255) / 256), (unsigned)parts),
+                                dim3(kThreads), 0, s, a);
+    }
+    if (a.dim <= 256) return grad_go<DT, 1, 1, VEC>(a, parts, s);
+    if (a.dim <= 1024) return grad_go<DT, 1, 4, VEC>(a, parts, s);
+    if (a.dim <= 2048) return grad_go<DT, 8, 1, VEC>(a, parts, s);
+    if (a.dim <= 4096) return grad_go<DT, 8, 2, VEC>(a, parts, s);
+    return grad_go<DT, 8, 4, VEC>(a, parts, s);
+}
+
+int64_t norm_parts(int64_t n, int64_t dim)
+{
+    if (dim > 8192) return (n + 7) / 8 < kStripParts ? (n + 7) / 8 : kStripParts;
+    const int64_t groups = kWarps / row_warps(dim), blocks = (n + groups - 1) / groups;
+    return blocks < kMostBlocks ? blocks : kMostBlocks;
+}
+
+}  // namespace
+
+cudaError_t launch_norm(int32_t dt, const NormArgs &a, int sms, cudaStream_t s)
+{
+    if (a.rows <= 0 || a.dim <= 0) return cudaSuccess;
+    Norm n = {rows::in(a.x, a.rows, a.dim, a.x_stride, dt),
+              rows::in(a.residual, a.rows, a.dim, a.residual_stride, dt),
+              rows::in(a.weight, 1, a.dim, a.dim, dt),
+              a.rows, a.dim, a.eps, a.sum, a.y, a.sum_stride, a.y_stride, a.q, a.rstd};
+    const bool vec = rows_aligned(a.x, a.x_stride, dt, a.dim) &&
+                     rows_aligned(a.weight, 0, dt, a.dim) &&
+                     (!a.residual || rows_aligned(a.residual, a.residual_stride, dt, a.dim)) &&
+                     (!a.sum || rows_aligned(a.sum, a.sum_stride, dt, a.dim)) &&
+                     (!a.y || rows_aligned(a.y, a.y_stride, dt, a.dim));
+    auto go = [&](auto t) {
+        constexpr int DT = decltype(t)::value;
+        return vec ? norm_pick<DT, true>(n, sms, s) : norm_pick<DT, false>(n, sms, s);
+    };
+    return dt == F32 ? go(std::integral_constant<int, F32>{})
+           : dt == BF16 ? go(std::integral_constant<int, BF16>{})
+                        : go(std::integral_constant<int, F16>{});
+}
+
+int64_t norm_grad_workspace(int64_t rows, int64_t dim)
+{
+    return norm_parts(rows, dim) * dim * 4;
+}
+
+cudaError_t launch_norm_grad(int32_t dt, int32_t wdt, const NormGradArgs &a, float *workspace,
+                             cudaStream_t s)
+{
+    if (a.dim <= 0) return cudaSuccess;
+    const int64_t parts = norm_parts(a.rows, a.dim);
+    if (a.rows > 0) {
+        NormGrad n = {rows::in(a.dy, a.rows, a.dim, a.dy_stride, dt),
+                      rows::in(a.ds, a.rows, a.dim, a.ds_stride, dt),
+                      rows::in(a.sum, a.rows, a.dim, a.sum_stride, dt),
+                      rows::in(a.weight, 1, a.dim, a.dim, dt),
+                      a.rstd, a.rows, a.dim, a.dx, a.dx_stride, a.dweight ? workspace : nullptr};
+        const bool vec = rows_aligned(a.dy, a.dy_stride, dt, a.dim) &&
+                         rows_aligned(a.sum, a.sum_stride, dt, a.dim) &&
+                         rows_aligned(a.weight, 0, dt, a.dim) &&
+                         (!a.ds || rows_aligned(a.ds, a.ds_stride, dt, a.dim)) &&
+                         rows_aligned(a.dx, a.dx_stride, dt, a.dim);
+        auto go = [&](auto t) {
+            constexpr int DT = decltype(t)::value;
+            return vec ? grad_pick<DT, true>(n, parts, s) : grad_pick<DT, false>(n, parts, s);
+        };
+        const cudaError_t e = dt == F32 ? go(std::integral_constant<int, F32>{})
+                              : dt == BF16 ? go(std::integral_constant<int, BF16>{})
+                                           : go(std::integral_constant<int, F16>{});
+        if (e != cudaSuccess) return e;
+    }
+    if (!a.dweight) return cudaSuccess;
+    return launch_column_sums(wdt, workspace, parts, a.dim, a.dweight, a.accumulate, s);
+}
+
+}  // namespace zgb

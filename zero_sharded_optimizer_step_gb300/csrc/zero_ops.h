@@ -1,6 +1,6 @@
 // Internal interface between the training operators' C ABI (zero_ops_abi.cu)
 // and their kernels (zero_embed.cu, zero_dropout.cu, zero_mx4.cu,
-// zero_mx4_matmul.cu).  Element types are the DType codes of
+// zero_mx4_matmul.cu, zero_matmul.cu, zero_norm.cu, zero_activation.cu).  Element types are the DType codes of
 // zero_internal.h; every launcher returns a cudaError_t and launches on `s`.
 #pragma once
 
@@ -127,5 +127,85 @@ struct MxMatmulArgs {
 };
 cudaError_t launch_mx4_matmul(int32_t dt, const MxMatmulArgs &a, int sms, cudaStream_t s);
 cudaError_t mx4_timeouts(unsigned int *count);
+
+// ---- products of 16-bit matrices
+//
+// out = act(A B^T (+ A2 B2^T) + bias) + residual, or, gated, act(A B^T) * (A B2^T).
+struct ProductArgs {
+    const void *a, *b, *a2, *b2;           // a2, b2 may be null; gated: b2 alone is given
+    int64_t a_stride, b_stride, a2_stride, b2_stride;
+    int32_t a_cols, b_cols;                // the matrix lies as its transpose, k by m or n
+    int32_t gated, act;                    // act: zero_act.cuh
+    int64_t m, n, k;
+    const void *bias, *residual;           // [n] of the operands' type, [m, n] of the result's
+    int64_t residual_stride;
+    // what the backward pass needs: the sums with the bias in the operands' type, or
+    // packed (zero_pack8.cuh); kept2 the gated block's second ones
+    void *kept, *kept2;
+    int64_t kept_stride;
+    unsigned char *kept_q, *kept2_q;
+    void *out;                             // [m, n]
+    int64_t stride;
+};
+// Bytes for the operands whose rows are not on 16-byte boundaries.
+int64_t product_workspace(const ProductArgs &a);
+cudaError_t launch_product(int32_t dt, int32_t odt, ProductArgs a, void *workspace, int sms,
+                           cudaStream_t s);
+cudaError_t matmul_timeouts(unsigned int *count);
+
+// ---- the norm (dt of all matrices and the weight; gradients of wdt)
+struct NormArgs {
+    const void *x, *residual, *weight;     // residual may be null
+    int64_t rows, dim, x_stride, residual_stride;
+    float eps;
+    void *sum, *y;                         // either may be null
+    int64_t sum_stride, y_stride;
+    unsigned char *q;                      // y packed, or null
+    float *rstd;                           // [rows], or null
+};
+cudaError_t launch_norm(int32_t dt, const NormArgs &a, int sms, cudaStream_t s);
+
+struct NormGradArgs {
+    const void *dy, *ds, *sum, *weight;    // ds may be null
+    const float *rstd;
+    int64_t rows, dim, dy_stride, ds_stride, sum_stride;
+    void *dx, *dweight;                    // dweight may be null
+    int64_t dx_stride;
+    int32_t accumulate;                    // dweight
+};
+int64_t norm_grad_workspace(int64_t rows, int64_t dim);
+cudaError_t launch_norm_grad(int32_t dt, int32_t wdt, const NormGradArgs &a, float *workspace,
+                             cudaStream_t s);
+
+// ---- through activations; z, g, u in the type or packed (one of the two is given)
+struct ActGradArgs {
+    const void *dy, *kept;
+    unsigned char *kept_q;
+    int64_t rows, cols, dy_stride, kept_stride;
+    int32_t act;
+    void *dz, *dbias;                      // either may be null
+    int64_t dz_stride;
+    int32_t accumulate;                    // dbias
+};
+int64_t activation_grad_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_activation_grad(int32_t dt, int32_t bdt, const ActGradArgs &a, float *workspace,
+                                   cudaStream_t s);
+
+struct GatedGradArgs {
+    const void *dh, *gate, *up;
+    unsigned char *gate_q, *up_q;
+    int64_t rows, cols, dh_stride, kept_stride;
+    int32_t act;
+    void *dgate, *dup, *h;                 // h may be null
+    int64_t grad_stride, h_stride;
+};
+cudaError_t launch_gated_grad(int32_t dt, const GatedGradArgs &a, cudaStream_t s);
+
+// ---- rows in 8 bits (zero_pack8.cuh)
+int64_t pack8_bytes(int64_t rows, int64_t cols);
+cudaError_t launch_pack8(int32_t dt, const void *x, int64_t rows, int64_t cols, int64_t stride,
+                         unsigned char *q, cudaStream_t s);
+cudaError_t launch_unpack8(int32_t dt, const unsigned char *q, int64_t rows, int64_t cols,
+                           void *out, int64_t stride, cudaStream_t s);
 
 }  // namespace zgb

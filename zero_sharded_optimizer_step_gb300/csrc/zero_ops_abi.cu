@@ -1,5 +1,6 @@
 // C ABI of the training operators: the embedding and its gradient, dropout,
-// and the microscaled 4-bit quantisation and product.  Argument checks and
+// the microscaled 4-bit quantisation and product, the norm, 16-bit products and
+// gated blocks, and rows kept in 8 bits.  Argument checks and
 // the launches; the declarations and their contracts are in include/zero.h.
 #include <atomic>
 #include <cmath>
@@ -79,6 +80,50 @@ int check_records(const char *name, const void *q, int64_t rows, int64_t cols)
     if (rows > 0 && cols > 0 && !q) return report(ZERO_EINVAL, "%s must not be null", name);
     if (!aligned(q, 16)) return report(ZERO_EALIGN, "%s is not aligned to 16 bytes", name);
     return ZERO_OK;
+}
+
+bool valid_16(int32_t d) { return d == ZERO_BF16 || d == ZERO_F16; }
+
+bool valid_activation(int32_t a) { return a >= ZERO_ACT_NONE && a <= ZERO_ACT_SILU; }
+
+int check_activation(int32_t a)
+{
+    return valid_activation(a) ? ZERO_OK : report(ZERO_EINVAL, "unknown activation %d", a);
+}
+
+bool size_ok(int64_t v) { return v >= 0 && v <= kMost; }
+
+// A matrix that may be NULL.
+int check_optional(const char *name, const void *p, int32_t dt, int64_t rows, int64_t cols,
+                   int64_t stride)
+{
+    return p ? check_matrix(name, p, dt, rows, cols, stride) : ZERO_OK;
+}
+
+// A vector of `n` elements.
+int check_vector(const char *name, const void *p, int32_t dt, int64_t n)
+{
+    return check_matrix(name, p, dt, 1, n, n);
+}
+
+int check_workspace(const void *workspace, int64_t bytes, int64_t need)
+{
+    if (need == 0) return ZERO_OK;
+    if (!workspace || bytes < need)
+        return report(ZERO_EINVAL, "the workspace has %lld bytes of the %lld needed",
+                      (long long)(workspace ? bytes : 0), (long long)need);
+    if (!aligned(workspace, 16))
+        return report(ZERO_EALIGN, "the workspace is not aligned to 16 bytes");
+    return ZERO_OK;
+}
+
+// What a call keeps or reads back: in the type, packed, or not at all.
+int check_kept(const char *name, const void *kept, const void *q, int32_t dt, int64_t rows,
+               int64_t cols, int64_t stride)
+{
+    if (kept && q) return report(ZERO_EINVAL, "%s is given in the type and in 8 bits", name);
+    const int rc = check_optional(name, kept, dt, rows, cols, stride);
+    return rc != ZERO_OK ? rc : q ? check_records(name, q, rows, cols) : ZERO_OK;
 }
 
 }  // namespace
@@ -253,6 +298,258 @@ int zero_mx4_timeouts(uint32_t *count)
     unsigned int h = 0;
     cudaError_t e = zgb::mx4_timeouts(&h);
     if (e != cudaSuccess) return launched(e, "reading the product's timeout counter");
+    *count = h;
+    return h ? ZERO_ETIMEOUT : ZERO_OK;
+}
+
+int64_t zero_pack8_bytes(int64_t rows, int64_t cols)
+{
+    if (!size_ok(rows) || !size_ok(cols)) return -1;
+    return zgb::pack8_bytes(rows, cols);
+}
+
+int zero_pack8(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t stride, void *q,
+               void *stream)
+{
+    ZERO_TRY(check_matrix("x", x, dtype, rows, cols, stride));
+    ZERO_TRY(check_records("q", q, rows, cols));
+    if (rows == 0 || cols == 0) return ZERO_OK;
+    return launched(zgb::launch_pack8(dtype, x, rows, cols, stride,
+                                      static_cast<unsigned char *>(q), (cudaStream_t)stream),
+                    "the packing");
+}
+
+int zero_unpack8(const void *q, int64_t rows, int64_t cols, void *out, int32_t dtype,
+                 int64_t stride, void *stream)
+{
+    ZERO_TRY(check_records("q", q, rows, cols));
+    ZERO_TRY(check_matrix("out", out, dtype, rows, cols, stride));
+    if (rows == 0 || cols == 0) return ZERO_OK;
+    return launched(zgb::launch_unpack8(dtype, static_cast<const unsigned char *>(q), rows, cols,
+                                        out, stride, (cudaStream_t)stream),
+                    "the values");
+}
+
+int zero_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                  const void *weight, int32_t dtype, int64_t rows, int64_t dim, float eps,
+                  void *sum, int64_t sum_stride, void *y, int64_t y_stride, void *q, float *rstd,
+                  void *stream)
+{
+    ZERO_TRY(check_matrix("x", x, dtype, rows, dim, x_stride));
+    ZERO_TRY(check_optional("residual", residual, dtype, rows, dim, residual_stride));
+    ZERO_TRY(check_vector("weight", weight, dtype, dim));
+    ZERO_TRY(check_optional("sum", sum, dtype, rows, dim, sum_stride));
+    ZERO_TRY(check_optional("y", y, dtype, rows, dim, y_stride));
+    if (!(eps >= 0.0f) || !std::isfinite(eps))
+        return report(ZERO_EINVAL, "eps must be finite and not negative");
+    if (!aligned(rstd, 4)) return report(ZERO_EALIGN, "rstd is not aligned to 4 bytes");
+    if (q) ZERO_TRY(check_records("q", q, rows, dim));
+    if (rows == 0 || dim == 0) return ZERO_OK;
+    if (!y && !q) return report(ZERO_EINVAL, "y and q must not both be null");
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
+    zgb::NormArgs a = {x, residual, weight, rows, dim, x_stride, residual_stride, eps, sum, y,
+                       sum_stride, y_stride, static_cast<unsigned char *>(q), rstd};
+    return launched(zgb::launch_norm(dtype, a, sms, (cudaStream_t)stream), "the norm");
+}
+
+int64_t zero_rms_norm_grad_workspace(int64_t rows, int64_t dim)
+{
+    if (!size_ok(rows) || !size_ok(dim)) return -1;
+    return zgb::norm_grad_workspace(rows, dim);
+}
+
+int zero_rms_norm_grad(const void *dy, int64_t dy_stride, const void *dsum, int64_t dsum_stride,
+                       const void *sum, int64_t sum_stride, const void *weight, const float *rstd,
+                       int32_t dtype, int64_t rows, int64_t dim, void *dx, int64_t dx_stride,
+                       void *dweight, int32_t grad_dtype, int32_t accumulate, void *workspace,
+                       int64_t workspace_bytes, void *stream)
+{
+    ZERO_TRY(check_matrix("dy", dy, dtype, rows, dim, dy_stride));
+    ZERO_TRY(check_optional("dsum", dsum, dtype, rows, dim, dsum_stride));
+    ZERO_TRY(check_matrix("sum", sum, dtype, rows, dim, sum_stride));
+    ZERO_TRY(check_vector("weight", weight, dtype, dim));
+    ZERO_TRY(check_matrix("dx", dx, dtype, rows, dim, dx_stride));
+    if (dweight) ZERO_TRY(check_vector("dweight", dweight, grad_dtype, dim));
+    if (rows > 0 && dim > 0 && !rstd) return report(ZERO_EINVAL, "rstd must not be null");
+    if (!aligned(rstd, 4)) return report(ZERO_EALIGN, "rstd is not aligned to 4 bytes");
+    if (dim == 0 || (rows == 0 && (!dweight || accumulate))) return ZERO_OK;
+    if (dweight)
+        ZERO_TRY(check_workspace(workspace, workspace_bytes, zgb::norm_grad_workspace(rows, dim)));
+    zgb::NormGradArgs a = {dy, dsum, sum, weight, rstd, rows, dim, dy_stride, dsum_stride,
+                           sum_stride, dx, dweight, dx_stride, accumulate != 0};
+    return launched(zgb::launch_norm_grad(dtype, grad_dtype, a, static_cast<float *>(workspace),
+                                          (cudaStream_t)stream),
+                    "the norm's gradient");
+}
+
+int64_t zero_matmul_workspace(const void *a, int32_t a_cols, int64_t a_stride, const void *b,
+                              int32_t b_cols, int64_t b_stride, const void *a2, int64_t a2_stride,
+                              const void *b2, int64_t b2_stride, int64_t m, int64_t n, int64_t k)
+{
+    if (!size_ok(m) || !size_ok(n) || !size_ok(k)) return -1;
+    zgb::ProductArgs p = {};
+    p.a = a, p.b = b, p.a2 = a2, p.b2 = b2;
+    p.a_stride = a_stride, p.b_stride = b_stride, p.a2_stride = a2_stride, p.b2_stride = b2_stride;
+    p.a_cols = a_cols != 0, p.b_cols = b_cols != 0;
+    p.m = m, p.n = n, p.k = k;
+    return zgb::product_workspace(p);
+}
+
+int zero_matmul(const void *a, int32_t a_cols, int64_t a_stride, const void *b, int32_t b_cols,
+                int64_t b_stride, const void *a2, int64_t a2_stride, const void *b2,
+                int64_t b2_stride, int32_t dtype, int64_t m, int64_t n, int64_t k,
+                const void *bias, int32_t activation, const void *residual,
+                int64_t residual_stride, void *kept, int64_t kept_stride, void *kept_q, void *out,
+                int32_t out_dtype, int64_t out_stride, int32_t accumulate, void *workspace,
+                int64_t workspace_bytes, void *stream)
+{
+    if (!valid_16(dtype)) return report(ZERO_EINVAL, "the operands are bf16 or fp16, not %d", dtype);
+    if (out_dtype != dtype && out_dtype != ZERO_F32)
+        return report(ZERO_EINVAL, "the result is of the operands' type or fp32, not %d", out_dtype);
+    auto operand = [&](const char *name, const void *p, int64_t rows, int32_t cols, int64_t stride) {
+        return cols ? check_matrix(name, p, dtype, k, rows, stride)
+                    : check_matrix(name, p, dtype, rows, k, stride);
+    };
+    ZERO_TRY(operand("a", a, m, a_cols, a_stride));
+    ZERO_TRY(operand("b", b, n, b_cols, b_stride));
+    if ((a2 != nullptr) != (b2 != nullptr))
+        return report(ZERO_EINVAL, "a2 and b2 are given together");
+    if (a2) {
+        ZERO_TRY(operand("a2", a2, m, a_cols, a2_stride));
+        ZERO_TRY(operand("b2", b2, n, b_cols, b2_stride));
+    }
+    if (bias) ZERO_TRY(check_vector("bias", bias, dtype, n));
+    ZERO_TRY(check_activation(activation));
+    ZERO_TRY(check_optional("residual", residual, out_dtype, m, n, residual_stride));
+    if (residual && accumulate)
+        return report(ZERO_EINVAL, "a residual and accumulate are not given together");
+    ZERO_TRY(check_kept("kept", kept, kept_q, dtype, m, n, kept_stride));
+    ZERO_TRY(check_matrix("out", out, out_dtype, m, n, out_stride));
+    if (m == 0 || n == 0) return ZERO_OK;
+    zgb::ProductArgs p = {};
+    p.a = a, p.b = b, p.a2 = a2, p.b2 = b2;
+    p.a_stride = a_stride, p.b_stride = b_stride, p.a2_stride = a2_stride, p.b2_stride = b2_stride;
+    p.a_cols = a_cols != 0, p.b_cols = b_cols != 0;
+    p.act = activation;
+    p.m = m, p.n = n, p.k = k;
+    p.bias = bias;
+    p.residual = accumulate ? out : residual;
+    p.residual_stride = accumulate ? out_stride : residual_stride;
+    p.kept = kept, p.kept_stride = kept_stride, p.kept_q = static_cast<unsigned char *>(kept_q);
+    p.out = out, p.stride = out_stride;
+    ZERO_TRY(check_workspace(workspace, workspace_bytes, zgb::product_workspace(p)));
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
+    return launched(zgb::launch_product(dtype, out_dtype, p, workspace, sms, (cudaStream_t)stream),
+                    "the product");
+}
+
+int64_t zero_gated_workspace(const void *x, int64_t x_stride, const void *w_gate,
+                             int64_t gate_stride, const void *w_up, int64_t up_stride, int64_t m,
+                             int64_t n, int64_t k)
+{
+    return zero_matmul_workspace(x, 0, x_stride, w_gate, 0, gate_stride, nullptr, 0, w_up,
+                                 up_stride, m, n, k);
+}
+
+int zero_gated(const void *x, int64_t x_stride, const void *w_gate, int64_t gate_stride,
+               const void *w_up, int64_t up_stride, int32_t dtype, int64_t m, int64_t n, int64_t k,
+               int32_t activation, void *gate, void *up, int64_t kept_stride, void *gate_q,
+               void *up_q, void *h, int64_t h_stride, void *workspace, int64_t workspace_bytes,
+               void *stream)
+{
+    if (!valid_16(dtype)) return report(ZERO_EINVAL, "the operands are bf16 or fp16, not %d", dtype);
+    ZERO_TRY(check_matrix("x", x, dtype, m, k, x_stride));
+    ZERO_TRY(check_matrix("w_gate", w_gate, dtype, n, k, gate_stride));
+    ZERO_TRY(check_matrix("w_up", w_up, dtype, n, k, up_stride));
+    ZERO_TRY(check_activation(activation));
+    if ((gate != nullptr) != (up != nullptr) || (gate_q != nullptr) != (up_q != nullptr))
+        return report(ZERO_EINVAL, "the gate and the other projection are kept together");
+    ZERO_TRY(check_kept("gate", gate, gate_q, dtype, m, n, kept_stride));
+    ZERO_TRY(check_kept("up", up, up_q, dtype, m, n, kept_stride));
+    ZERO_TRY(check_matrix("h", h, dtype, m, n, h_stride));
+    if (m == 0 || n == 0) return ZERO_OK;
+    zgb::ProductArgs p = {};
+    p.a = x, p.b = w_gate, p.b2 = w_up;
+    p.a_stride = x_stride, p.b_stride = gate_stride, p.b2_stride = up_stride;
+    p.gated = 1;
+    p.act = activation;
+    p.m = m, p.n = n, p.k = k;
+    p.kept = gate, p.kept2 = up, p.kept_stride = kept_stride;
+    p.kept_q = static_cast<unsigned char *>(gate_q);
+    p.kept2_q = static_cast<unsigned char *>(up_q);
+    p.out = h, p.stride = h_stride;
+    ZERO_TRY(check_workspace(workspace, workspace_bytes, zgb::product_workspace(p)));
+    const int sms = sm_count();
+    if (!sms) return ZERO_ECUDA;
+    return launched(zgb::launch_product(dtype, dtype, p, workspace, sms, (cudaStream_t)stream),
+                    "the gated block");
+}
+
+int64_t zero_activation_grad_workspace(int64_t rows, int64_t cols)
+{
+    if (!size_ok(rows) || !size_ok(cols)) return -1;
+    return zgb::activation_grad_workspace(rows, cols);
+}
+
+int zero_activation_grad(const void *dy, int64_t dy_stride, const void *kept, int64_t kept_stride,
+                         const void *kept_q, int32_t activation, int32_t dtype, int64_t rows,
+                         int64_t cols, void *dz, int64_t dz_stride, void *dbias,
+                         int32_t bias_dtype, int32_t accumulate, void *workspace,
+                         int64_t workspace_bytes, void *stream)
+{
+    ZERO_TRY(check_matrix("dy", dy, dtype, rows, cols, dy_stride));
+    ZERO_TRY(check_activation(activation));
+    ZERO_TRY(check_kept("kept", kept, kept_q, dtype, rows, cols, kept_stride));
+    ZERO_TRY(check_optional("dz", dz, dtype, rows, cols, dz_stride));
+    if (dbias) ZERO_TRY(check_vector("dbias", dbias, bias_dtype, cols));
+    if (cols == 0) return ZERO_OK;
+    if (!dz && !dbias) return report(ZERO_EINVAL, "dz and dbias must not both be null");
+    if (rows > 0 && activation != ZERO_ACT_NONE && !kept && !kept_q)
+        return report(ZERO_EINVAL, "kept and kept_q must not both be null");
+    if (rows == 0 && (!dbias || accumulate)) return ZERO_OK;
+    if (dbias)
+        ZERO_TRY(check_workspace(workspace, workspace_bytes,
+                                 zgb::activation_grad_workspace(rows, cols)));
+    zgb::ActGradArgs a = {dy, kept, static_cast<unsigned char *>(const_cast<void *>(kept_q)),
+                          rows, cols, dy_stride, kept_stride, activation, dz, dbias, dz_stride,
+                          accumulate != 0};
+    return launched(zgb::launch_activation_grad(dtype, bias_dtype, a,
+                                                static_cast<float *>(workspace),
+                                                (cudaStream_t)stream),
+                    "the activation's gradient");
+}
+
+int zero_gated_grad(const void *dh, int64_t dh_stride, const void *gate, const void *up,
+                    int64_t kept_stride, const void *gate_q, const void *up_q, int32_t activation,
+                    int32_t dtype, int64_t rows, int64_t cols, void *dgate, void *dup,
+                    int64_t grad_stride, void *h, int64_t h_stride, void *stream)
+{
+    ZERO_TRY(check_matrix("dh", dh, dtype, rows, cols, dh_stride));
+    ZERO_TRY(check_activation(activation));
+    if ((gate != nullptr) != (up != nullptr) || (gate_q != nullptr) != (up_q != nullptr))
+        return report(ZERO_EINVAL, "the gate and the other projection are given together");
+    ZERO_TRY(check_kept("gate", gate, gate_q, dtype, rows, cols, kept_stride));
+    ZERO_TRY(check_kept("up", up, up_q, dtype, rows, cols, kept_stride));
+    ZERO_TRY(check_matrix("dgate", dgate, dtype, rows, cols, grad_stride));
+    ZERO_TRY(check_matrix("dup", dup, dtype, rows, cols, grad_stride));
+    ZERO_TRY(check_optional("h", h, dtype, rows, cols, h_stride));
+    if (rows == 0 || cols == 0) return ZERO_OK;
+    if (!gate && !gate_q) return report(ZERO_EINVAL, "gate and gate_q must not both be null");
+    auto bytes = [](const void *p) { return static_cast<unsigned char *>(const_cast<void *>(p)); };
+    zgb::GatedGradArgs a = {dh, gate, up, bytes(gate_q), bytes(up_q), rows, cols, dh_stride,
+                            kept_stride, activation, dgate, dup, h, grad_stride, h_stride};
+    return launched(zgb::launch_gated_grad(dtype, a, (cudaStream_t)stream),
+                    "the gated block's gradient");
+}
+
+int zero_matmul_timeouts(uint32_t *count)
+{
+    if (!count) return report(ZERO_EINVAL, "null argument");
+    unsigned int h = 0;
+    cudaError_t e = zgb::matmul_timeouts(&h);
+    if (e != cudaSuccess) return launched(e, "reading the products' timeout counter");
     *count = h;
     return h ? ZERO_ETIMEOUT : ZERO_OK;
 }
