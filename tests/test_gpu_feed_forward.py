@@ -348,7 +348,7 @@ def test_product(dtype, a_cols, b_cols, m, n, k):
     assert out.untouched()
     wide = space(m, n, torch.float32, n + 3, 1)
     need = product(as_lies(a, a_cols, 3, 1), a_cols, as_lies(b, b_cols, 5, 3), b_cols, wide)
-    assert need > 0
+    assert need > 0 or (m <= 4 and not a_cols and not b_cols)     # few rows need no copy
     F.within(wide.t, want, err)
     assert wide.untouched()
     assert z.zero_matmul_timeouts() == 0

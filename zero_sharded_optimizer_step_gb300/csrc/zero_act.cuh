@@ -5,6 +5,8 @@
 // nearly equal numbers are avoided: p (1 - p) of a logistic p is e / (1 + e)^2.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 namespace zgb {
@@ -78,6 +80,19 @@ __device__ __forceinline__ void both(float v, int32_t kind, float &y, float &slo
     default:
         y = v;
         slope = 1.0f;
+    }
+}
+
+// f(kind) with the activation's kind as a constant: one switch around the loop over
+// a thread's elements, instead of one in it.
+template <class F> __device__ __forceinline__ void with_kind(int32_t kind, F f)
+{
+    switch (kind) {
+    case kActRelu: f(std::integral_constant<int32_t, kActRelu>{}); break;
+    case kActGelu: f(std::integral_constant<int32_t, kActGelu>{}); break;
+    case kActGeluTanh: f(std::integral_constant<int32_t, kActGeluTanh>{}); break;
+    case kActSilu: f(std::integral_constant<int32_t, kActSilu>{}); break;
+    default: f(std::integral_constant<int32_t, kActNone>{});
     }
 }
 

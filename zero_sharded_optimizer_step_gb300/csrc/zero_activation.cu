@@ -93,12 +93,14 @@ activation_grad_kernel(const __grid_constant__ ActGrad a)
             if (a.act != kActNone) {
                 float z[8];
                 ze[u].take(z);
+                act::with_kind(a.act, [&](auto kind) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float y, slope;
-                    act::both(z[e], a.act, y, slope);
-                    d[e] = __fmul_rn(d[e], slope);
-                }
+                    for (int e = 0; e < 8; ++e) {
+                        float y, slope;
+                        act::both(z[e], decltype(kind)::value, y, slope);
+                        d[e] = __fmul_rn(d[e], slope);
+                    }
+                });
             }
             if (a.dz) rows::put<DT, VEC>(a.dz, a.dz_stride, r, c0, a.cols, d);
 #pragma unroll
@@ -157,14 +159,16 @@ gated_grad_kernel(const __grid_constant__ GatedGrad a)
     dhe.take(dh);
     ge.take(g);
     ue.take(u);
+    act::with_kind(a.act, [&](auto kind) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float slope;
-        act::both(g[e], a.act, f[e], slope);
-        d[e] = __fmul_rn(__fmul_rn(dh[e], u[e]), slope);
-        dh[e] = __fmul_rn(dh[e], f[e]);
-        f[e] = __fmul_rn(f[e], u[e]);
-    }
+        for (int e = 0; e < 8; ++e) {
+            float slope;
+            act::both(g[e], decltype(kind)::value, f[e], slope);
+            d[e] = __fmul_rn(__fmul_rn(dh[e], u[e]), slope);
+            dh[e] = __fmul_rn(dh[e], f[e]);
+            f[e] = __fmul_rn(f[e], u[e]);
+        }
+    });
     rows::put<DT, VEC>(a.dg, a.grad_stride, r, c0, a.cols, d);
     rows::put<DT, VEC>(a.du, a.grad_stride, r, c0, a.cols, dh);
     if (a.h) rows::put<DT, VEC>(a.h, a.h_stride, r, c0, a.cols, f);

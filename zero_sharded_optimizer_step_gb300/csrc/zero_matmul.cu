@@ -24,6 +24,7 @@
 #include "zero_elems.cuh"
 #include "zero_ops.h"
 #include "zero_pack8.cuh"
+#include "zero_rows.cuh"
 #include "zero_tensor.cuh"
 
 namespace zgb {
@@ -124,6 +125,120 @@ __device__ __forceinline__ void finish_lane(const ProductArgs &a, int64_t i, int
     }
 }
 
+// Elements e < valid of the four from element `at` on; `vec`: they lie on a
+// boundary of four.
+template <int DT>
+__device__ __forceinline__ void load_four(const void *p, int64_t at, bool vec, int valid,
+                                          float (&f)[4])
+{
+    using T = typename elems::El<DT>::T;
+    if (vec && valid == 4) {
+        if constexpr (DT == F32) {
+            const float4 v = *reinterpret_cast<const float4 *>(static_cast<const T *>(p) + at);
+            f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p) + at);
+            elems::widen2<DT>(v.x, f[0], f[1]);
+            elems::widen2<DT>(v.y, f[2], f[3]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = e < valid ? elems::load1<DT>(p, at + e) : 0.0f;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_four(void *p, int64_t at, bool vec, int valid,
+                                           const float (&f)[4])
+{
+    using T = typename elems::El<DT>::T;
+    if (vec && valid == 4) {
+        if constexpr (DT == F32)
+            *reinterpret_cast<float4 *>(static_cast<T *>(p) + at) =
+                make_float4(f[0], f[1], f[2], f[3]);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<T *>(p) + at) =
+                make_uint2(elems::narrow2<DT>(f[0], f[1]), elems::narrow2<DT>(f[2], f[3]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < valid) elems::store1<DT>(p, at + e, f[e]);
+    }
+}
+
+// The activation of an array.
+template <int U, int N> __device__ __forceinline__ void activate(float (&z)[U][N], int32_t kind)
+{
+    if (kind == kActNone) return;
+    act::with_kind(kind, [&](auto k) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[u][e] = act::value(z[u][e], decltype(k)::value);
+    });
+}
+
+// Four columns from j on of the U rows i[u], `valid` of them the result's, by a
+// thread whose seven neighbours hold the rest of 32 from a multiple of 32 on.  The
+// whole warp comes here together; a row that is not `there` is left out.  Step by
+// step for all rows, so that their latencies overlap.
+template <int DT, int ODT, bool GATED, int U>
+__device__ __forceinline__ void finish_fours(const ProductArgs &a, const int64_t (&i)[U],
+                                             const bool (&there)[U], int64_t j, bool vec,
+                                             int valid, float (&z)[U][4], float (&z2)[U][4],
+                                             const float (&bias)[4])
+{
+    float r[U][4];
+    if (a.residual) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            load_four<ODT>(a.residual, i[u] * a.residual_stride + j, vec, there[u] ? valid : 0,
+                           r[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[u][e] = __fadd_rn(z[u][e], bias[e]);
+    if (a.kept) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            store_four<DT>(a.kept, i[u] * a.kept_stride + j, vec, there[u] ? valid : 0, z[u]);
+            if constexpr (GATED)
+                store_four<DT>(a.kept2, i[u] * a.kept_stride + j, vec, there[u] ? valid : 0,
+                               z2[u]);
+        }
+    }
+    if (a.kept_q) {
+        const pack8::View q = pack8::view(a.kept_q, a.m, a.n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e >= valid) z[u][e] = z2[u][e] = 0.0f;
+            pack8::put_four(q, i[u], j, there[u] && j < q.wide, z[u]);
+            if constexpr (GATED)
+                pack8::put_four(pack8::view(a.kept2_q, a.m, a.n), i[u], j,
+                                there[u] && j < q.wide, z2[u]);
+        }
+    }
+    activate(z, a.act);
+    if constexpr (GATED) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[u][e] = __fmul_rn(z[u][e], z2[u][e]);
+    }
+    if (a.residual) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[u][e] = __fadd_rn(z[u][e], r[u][e]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        store_four<ODT>(a.out, i[u] * a.stride + j, vec, there[u] ? valid : 0, z[u]);
+}
+
 // 16 columns of a row on 32-byte boundaries.
 template <int DT> __device__ __forceinline__ void load_run(const void *p, int64_t at, float *f)
 {
@@ -183,18 +298,7 @@ __device__ __forceinline__ void finish_run(const ProductArgs &a, int64_t i, int6
         pack8::put_thread(pack8::view(a.kept_q, a.m, a.n), i, j, z);
         if constexpr (GATED) pack8::put_thread(pack8::view(a.kept2_q, a.m, a.n), i, j, z2);
     }
-    // one switch for the run: the activation's code is laid out once for each kind
-    auto all = [&](auto f) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) z[e] = f(z[e]);
-    };
-    switch (a.act) {
-    case kActRelu: all([](float v) { return act::value(v, kActRelu); }); break;
-    case kActGelu: all([](float v) { return act::value(v, kActGelu); }); break;
-    case kActGeluTanh: all([](float v) { return act::value(v, kActGeluTanh); }); break;
-    case kActSilu: all([](float v) { return act::value(v, kActSilu); }); break;
-    default: break;
-    }
+    activate(reinterpret_cast<float(&)[1][32]>(z), a.act);
     if constexpr (GATED) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) z[e] = __fmul_rn(z[e], z2[e]);
@@ -211,6 +315,119 @@ __device__ __forceinline__ void finish_run(const ProductArgs &a, int64_t i, int6
     }
 }
 
+// 32 columns from j on of 32 rows from i0 on, a row a lane.  Rows off the
+// boundaries and ragged ends go through the warp's shared memory (`staged`, 32 by
+// kStagePad floats), so that its accesses are consecutive.
+constexpr int kStagePad = 33;
+
+template <int DT, int ODT, bool GATED>
+__device__ __forceinline__ void finish_rows(const ProductArgs &a, bool vec, float *staged,
+                                            int64_t i0, int64_t j, float (&z)[32],
+                                            float (&z2)[32])
+{
+    const int lane = threadIdx.x & 31;
+    if (j >= a.n || i0 >= a.m) return;
+    if (vec && j + 32 <= a.n) {
+        if (i0 + lane < a.m) finish_run<DT, ODT, GATED>(a, i0 + lane, j, z, z2);
+        return;
+    }
+    const float bias = a.bias && j + lane < a.n ? elems::load1<DT>(a.bias, j + lane) : 0.0f;
+    const int64_t rows = a.m - i0 < 32 ? a.m - i0 : 32;
+    float w2[32];
+    __syncwarp();
+    if constexpr (GATED) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) staged[lane * kStagePad + e] = z2[e];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) w2[e] = staged[e * kStagePad + lane];
+        __syncwarp();
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) staged[lane * kStagePad + e] = z[e];
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (e < rows)
+            finish_lane<DT, ODT, GATED>(a, i0 + e, j + lane, j + lane < a.n,
+                                        staged[e * kStagePad + lane], GATED ? w2[e] : 0.0f, bias);
+    __syncwarp();
+}
+
+// ------------------------------------------------------- one to four rows
+//
+// The weights' bytes are all there is: a warp reads four rows of B (of both, in a
+// gated block) in the memory's own order, 512 bytes of each at a time, multiplies in fp32 and
+// adds up over its lanes.  A block makes 32 columns of the result; KS warps share a
+// row's length where the blocks are few.  No copy engine and no tensor memory to set
+// up, and rows need no boundary.
+template <int DT, int ODT, bool GATED, int M, int KS, bool VEC>
+__global__ void __launch_bounds__(256 * KS)
+matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ rows::In x,
+              const __grid_constant__ rows::In w, const __grid_constant__ rows::In w2)
+{
+    constexpr int R = 4, kWeights = GATED ? 2 : 1;
+    __shared__ float part[kWeights][KS][M][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp / 8;
+    const int64_t j0 = (int64_t)blockIdx.x * 32, first = j0 + (warp % 8) * R;
+    pdl_wait();
+    pdl_launch_dependents();
+    float acc[kWeights][R][M];
+#pragma unroll
+    for (int g = 0; g < kWeights; ++g)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < M; ++t) acc[g][r][t] = 0.0f;
+#pragma unroll 2
+    for (int64_t c0 = share * 256; c0 < a.k; c0 += KS * 256) {
+        rows::Eight<DT, VEC> we[kWeights][R], xe[M];
+#pragma unroll
+        for (int g = 0; g < kWeights; ++g)
+#pragma unroll
+            for (int r = 0; r < R; ++r)      // (the last row again past the end: not written)
+                we[g][r].ask(g ? w2 : w, first + r < a.n ? first + r : a.n - 1, c0, a.k);
+#pragma unroll
+        for (int t = 0; t < M; ++t) xe[t].ask(x, t < a.m ? t : 0, c0, a.k);
+        float xv[M][8];
+#pragma unroll
+        for (int t = 0; t < M; ++t) xe[t].take(xv[t]);
+#pragma unroll
+        for (int g = 0; g < kWeights; ++g)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float f[8];
+                we[g][r].take(f);
+#pragma unroll
+                for (int t = 0; t < M; ++t)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        acc[g][r][t] = __fmaf_rn(f[e], xv[t][e], acc[g][r][t]);
+            }
+    }
+#pragma unroll
+    for (int g = 0; g < kWeights; ++g)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < M; ++t) {
+                const float v = rows::warp_sum(acc[g][r][t]);
+                if (lane == 0) part[g][share][t][(warp % 8) * R + r] = v;
+            }
+    __syncthreads();
+    if (warp >= M || warp >= a.m) return;
+    float z[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int g = 0; g < kWeights; ++g) {
+        z[g] = part[g][0][warp][lane];
+#pragma unroll
+        for (int s = 1; s < KS; ++s) z[g] = __fadd_rn(z[g], part[g][s][warp][lane]);
+    }
+    const int64_t j = j0 + lane;
+    const float bias = a.bias && j < a.n ? elems::load1<DT>(a.bias, j) : 0.0f;
+    finish_lane<DT, ODT, GATED>(a, warp, j, j < a.n, z[0], z[1], bias);
+}
+
 // ------------------------------------------------- few rows, or few tiles
 //
 // The accumulator's 128 lanes are 128 rows of B (128 consecutive columns of
@@ -221,21 +438,20 @@ __device__ __forceinline__ void finish_run(const ProductArgs &a, int64_t i, int6
 // With fewer tiles than SMs the columns c are split over a cluster of up to 8
 // blocks, whose partial sums join through distributed shared memory in the blocks'
 // order.
-template <int NT, bool GATED, bool ACOLS> struct Tile {
-    static_assert(!ACOLS || NT >= 64, "a transposed chunk has 64 rows");
+template <int NT, bool GATED> struct Tile {
     static constexpr int kWeights = GATED ? 2 : 1;
     static constexpr int kStage = kWeights * kHalf + NT * kLine;
     static constexpr int kCols = kWeights * NT;
     static constexpr int kTmem = kCols <= 32 ? 32 : kCols;
     static constexpr int kMost = (kSmemBlock - 1024) / kStage;
     static constexpr int kStages = kMost < 8 ? kMost : 8;
-    static constexpr int kPart = kWeights * NT * 128 * 4;   // a split's partial sums
     // A block's share of an SM's shared memory is at least its share of the tensor
     // memory, so that no block waits for tensor memory that another one
     // holds: two that wait for their cluster peers so would wait forever.
-    static constexpr int smem(int stages)
+    static constexpr int smem(int stages, int span)
     {
-        const int ring = stages * kStage > kPart ? stages * kStage : kPart;
+        const int part = kWeights * span * 128 * 4;         // the sums, when they are done
+        const int ring = stages * kStage > part ? stages * kStage : part;
         const int share = (kSmemSm / (512 / kTmem) + 127) / 128 * 128;
         return ring + 1024 > share ? ring + 1024 : share;
     }
@@ -243,71 +459,85 @@ template <int NT, bool GATED, bool ACOLS> struct Tile {
 };
 
 constexpr int kOneThreads = 192;
+constexpr int kMostBlocks = 3;                         // of an SM
 
 struct OneArgs {
     CUtensorMap a, b, b2, a2;
     int64_t kt1, kt, tiles_n;            // stages of the first pair of operands, of both
     int32_t splits, stages;
+    int32_t span;                        // an accumulator's columns in shared memory
+    int32_t vec;                         // runs of columns lie on their boundaries
 };
 
-__device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank)
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(addr, rank))
-                 : "memory");
-    return v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// Adds up the SP splits' partial sums, [column][lane] in every block's shared
-// memory, in the blocks' order, and writes them: blocks and warps take 32 lanes
-// of a column each in turn.
-template <int DT, int ODT, bool GATED, int NT, int SP>
-__device__ __forceinline__ void join(const ProductArgs &a, const float *part, uint32_t rank,
-                                     int64_t i0, int64_t j0, int cols)
+// Four consecutive partial sums, of this block or added up over a split's blocks
+// in their order; all of a split's are asked for before the first is used.
+__device__ __forceinline__ float4 sum4(const float *at, int splits)
 {
-    constexpr int U = SP == 1 ? 4 : SP < 8 ? 2 : 1;    // runs on their way together
-    constexpr int kSums = GATED ? 2 : 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // (a whole block's warp finds its own lanes' sums)
+    if (splits == 1) return *reinterpret_cast<const float4 *>(at);
+    float4 v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < splits) v[q] = load_peer4(saddr(at), q);
+    float4 sum = v[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q)
+        if (q < splits) {
+            sum.x = __fadd_rn(sum.x, v[q].x);
+            sum.y = __fadd_rn(sum.y, v[q].y);
+            sum.z = __fadd_rn(sum.z, v[q].z);
+            sum.w = __fadd_rn(sum.w, v[q].w);
+        }
+    return sum;
+}
+
+// Adds up the splits' partial sums, rows of 128 columns of the result (`pitch`
+// floats apart) in every block's shared memory, and writes the result.  A warp
+// takes whole rows, four columns a lane, so that what it reads from a peer is consecutive: U of the rows
+// that fall to its block at a time.
+template <int DT, int ODT, bool GATED, int U>
+__device__ __forceinline__ void join(const ProductArgs &a, const float *part, int pitch,
+                                     const OneArgs &g, uint32_t rank, int64_t i0, int64_t j0,
+                                     int rows)
+{
+    constexpr int kWarps = kOneThreads / 32;
+    const int splits = g.splits, warp = threadIdx.x >> 5, lane4 = (threadIdx.x & 31) * 4;
+    const int64_t j = j0 + lane4, left = a.n - j;
+    const int valid = left >= 4 ? 4 : left > 0 ? (int)left : 0;
+    float bias[4] = {0, 0, 0, 0};
+    if (a.bias) load_four<DT>(a.bias, j, g.vec != 0, valid, bias);
 #pragma unroll 1
-    for (int first = (int)rank * 4 + warp; first < cols * 4; first += U * SP * 4) {
-        float v[U][kSums][SP];
+    for (int r0 = (int)rank + warp * splits; r0 < rows; r0 += U * kWarps * splits) {
+        int64_t i[U];
+        bool there[U];
+        float z[U][4], z2[U][4];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int run = first + u * SP * 4;
-            if (run >= cols * 4) break;
-#pragma unroll
-            for (int g = 0; g < kSums; ++g)
-#pragma unroll
-                for (int q = 0; q < SP; ++q)
-                    v[u][g][q] = SP == 1 ? part[g * NT * 128 + run * 32 + lane]
-                                         : load_peer(saddr(part + g * NT * 128 + run * 32 + lane),
-                                                     q);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int run = first + u * SP * 4;
-            if (run >= cols * 4) break;
-            float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int g = 0; g < kSums; ++g) {
-                sum[g] = v[u][g][0];
-#pragma unroll
-                for (int q = 1; q < SP; ++q) sum[g] = __fadd_rn(sum[g], v[u][g][q]);
+            const int r = r0 + u * kWarps * splits;
+            there[u] = r < rows;
+            i[u] = i0 + r;
+            float4 s = make_float4(0, 0, 0, 0), s2 = s;
+            const float *at = part + r * pitch + lane4;
+            if (there[u]) {
+                s = sum4(at, splits);
+                if constexpr (GATED) s2 = sum4(at + g.span * pitch, splits);
             }
-            const int64_t j = j0 + (run & 3) * 32 + lane;
-            if (j - lane >= a.n) continue;
-            const float bias = a.bias && j < a.n ? elems::load1<DT>(a.bias, j) : 0.0f;
-            finish_lane<DT, ODT, GATED>(a, i0 + (run >> 2), j, j < a.n, sum[0], sum[1], bias);
+            z[u][0] = s.x, z[u][1] = s.y, z[u][2] = s.z, z[u][3] = s.w;
+            z2[u][0] = s2.x, z2[u][1] = s2.y, z2[u][2] = s2.z, z2[u][3] = s2.w;
         }
+        finish_fours<DT, ODT, GATED, U>(a, i, there, j, g.vec != 0, valid, z, z2, bias);
     }
 }
 
-template <int DT, int ODT, bool GATED, int NT, bool ACOLS>
-__global__ void __launch_bounds__(kOneThreads, 2)
+template <int DT, int ODT, bool GATED, int NT>
+__global__ void __launch_bounds__(kOneThreads, kMostBlocks)
 matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ OneArgs g)
 {
-    using Tl = Tile<NT, GATED, ACOLS>;
+    using Tl = Tile<NT, GATED>;
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t bars[2 * Tl::kStages + 1];
     __shared__ uint32_t tmem_base, failed;
@@ -335,6 +565,10 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        if (one && g.kt > 0) {
+            prefetch_map(&g.a);
+            prefetch_map(&g.b);
+        }
         __syncwarp();
         pdl_wait();
         const int32_t jx = (int32_t)(tn * 128), ix = (int32_t)(tm * NT);
@@ -355,13 +589,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
             weights(st, !GATED && second ? &g.b2 : &g.b, c, full(s));
             if constexpr (GATED) weights(st + kHalf, &g.b2, c, full(s));
             const CUtensorMap *map = second ? &g.a2 : &g.a;
-            if constexpr (ACOLS) {
-#pragma unroll
-                for (int h = 0; h < NT / 64; ++h)
-                    box_load(tok + h * (kHalf / 2), map, ix + 64 * h, c, full(s));
-            } else {
-                box_load(tok, map, c, ix, full(s));
-            }
+            box_load(tok, map, c, ix, full(s));
         };
         // the first stages' copies need not wait for the other warps
         const int ahead = rounds < g.stages ? rounds : g.stages;
@@ -386,8 +614,8 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const bool one = elect_one();
         const uint32_t tmem = tmem_base;
-        const Layout lb = layout_of(a.b_cols), la = layout_of(ACOLS);
-        const uint32_t desc = shape_desc<DT>(a.b_cols, ACOLS) | ((uint32_t)(NT >> 3) << 17) |
+        const Layout lb = layout_of(a.b_cols), la = layout_of(0);
+        const uint32_t desc = shape_desc<DT>(a.b_cols, 0) | ((uint32_t)(NT >> 3) << 17) |
                               ((128u >> 4) << 24);
         int s = 0;
         uint32_t phase = 0;
@@ -431,30 +659,27 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
     const int64_t i0 = tm * NT;
     const int cols = (int)(a.m - i0 < NT ? a.m - i0 : NT);
     // The sums go where the stages were, [column][lane]: all copies have landed and
-    // all products have read them.  A split's blocks read each other's from there;
-    // a whole block's warps read their own, so that one piece of code, which is not laid
-    // out once for each register, writes the result.
+    // all products have read them.  From there all threads write the result,
+    // eight consecutive columns of a row each, a split's blocks each a share of the rows.
     float *part = reinterpret_cast<float *>(dyn + (ring - saddr(dyn)));
     if (warp < 4 && ok) {
         const uint32_t lanes = tmem_base + ((uint32_t)(warp * 32) << 16);
 #pragma unroll 1
-        for (int c = 0; c < Tl::kWeights * NT; c += 16) {
-            if ((c & (NT - 1)) >= cols) continue;
-            float v[16];
-            load16(lanes + c, v);
+        for (int c = 0; c < g.span; c += 16) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                part[(c + e) * 128 + warp * 32 + lane] = g.kt == 0 ? 0.0f : v[e];  // empty sums
+            for (int w = 0; w < Tl::kWeights; ++w) {
+                float v[16];
+                load16(lanes + w * NT + c, v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)                 // (or empty sums)
+                    part[(w * g.span + c + e) * 128 + warp * 32 + lane] = g.kt == 0 ? 0.0f : v[e];
+            }
         }
     }
     if (g.splits > 1) cluster_sync();
-    __syncwarp();
-    if (warp < 4 && ok) {
-        if (g.splits == 1) join<DT, ODT, GATED, NT, 1>(a, part, rank, i0, tn * 128, cols);
-        else if (g.splits == 2) join<DT, ODT, GATED, NT, 2>(a, part, rank, i0, tn * 128, cols);
-        else if (g.splits == 4) join<DT, ODT, GATED, NT, 4>(a, part, rank, i0, tn * 128, cols);
-        else join<DT, ODT, GATED, NT, 8>(a, part, rank, i0, tn * 128, cols);
-    }
+    else __syncthreads();
+    if (!failed)
+        join<DT, ODT, GATED, NT < 64 ? 1 : 2>(a, part, 128, g, rank, i0, tn * 128, cols);
     if (g.splits > 1) cluster_sync();       // the peers have read this block's shared memory
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -464,6 +689,182 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
     if (warp == 5)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"((uint32_t)Tl::kTmem));
+}
+
+// ------------------------------------------------------ some rows, few tiles
+//
+// Products of more than 64 rows that are too small for the pairs: tiles of 128
+// by 128, a block each or, split along c, a cluster of blocks.  Lanes are rows of A, so
+// that a thread holds 32 consecutive columns of a row of the result at a time.  Both
+// operands in either order.
+constexpr int kMidStage = 2 * kHalf;
+constexpr int kMidStages = 7;
+constexpr int kMidPad = 132;                             // floats of a row of partial sums
+constexpr int kMidPart = 128 * kMidPad * 4;
+constexpr int kMidStaged = (kOneThreads / 32) * 32 * kStagePad * 4;
+
+constexpr int mid_smem(int stages)
+{
+    const int ring = stages * kMidStage;
+    return (ring > kMidPart + kMidStaged ? ring : kMidPart + kMidStaged) + 1024;
+}
+static_assert(mid_smem(kMidStages) <= kSmemBlock, "one block's shared memory");
+
+template <int DT, int ODT>
+__global__ void __launch_bounds__(kOneThreads, 2)
+matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ OneArgs g)
+{
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * kMidStages + 1];
+    __shared__ uint32_t tmem_base, failed;
+    const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = g.splits > 1 ? cluster_rank() : 0;
+    const int64_t tile = blockIdx.x / g.splits;
+    const int64_t tn = tile % g.tiles_n, tm = tile / g.tiles_n;
+    const int64_t k0 = g.kt * rank / g.splits, k1 = g.kt * (rank + 1) / g.splits;
+    const int rounds = (int)(k1 - k0);
+    const uint32_t done_bar = saddr(&bars[2 * kMidStages]);
+    auto full = [&](int s) { return saddr(&bars[s]); };
+    auto empty = [&](int s) { return saddr(&bars[kMidStages + s]); };
+
+    bool ok = true;
+    if (warp == 4) {                                         // the copies
+        const bool one = elect_one();
+        if (one) {
+            for (int s = 0; s < kMidStages; ++s) {
+                bar_init(full(s), 1);
+                bar_init(empty(s), 1);
+            }
+            bar_init(done_bar, 1);
+            failed = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            prefetch_map(&g.a);
+            prefetch_map(&g.b);
+        }
+        __syncwarp();
+        pdl_wait();
+        const int32_t ix = (int32_t)(tm * 128), jx = (int32_t)(tn * 128);
+        auto half = [&](uint32_t to, const CUtensorMap *map, int32_t cols, int32_t x, int32_t c,
+                        uint32_t bar) {
+            if (cols) {
+                box_load(to, map, x, c, bar);
+                box_load(to + kHalf / 2, map, x + 64, c, bar);
+            } else {
+                box_load(to, map, c, x, bar);
+            }
+        };
+        auto load = [&](int it, int s) {
+            const int64_t kt = k0 + it;
+            const bool second = kt >= g.kt1;
+            const int32_t c = (int32_t)((second ? kt - g.kt1 : kt) * kDepth);
+            const uint32_t st = ring + s * kMidStage;
+            bar_expect(full(s), kMidStage);
+            half(st, second ? &g.a2 : &g.a, a.a_cols, ix, c, full(s));
+            half(st + kHalf, second ? &g.b2 : &g.b, a.b_cols, jx, c, full(s));
+        };
+        const int ahead = rounds < g.stages ? rounds : g.stages;
+        for (int it = 0; it < ahead; ++it)
+            if (one) load(it, it);
+        __syncthreads();
+        int s = 0;
+        uint32_t phase = 0;
+        for (int it = ahead; it < rounds; ++it) {
+            ok = bar_wait(empty(s), phase);
+            if (!ok) break;
+            if (one) load(it, s);
+            __syncwarp();
+            if (++s == g.stages) s = 0, phase ^= 1;
+        }
+    } else if (warp == 5) {                                  // the products
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         saddr(&tmem_base)), "r"(128u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncthreads();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const bool one = elect_one();
+        const uint32_t tmem = tmem_base;
+        const Layout la = layout_of(a.a_cols), lb = layout_of(a.b_cols);
+        const uint32_t desc = shape_desc<DT>(a.a_cols, a.b_cols) | ((128u >> 3) << 17) |
+                              ((128u >> 4) << 24);
+        int s = 0;
+        uint32_t phase = 0;
+        for (int it = 0; it < rounds; ++it) {
+            ok = bar_wait(full(s), phase);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (one) {
+                const uint64_t da = at(la, ring + s * kMidStage);
+                const uint64_t db = at(lb, ring + s * kMidStage + kHalf);
+                const int64_t kt = k0 + it;
+                const int64_t left = a.k - (kt >= g.kt1 ? kt - g.kt1 : kt) * kDepth;
+                const int steps = left >= kDepth ? 4 : (int)((left + 15) / 16);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q >= steps) break;
+                    mma1(tmem, da + q * la.step, db + q * lb.step, desc, it > 0 || q > 0);
+                }
+                commit(empty(s));
+            }
+            __syncwarp();
+            if (++s == g.stages) s = 0, phase ^= 1;
+        }
+        if (ok && one) commit(done_bar);
+        __syncwarp();
+    } else {                                                 // the results
+        pdl_wait();
+        __syncthreads();
+        pdl_launch_dependents();
+        ok = bar_wait(done_bar, 0);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    if (!ok) {
+        if (lane == 0) atomicAdd(&g_matmul_timeouts, 1u);
+        failed = 1;
+    }
+    __syncwarp();
+    const int64_t i0 = tm * 128, j0 = tn * 128;
+    // all copies have landed and all products have read them: the stages' place is free
+    float *part = reinterpret_cast<float *>(dyn + (ring - saddr(dyn)));
+    float *staged = part + kMidPart / 4 + warp * 32 * kStagePad;
+    if (warp < 4 && ok) {
+        const uint32_t lanes = tmem_base + ((uint32_t)(warp * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+            if (j0 + c >= a.n) break;
+            uint32_t r[32];
+            load32(lanes + c, r);
+            if (g.splits == 1) {
+                float z[32], z2[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(r[e]), z2[e] = 0.0f;
+                finish_rows<DT, ODT, false>(a, g.vec != 0, staged, i0 + warp * 32, j0 + c, z, z2);
+            } else {
+                float4 *row = reinterpret_cast<float4 *>(part + (warp * 32 + lane) * kMidPad + c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    row[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                         __uint_as_float(r[4 * e + 2]),
+                                         __uint_as_float(r[4 * e + 3]));
+            }
+        }
+    }
+    if (g.splits > 1) {
+        cluster_sync();
+        const int rows = (int)(a.m - i0 < 128 ? a.m - i0 : 128);
+        if (!failed) join<DT, ODT, false, 4>(a, part, kMidPad, g, rank, i0, j0, rows);
+        cluster_sync();       // the peers have read this block's shared memory
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
+        for (int s = 0; s < g.stages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
+    __syncthreads();
+    if (warp == 5)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(128u));
 }
 
 // ------------------------------------------------------------ the pair kernel
@@ -484,7 +885,6 @@ constexpr int kPairStages = 6;
 constexpr int kPairStage = 2 * kHalf;
 constexpr int kPairWarps = 8;                            // of results
 constexpr int kPairThreads = (kPairWarps + 2) * 32;
-constexpr int kStagePad = 33;                            // floats of a staged row
 constexpr int kPairStaged = kPairWarps * 32 * kStagePad * 4;
 constexpr int kPairSmem = kPairStages * kPairStage + kPairStaged + 1024;
 static_assert(kPairSmem <= kSmemBlock, "one block's shared memory");
@@ -493,6 +893,7 @@ struct PairArgs {
     CUtensorMap a, b, b2, a2;
     int64_t kt1, kt;                     // stages of the first pair of operands, of both
     int64_t tiles_n, tiles_m;
+    int32_t half;                        // rows of B that either block brings, at most 128
     int32_t vec;                         // finish_run's boundaries hold
 };
 
@@ -506,16 +907,12 @@ __device__ __forceinline__ void pair_tile(const PairArgs &g, int64_t t, int64_t 
     tm = band * 8 + in - tn * wide;
 }
 
-// Rows of B that either block brings for tile column tn.
-template <bool GATED> __device__ __forceinline__ int half_of(int64_t n, int64_t tn)
+// Rows of B that either block brings for tile column tn: fewer for the last one.
+template <bool GATED> __device__ __forceinline__ int half_of(const PairArgs &g, int64_t n, int64_t tn)
 {
-    if constexpr (GATED) {
-        const int64_t left = n - tn * 128;
-        return left >= 128 ? 128 : (int)((left + 15) / 16 * 16);
-    } else {
-        const int64_t left = n - tn * 256;
-        return left >= 256 ? 128 : (int)((left + 31) / 32 * 16);
-    }
+    const int64_t left = n - tn * (GATED ? g.half : 2 * g.half);
+    if constexpr (GATED) return left >= g.half ? g.half : (int)((left + 15) / 16 * 16);
+    else return left >= 2 * g.half ? g.half : (int)((left + 31) / 32 * 16);
 }
 
 template <int DT, int ODT, bool GATED>
@@ -558,14 +955,17 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
     bool ok = true;
     if (warp == kPairWarps) {                                // the copies
         const bool one = elect_one();
+        // (the transpose comes in chunks of 64 rows)
+        const int brought = (a.b_cols ? (g.half + 63) / 64 * 64 : g.half) * kLine;
         int s = 0;
         uint32_t phase = 1;                                  // the stages start empty
         for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
             int64_t tn, tm;
             pair_tile(g, t, tn, tm);
             const int32_t ix = (int32_t)(tm * 256 + rank * 128);
-            const int32_t jx = GATED ? (int32_t)(tn * 128)
-                                     : (int32_t)(tn * 256 + rank * half_of<GATED>(a.n, tn));
+            const int32_t jx = GATED ? (int32_t)(tn * g.half)
+                                     : (int32_t)(tn * 2 * g.half +
+                                                 rank * half_of<GATED>(g, a.n, tn));
             for (int64_t kt = 0; kt < g.kt; ++kt) {
                 ok = bar_wait(empty(s), phase);
                 if (!ok) break;
@@ -575,7 +975,7 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
                     const CUtensorMap *ma = second ? &g.a2 : &g.a;
                     const CUtensorMap *mb = (GATED ? rank != 0 : second) ? &g.b2 : &g.b;
                     const uint32_t st = ring + s * kPairStage, bar = peer_addr(full(s), 0);
-                    if (rank == 0) bar_expect(full(s), 2 * kPairStage);
+                    if (rank == 0) bar_expect(full(s), (uint32_t)(2 * (kHalf + brought)));
                     if (a.a_cols) {
                         tensor_load(st, ma, ix, c, bar);
                         tensor_load(st + kHalf / 2, ma, ix + 64, c, bar);
@@ -584,7 +984,8 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
                     }
                     if (a.b_cols) {
                         tensor_load(st + kHalf, mb, jx, c, bar);
-                        tensor_load(st + kHalf + kHalf / 2, mb, jx + 64, c, bar);
+                        if (g.half > 64)
+                            tensor_load(st + kHalf + kHalf / 2, mb, jx + 64, c, bar);
                     } else {
                         tensor_load(st + kHalf, mb, c, jx, bar);
                     }
@@ -604,7 +1005,7 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
             for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
                 int64_t tn, tm;
                 pair_tile(g, t, tn, tm);
-                const uint32_t desc = shape | ((uint32_t)(2 * half_of<GATED>(a.n, tn)) >> 3 << 17);
+                const uint32_t desc = shape | ((uint32_t)(2 * half_of<GATED>(g, a.n, tn)) >> 3 << 17);
                 const uint32_t acc = tmem + i * 256;
                 ok = bar_wait(drained((int)i), drained_phase);
                 if (!ok) break;
@@ -645,9 +1046,9 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
             ok = bar_wait(done((int)b), done_phase);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const int half = half_of<GATED>(a.n, tn);
+            const int half = half_of<GATED>(g, a.n, tn);
             const int64_t i0 = tm * 256 + rank * 128 + part * 32;
-            const int64_t j0 = tn * (GATED ? 128 : 256);
+            const int64_t j0 = tn * (GATED ? g.half : 2 * g.half);
             const int wide = GATED ? half : 2 * half;        // columns of the result
 #pragma unroll 1
             for (int c = turn * 32; c < wide; c += 64) {
@@ -661,35 +1062,7 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
                     z[e] = __uint_as_float(r[e]);
                     z2[e] = GATED ? __uint_as_float(r2[e]) : 0.0f;
                 }
-                const int64_t j = j0 + c;
-                if (g.vec && j + 32 <= a.n) {
-                    if (i0 + lane < a.m) finish_run<DT, ODT, GATED>(a, i0 + lane, j, z, z2);
-                    continue;
-                }
-                // rows off the boundaries, or a ragged end: through shared memory, so that
-                // a warp's accesses are consecutive
-                const float bias = a.bias && j + lane < a.n ? elems::load1<DT>(a.bias, j + lane)
-                                                            : 0.0f;
-                const int64_t rows = a.m - i0 < 32 ? a.m - i0 : 32;
-                float w2[32];
-                __syncwarp();
-                if constexpr (GATED) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) staged[lane * kStagePad + e] = z2[e];
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) w2[e] = staged[e * kStagePad + lane];
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) staged[lane * kStagePad + e] = z[e];
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (e < rows)
-                        finish_lane<DT, ODT, GATED>(a, i0 + e, j + lane, j + lane < a.n,
-                                                    staged[e * kStagePad + lane],
-                                                    GATED ? w2[e] : 0.0f, bias);
+                finish_rows<DT, ODT, GATED>(a, g.vec != 0, staged, i0, j0 + c, z, z2);
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
@@ -808,6 +1181,18 @@ cudaError_t operand_maps(const ProductArgs &a, G &g, int rows_a, int rows_b)
     return e;
 }
 
+// Whether runs of so many bytes of a row of everything that is written beside
+// the result, and of what is added, lie on their boundaries.
+bool runs_aligned(const ProductArgs &a, int64_t bytes, int out_size)
+{
+    auto rows = [&](const void *p, int64_t stride, int es) {
+        return !p || ((uintptr_t)p % bytes == 0 && stride * es % bytes == 0);
+    };
+    return rows(a.out, a.stride, out_size) && rows(a.residual, a.residual_stride, out_size) &&
+           rows(a.kept, a.kept_stride, 2) && rows(a.kept2, a.kept_stride, 2) &&
+           ((uintptr_t)a.bias & 15) == 0;
+}
+
 template <int DT, int ODT, bool GATED>
 cudaError_t pair_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
@@ -817,33 +1202,111 @@ cudaError_t pair_go(const ProductArgs &a, int sms, cudaStream_t s)
                      kSmemBlock, done);
     if (e != cudaSuccess) return e;
     PairArgs g;
-    e = operand_maps(a, g, 128, 128);
+    // The tile's width that leaves the pairs the least columns to go through, one after
+    // the other: with few tiles a pair, 256 can leave most of them idle at the end.
+    // (6400 x 1600 over 8192 columns c, 76 pairs: 175 tiles of 256 go three deep, and so do 225 of 192.)
+    // A narrower tile reads A more often: it has to save an eighth.
+    g.tiles_m = (a.m + 255) / 256;
+    int64_t least = 0;
+    for (int half = 128; half >= 64; half -= GATED ? 32 : 16) {   // blocks of 32 stay whole
+        const int64_t wide = GATED ? half : 2 * half, across = (a.n + wide - 1) / wide;
+        const int64_t deep = (across * g.tiles_m + sms / 2 - 1) / (sms / 2) * half;
+        if (half < 128 && deep * 8 > least * 7) continue;
+        least = deep;
+        g.half = half;
+        g.tiles_n = across;
+    }
+    e = operand_maps(a, g, 128, g.half);
     if (e != cudaSuccess) return e;
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
-    g.tiles_n = GATED ? (a.n + 127) / 128 : (a.n + 255) / 256;
-    g.tiles_m = (a.m + 255) / 256;
-    auto rows32 = [](const void *p, int64_t stride, int es) {
-        return !p || (((uintptr_t)p & 31) == 0 && stride * es % 32 == 0);
-    };
-    constexpr int os = ODT == F32 ? 4 : 2;
-    g.vec = rows32(a.out, a.stride, os) && rows32(a.residual, a.residual_stride, os) &&
-            rows32(a.kept, a.kept_stride, 2) && rows32(a.kept2, a.kept_stride, 2) &&
-            ((uintptr_t)a.bias & 15) == 0;
+    g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
     const int64_t tiles = g.tiles_n * g.tiles_m;
     const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
     return launch_dependent(matmul_pair_kernel<DT, ODT, GATED>, dim3((unsigned)(2 * pairs)),
                             dim3(kPairThreads), kSmemBlock, s, a, g);
 }
 
-template <int DT, int ODT, bool GATED, int NT, bool ACOLS>
+// A launch in clusters of `splits` blocks.
+struct Clusters {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Clusters(int64_t blocks, int splits, int smem, cudaStream_t s)
+    {
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(kOneThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)splits;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
+
+// How many clusters of `splits` blocks of a kernel find a place at once: fewer than
+// the SMs' number says, because a cluster's blocks share a group of SMs.  Asked for once
+// for each split and ring length (every device of this build's kind has the same).
+struct Room {
+    std::atomic<int> known[9][16] = {};
+    int of(const void *kernel, int splits, int stages, int smem)
+    {
+        std::atomic<int> &at = known[splits][stages];
+        int n = at.load(std::memory_order_relaxed);
+        if (n) return n - 1;
+        Clusters c(splits, splits, smem, nullptr);
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &c.cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        at.store(n + 1, std::memory_order_relaxed);
+        return n;
+    }
+};
+
+// The split and the ring's length that leave the fullest SM the fewest stages, a join
+// counting as kJoin of them, as long as all clusters find a place at once.
+// `smem(stages)`: a block's shared memory; `most`: stages of the longest ring.
+template <class Smem>
+void choose_split(OneArgs &g, int64_t tiles, int sms, const void *kernel, Room &room, int most,
+                  int blocks_sm, Smem smem)
+{
+    constexpr int kJoin = 4;
+    auto ring = [&](int splits, int per_sm) {
+        const int64_t rounds = (g.kt + splits - 1) / splits;
+        int st = rounds < 1 ? 1 : rounds < most ? (int)rounds : most;
+        while (st > 0 && (smem(st) + 1024) * per_sm > kSmemSm) --st;
+        return st;
+    };
+    g.splits = 1;
+    g.stages = ring(1, 1);
+    int64_t least = (tiles + sms - 1) / sms * g.kt;
+    for (int n = 2; n <= 8 && g.kt >= 2 * n; ++n) {
+        const int64_t per_sm = (tiles * n + sms - 1) / sms;
+        if (per_sm > blocks_sm) break;
+        const int64_t rounds = (g.kt + n - 1) / n, cost = per_sm * rounds + kJoin;
+        if (cost >= least) continue;
+        // (blocks that share an SM want three stages at least to keep their copies coming)
+        const int st = ring(n, (int)per_sm);
+        if (st < 1 || (st < 3 && st < rounds) || room.of(kernel, n, st, smem(st)) < tiles) continue;
+        least = cost;
+        g.splits = n;
+        g.stages = st;
+    }
+}
+
+template <int DT, int ODT, bool GATED, int NT>
 cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
-    using Tl = Tile<NT, GATED, ACOLS>;
+    using Tl = Tile<NT, GATED>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e =
-        allow_shared(reinterpret_cast<const void *>(matmul_kernel<DT, ODT, GATED, NT, ACOLS>),
-                     Tl::smem(Tl::kStages), done);
+    static Room room;
+    const auto kernel = matmul_kernel<DT, ODT, GATED, NT>;
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSmemBlock, done);
     if (e != cudaSuccess) return e;
     OneArgs g;
     e = operand_maps(a, g, NT, 128);
@@ -851,57 +1314,89 @@ cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
     g.tiles_n = (a.n + 127) / 128;
+    g.vec = runs_aligned(a, ODT == F32 ? 16 : 8, ODT == F32 ? 4 : 2);
+    g.span = a.m < NT ? (int)((a.m + 15) / 16 * 16) : NT;
     const int64_t tiles = g.tiles_n * ((a.m + NT - 1) / NT);
-    // The split that leaves the fullest SM the fewest stages, a join counting
-    // as kJoin of them, as long as all blocks find a place at once.
-    constexpr int kJoin = 4;
-    auto stages = [&](int splits) {
-        const int64_t most = (g.kt + splits - 1) / splits;
-        return most < 1 ? 1 : most < Tl::kStages ? (int)most : Tl::kStages;
-    };
-    g.splits = 1;
-    int64_t least = (tiles + sms - 1) / sms * g.kt;
-    for (int n = 2; n <= 8 && g.kt >= 2 * n; n *= 2) {
-        const int64_t per_sm = (tiles * n + sms - 1) / sms;
-        if (per_sm > kSmemSm / (Tl::smem(stages(n)) + 1024)) break;
-        const int64_t cost = per_sm * ((g.kt + n - 1) / n) + kJoin;
-        if (cost < least) least = cost, g.splits = n;
-    }
-    g.stages = stages(g.splits);
+    choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room, Tl::kStages,
+                 kMostBlocks, [&](int stages) { return Tl::smem(stages, g.span); });
     const int64_t blocks = tiles * g.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kOneThreads);
-    cfg.dynamicSmemBytes = Tl::smem(g.stages);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)g.splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, matmul_kernel<DT, ODT, GATED, NT, ACOLS>, a, g);
+    Clusters c(blocks, g.splits, Tl::smem(g.stages, g.span), s);
+    return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
+}
+
+template <int DT, int ODT> cudaError_t mid_go(const ProductArgs &a, int sms, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    static Room room;
+    const auto kernel = matmul_mid_kernel<DT, ODT>;
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSmemBlock, done);
+    if (e != cudaSuccess) return e;
+    OneArgs g;
+    e = operand_maps(a, g, 128, 128);
+    if (e != cudaSuccess) return e;
+    g.kt1 = (a.k + kDepth - 1) / kDepth;
+    g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
+    g.tiles_n = (a.n + 127) / 128;
+    g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
+    g.span = 128;
+    const int64_t tiles = g.tiles_n * ((a.m + 127) / 128);
+    choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room, kMidStages, 2,
+                 mid_smem);
+    const int64_t blocks = tiles * g.splits;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    Clusters c(blocks, g.splits, mid_smem(g.stages), s);
+    return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
+}
+
+// Whether the rows of A are so few that matvec_kernel takes the product.
+bool few_rows(const ProductArgs &a)
+{
+    return a.m <= 4 && a.k > 0 && !a.a_cols && !a.b_cols && !a.a2;
+}
+
+template <int DT, int ODT, bool GATED, int M>
+cudaError_t matvec_go(const ProductArgs &a, int sms, cudaStream_t s)
+{
+    const rows::In x = rows::in(a.a, a.m, a.k, a.a_stride, DT);
+    const rows::In w = rows::in(a.b, a.n, a.k, a.b_stride, DT);
+    const rows::In w2 = rows::in(a.b2, a.n, a.k, a.b2_stride, DT);
+    const bool vec = rows_aligned(a.a, a.a_stride, DT, a.k) &&
+                     rows_aligned(a.b, a.b_stride, DT, a.k) &&
+                     (!a.b2 || rows_aligned(a.b2, a.b2_stride, DT, a.k));
+    const int64_t blocks = (a.n + 31) / 32;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    // 16 warps an SM or more, as long as each has a few strides of its row
+    const int ks = blocks * 8 >= (int64_t)sms * 16 || a.k < 1024 ? 1
+                   : blocks * 16 >= (int64_t)sms * 16 || a.k < 2048 ? 2 : 4;
+    auto go = [&](auto k, int threads) {
+        return launch_dependent(k, dim3((unsigned)blocks), dim3(threads), 0, s, a, x, w, w2);
+    };
+    if (!vec) return ks == 1 ? go(matvec_kernel<DT, ODT, GATED, M, 1, false>, 256)
+                             : go(matvec_kernel<DT, ODT, GATED, M, 2, false>, 512);
+    if (ks == 1) return go(matvec_kernel<DT, ODT, GATED, M, 1, true>, 256);
+    if constexpr (M == 1)
+        if (ks == 4) return go(matvec_kernel<DT, ODT, GATED, M, 4, true>, 1024);
+    return go(matvec_kernel<DT, ODT, GATED, M, 2, true>, 512);
 }
 
 template <int DT, int ODT, bool GATED>
 cudaError_t pick(const ProductArgs &a, int sms, cudaStream_t s)
 {
+    if (few_rows(a))
+        return a.m == 1 ? matvec_go<DT, ODT, GATED, 1>(a, sms, s)
+                        : matvec_go<DT, ODT, GATED, 4>(a, sms, s);
     // Few rows, or no more tiles of 128 by 128 than SMs: the single blocks, whose
     // columns c can be split.  Beyond that the pairs.
     const int64_t tiles = ((a.n + 127) / 128) * ((a.m + 127) / 128);
     if (a.k > 0 && a.m > 64 && tiles > sms) return pair_go<DT, ODT, GATED>(a, sms, s);
-    if constexpr (!GATED) {
-        if (a.a_cols)
-            return a.m <= 64 ? one_go<DT, ODT, GATED, 64, true>(a, sms, s)
-                             : one_go<DT, ODT, GATED, 128, true>(a, sms, s);
+    if constexpr (GATED) {
+        if (a.m > 64) return one_go<DT, ODT, GATED, 128>(a, sms, s);
+    } else {
+        if (a.k > 0 && (a.m > 64 || a.a_cols)) return mid_go<DT, ODT>(a, sms, s);
     }
-    return a.m <= 16 ? one_go<DT, ODT, GATED, 16, false>(a, sms, s)
-           : a.m <= 64 ? one_go<DT, ODT, GATED, 64, false>(a, sms, s)
-                       : one_go<DT, ODT, GATED, 128, false>(a, sms, s);
+    return a.m <= 16 ? one_go<DT, ODT, GATED, 16>(a, sms, s)
+                     : one_go<DT, ODT, GATED, 64>(a, sms, s);
 }
 
 // An operand's place in the workspace, if it needs one: bytes.
@@ -922,6 +1417,7 @@ bool on_boundaries(const void *p, int64_t rows, int64_t stride)
 
 int64_t product_workspace(const ProductArgs &a)
 {
+    if (few_rows(a)) return 0;
     int64_t need = 0;
     auto add = [&](const void *p, int64_t rows, int32_t cols, int64_t stride) {
         const Place at = cols ? Place{a.k, rows, stride} : Place{rows, a.k, stride};
@@ -938,7 +1434,7 @@ cudaError_t launch_product(int32_t dt, int32_t odt, ProductArgs a, void *workspa
                            cudaStream_t s)
 {
     if (a.m <= 0 || a.n <= 0) return cudaSuccess;
-    if (a.k > 0) {
+    if (a.k > 0 && !few_rows(a)) {
         char *room = static_cast<char *>(workspace);
         cudaError_t e = cudaSuccess;
         auto settle = [&](const void *&p, int64_t rows, int32_t cols, int64_t &stride) {

@@ -133,6 +133,19 @@ __device__ __forceinline__ void put_eight(const View &q, int64_t r, int64_t j, b
     if ((threadIdx.x & 3) == 0) q.scales[r * (q.wide / kBlock) + j / kBlock] = (unsigned char)e;
 }
 
+// Eight neighbouring lanes hold them, 4 each: lane l's from column j on.
+__device__ __forceinline__ void put_four(const View &q, int64_t r, int64_t j, bool in,
+                                         const float (&v)[4])
+{
+    uint32_t top = max(max(magnitude(v[0]), magnitude(v[1])), max(magnitude(v[2]), magnitude(v[3])));
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (!in) return;
+    const uint32_t e = exponent(top);
+    *reinterpret_cast<uint32_t *>(q.codes + r * q.wide + j) = codes4(v, down(e));
+    if ((threadIdx.x & 7) == 0) q.scales[r * (q.wide / kBlock) + j / kBlock] = (unsigned char)e;
+}
+
 // Eight elements of row r from column j on (a whole eight below the pitch).
 template <int DT>
 __device__ __forceinline__ void get_eight(const View &q, int64_t r, int64_t j, float (&v)[8])

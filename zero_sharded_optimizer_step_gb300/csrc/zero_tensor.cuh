@@ -101,8 +101,10 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+// (The barrier's instructions want their warp converged.)
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
