@@ -560,7 +560,8 @@ else:
     _calls.bind_layers(*(ctypes.cast(getattr(_L, _name), _vp).value for _name in (
         "zero_pack8", "zero_unpack8", "zero_rms_norm", "zero_rms_norm_grad",
         "zero_matmul_workspace", "zero_matmul", "zero_gated_workspace", "zero_gated",
-        "zero_activation_grad", "zero_gated_grad")))
+        "zero_activation_grad", "zero_gated_grad", "zero_pack8_bytes",
+        "zero_rms_norm_grad_workspace", "zero_activation_grad_workspace")))
 
 
 def zero_embed(table, dtype: int, rows: int, dim: int, table_stride: int, tokens,
@@ -634,7 +635,7 @@ def zero_mx4_timeouts() -> int:
 
 
 def zero_pack8_bytes(rows: int, cols: int) -> int:
-    return _L.zero_pack8_bytes(rows, cols)
+    return _calls.pack8_bytes(rows, cols)
 
 
 def zero_pack8(x, dtype: int, rows: int, cols: int, stride: int, q, stream=None) -> None:
@@ -662,7 +663,7 @@ def zero_rms_norm(x, x_stride: int, residual, residual_stride: int, weight, dtyp
 
 
 def zero_rms_norm_grad_workspace(rows: int, dim: int) -> int:
-    return _L.zero_rms_norm_grad_workspace(rows, dim)
+    return _calls.norm_workspace(rows, dim)
 
 
 def zero_rms_norm_grad(dy, dy_stride: int, dsum, dsum_stride: int, sum, sum_stride: int, weight,
@@ -712,7 +713,7 @@ def zero_gated(x, x_stride: int, w_gate, gate_stride: int, w_up, up_stride: int,
 
 
 def zero_activation_grad_workspace(rows: int, cols: int) -> int:
-    return _L.zero_activation_grad_workspace(rows, cols)
+    return _calls.activation_workspace(rows, cols)
 
 
 def zero_activation_grad(dy, dy_stride: int, kept, kept_stride: int, kept_q, activation: int,

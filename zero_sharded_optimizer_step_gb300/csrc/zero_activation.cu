@@ -11,6 +11,7 @@
 #include "zero_ops.h"
 #include "zero_pack8.cuh"
 #include "zero_rows.cuh"
+#include "zero_tensor.cuh"
 
 namespace zgb {
 namespace {
@@ -60,10 +61,22 @@ struct ActGrad {
     void *dz;
     int64_t dz_stride;
     float *parts;                                // [gridDim.y][cols], or null
+    void *dbias;                                 // ONE: the sums go here at once
+    int32_t bias_dtype, accumulate;
 };
 
+__device__ __forceinline__ void put_sum(void *out, int32_t dt, int64_t c, float v, bool accumulate)
+{
+    if (dt == F32) elems::store1<F32>(out, c, accumulate ? __fadd_rn(elems::load1<F32>(out, c), v) : v);
+    else if (dt == BF16)
+        elems::store1<BF16>(out, c, accumulate ? __fadd_rn(elems::load1<BF16>(out, c), v) : v);
+    else elems::store1<F16>(out, c, accumulate ? __fadd_rn(elems::load1<F16>(out, c), v) : v);
+}
+
 // A block takes a strip of 256 columns and every gridDim.y-th eight of its rows.
-template <int DT, bool VEC, bool PACKED>
+// ONE: a strip's blocks are a cluster, whose first block adds up the sums of all through
+// distributed shared memory, in their order; otherwise a second kernel does.
+template <int DT, bool VEC, bool PACKED, bool ONE>
 __global__ void __launch_bounds__(kThreads)
 activation_grad_kernel(const __grid_constant__ ActGrad a)
 {
@@ -107,26 +120,39 @@ activation_grad_kernel(const __grid_constant__ ActGrad a)
             for (int e = 0; e < 8; ++e) sum[e] = __fadd_rn(sum[e], d[e]);
         }
     }
-    if (!a.parts) return;
+    if (!a.parts && !a.dbias) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) joined[warp][lane * 8 + e] = sum[e];
     __syncthreads();
     const int64_t c = c0 + threadIdx.x;
-    if (c < a.cols) {
-        float v = joined[0][threadIdx.x];
+    float v = joined[0][threadIdx.x];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) v = __fadd_rn(v, joined[i][threadIdx.x]);
-        a.parts[(int64_t)blockIdx.y * a.cols + c] = v;
+    for (int i = 1; i < kWarps; ++i) v = __fadd_rn(v, joined[i][threadIdx.x]);
+    if constexpr (ONE) {
+        __shared__ float total[256];
+        total[threadIdx.x] = v;
+        cluster_sync();
+        if (blockIdx.y == 0) {
+            for (uint32_t p = 1; p < gridDim.y; ++p)
+                v = __fadd_rn(v, load_peer(saddr(&total[threadIdx.x]), p));
+            if (c < a.cols) put_sum(a.dbias, a.bias_dtype, c, v, a.accumulate != 0);
+        }
+        cluster_sync();                          // the first block has read them
+    } else {
+        if (c < a.cols) a.parts[(int64_t)blockIdx.y * a.cols + c] = v;
     }
 }
 
 constexpr int64_t kBlocks = 152 * 8;             // about eight a SM
+constexpr int64_t kOneRows = 256;
 
 int64_t act_parts(int64_t n, int64_t cols)
 {
     const int64_t strips = (cols + 255) / 256, most = (n + kWarps - 1) / kWarps;
     int64_t parts = (kBlocks + strips - 1) / strips;
     parts = parts < most ? parts : most;
+    // with few rows eight blocks, a cluster, can do it in one launch
+    if (n <= kOneRows) parts = most < 8 ? most : 8;
     return parts < 1 ? 1 : parts < 65535 ? parts : 65535;
 }
 
@@ -141,37 +167,49 @@ struct GatedGrad {
     int64_t grad_stride, h_stride;
 };
 
+// Runs of 256 columns that a warp asks for together, so that enough bytes are on their way.
+template <int DT> constexpr int kRuns = DT == F32 ? 1 : 2;
+
 template <int DT, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(kThreads)
 gated_grad_kernel(const __grid_constant__ GatedGrad a)
 {
+    constexpr int U = kRuns<DT>;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t r = w / a.runs, c0 = (w - r * a.runs) * 256;
-    if (r >= a.n) return;
-    rows::Eight<DT, VEC> dhe;
-    Kept<DT, VEC, PACKED> ge, ue;
-    dhe.ask(a.dh, r, c0, a.cols);
-    ge.ask(a.g, a.gq, r, c0, a.cols);
-    ue.ask(a.u, a.uq, r, c0, a.cols);
-    float dh[8], g[8], u[8], f[8], d[8];
-    dhe.take(dh);
-    ge.take(g);
-    ue.take(u);
-    act::with_kind(a.act, [&](auto kind) {
+    const int64_t w = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * U;
+    int64_t r[U], c0[U];
+    rows::Eight<DT, VEC> dhe[U];
+    Kept<DT, VEC, PACKED> ge[U], ue[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float slope;
-            act::both(g[e], decltype(kind)::value, f[e], slope);
-            d[e] = __fmul_rn(__fmul_rn(dh[e], u[e]), slope);
-            dh[e] = __fmul_rn(dh[e], f[e]);
-            f[e] = __fmul_rn(f[e], u[e]);
-        }
-    });
-    rows::put<DT, VEC>(a.dg, a.grad_stride, r, c0, a.cols, d);
-    rows::put<DT, VEC>(a.du, a.grad_stride, r, c0, a.cols, dh);
-    if (a.h) rows::put<DT, VEC>(a.h, a.h_stride, r, c0, a.cols, f);
+    for (int k = 0; k < U; ++k) {
+        rows::run_at(w + k, a.runs, r[k], c0[k]);
+        if (r[k] >= a.n) break;
+        dhe[k].ask(a.dh, r[k], c0[k], a.cols);
+        ge[k].ask(a.g, a.gq, r[k], c0[k], a.cols);
+        ue[k].ask(a.u, a.uq, r[k], c0[k], a.cols);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (r[k] >= a.n) break;
+        float dh[8], g[8], u[8], f[8], d[8];
+        dhe[k].take(dh);
+        ge[k].take(g);
+        ue[k].take(u);
+        act::with_kind(a.act, [&](auto kind) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float slope;
+                act::both(g[e], decltype(kind)::value, f[e], slope);
+                d[e] = __fmul_rn(__fmul_rn(dh[e], u[e]), slope);
+                dh[e] = __fmul_rn(dh[e], f[e]);
+                f[e] = __fmul_rn(f[e], u[e]);
+            }
+        });
+        rows::put<DT, VEC>(a.dg, a.grad_stride, r[k], c0[k], a.cols, d);
+        rows::put<DT, VEC>(a.du, a.grad_stride, r[k], c0[k], a.cols, dh);
+        if (a.h) rows::put<DT, VEC>(a.h, a.h_stride, r[k], c0[k], a.cols, f);
+    }
 }
 
 // -------------------------------------------------------------- rows in 8 bits
@@ -181,17 +219,25 @@ __global__ void __launch_bounds__(kThreads)
 pack8_kernel(const __grid_constant__ rows::In x, const __grid_constant__ pack8::View q,
              int64_t n, int64_t cols, int64_t runs)
 {
+    constexpr int U = kRuns<DT>;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t r = w / runs, c0 = (w - r * runs) * 256;
-    if (r >= n) return;
-    rows::Eight<DT, VEC> e;
-    e.ask(x, r, c0, cols);
-    float f[8];
-    e.take(f);
-    const int64_t c = c0 + 8 * (threadIdx.x & 31);
-    pack8::put_eight(q, r, c, c < q.wide, f);
+    const int64_t w = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * U;
+    int64_t r[U], c0[U];
+    rows::Eight<DT, VEC> e[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        rows::run_at(w + k, runs, r[k], c0[k]);
+        if (r[k] < n) e[k].ask(x, r[k], c0[k], cols);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (r[k] >= n) break;
+        float f[8];
+        e[k].take(f);
+        const int64_t c = c0[k] + 8 * (threadIdx.x & 31);
+        pack8::put_eight(q, r[k], c, c < q.wide, f);
+    }
 }
 
 template <int DT, bool VEC>
@@ -199,15 +245,24 @@ __global__ void __launch_bounds__(kThreads)
 unpack8_kernel(const __grid_constant__ pack8::View q, int64_t n, int64_t cols, int64_t runs,
                void *out, int64_t stride)
 {
+    constexpr int U = kRuns<DT>;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t r = w / runs, c0 = (w - r * runs) * 256;
-    if (r >= n) return;
-    const int64_t c = c0 + 8 * (threadIdx.x & 31);
-    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (c < q.wide) pack8::get_eight<DT>(q, r, c, f);
-    rows::put<DT, VEC>(out, stride, r, c0, cols, f);
+    const int64_t w = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * U;
+    int64_t r[U], c0[U];
+    Kept<DT, VEC, true> e[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        rows::run_at(w + k, runs, r[k], c0[k]);
+        if (r[k] < n) e[k].ask(rows::In{}, q, r[k], c0[k], cols);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (r[k] >= n) break;
+        float f[8];
+        e[k].take(f);
+        rows::put<DT, VEC>(out, stride, r[k], c0[k], cols, f);
+    }
 }
 
 // ----------------------------------------------------------------- column sums
@@ -250,10 +305,11 @@ template <class F> cudaError_t by_type(int32_t dt, F f)
                         : f(std::integral_constant<int, F16>{});
 }
 
-// Blocks of eight warps for so many runs of 256 columns; 0 where there are too many.
-unsigned run_blocks(int64_t n, int64_t runs)
+// Blocks for so many runs of 256 columns; 0 where there are too many.
+unsigned run_blocks(int32_t dt, int64_t n, int64_t runs)
 {
-    const int64_t blocks = (n * runs + kWarps - 1) / kWarps;
+    const int64_t of = kWarps * (dt == F32 ? kRuns<F32> : kRuns<BF16>);
+    const int64_t blocks = (n * runs + of - 1) / of;
     return blocks > 0x7fffffff ? 0 : (unsigned)blocks;
 }
 
@@ -280,23 +336,42 @@ cudaError_t launch_activation_grad(int32_t dt, int32_t bdt, const ActGradArgs &a
     if (a.cols <= 0) return cudaSuccess;
     const int64_t parts = act_parts(a.rows, a.cols);
     if (a.rows > 0) {
+        const bool one = a.dbias && a.rows <= kOneRows;
         ActGrad g = {rows::in(a.dy, a.rows, a.cols, a.dy_stride, dt),
                      rows::in(a.kept, a.rows, a.cols, a.kept_stride, dt),
                      pack8::view(a.kept_q, a.rows, a.cols), a.rows, a.cols, a.act, a.dz,
-                     a.dz_stride, a.dbias ? workspace : nullptr};
+                     a.dz_stride, a.dbias && !one ? workspace : nullptr,
+                     one ? a.dbias : nullptr, bdt, a.accumulate};
         const bool vec = rows_aligned(a.dy, a.dy_stride, dt, a.cols) &&
                          (!a.kept || rows_aligned(a.kept, a.kept_stride, dt, a.cols)) &&
                          (!a.dz || rows_aligned(a.dz, a.dz_stride, dt, a.cols));
         const dim3 grid((unsigned)((a.cols + 255) / 256), (unsigned)parts);
         const cudaError_t e = by_type(dt, [&](auto t) {
             constexpr int DT = decltype(t)::value;
-            auto k = a.kept_q ? (vec ? activation_grad_kernel<DT, true, true>
-                                     : activation_grad_kernel<DT, false, true>)
-                              : (vec ? activation_grad_kernel<DT, true, false>
-                                     : activation_grad_kernel<DT, false, false>);
-            return launch_dependent(k, grid, dim3(kThreads), 0, s, g);
+            auto pick = [&](auto joined) {
+                constexpr bool ONE = decltype(joined)::value;
+                return a.kept_q ? (vec ? activation_grad_kernel<DT, true, true, ONE>
+                                       : activation_grad_kernel<DT, false, true, ONE>)
+                                : (vec ? activation_grad_kernel<DT, true, false, ONE>
+                                       : activation_grad_kernel<DT, false, false, ONE>);
+            };
+            if (!one) return launch_dependent(pick(std::false_type{}), grid, dim3(kThreads), 0, s, g);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = grid;
+            cfg.blockDim = dim3(kThreads);
+            cfg.stream = s;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = 1;
+            attr[1].val.clusterDim.y = (unsigned)parts;
+            attr[1].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            return cudaLaunchKernelEx(&cfg, pick(std::true_type{}), g);
         });
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || one) return e;
     }
     if (!a.dbias) return cudaSuccess;
     return launch_column_sums(bdt, workspace, a.rows > 0 ? parts : 0, a.cols, a.dbias,
@@ -318,7 +393,7 @@ cudaError_t launch_gated_grad(int32_t dt, const GatedGradArgs &a, cudaStream_t s
                      rows_aligned(a.dgate, a.grad_stride, dt, a.cols) &&
                      rows_aligned(a.dup, a.grad_stride, dt, a.cols) &&
                      (!a.h || rows_aligned(a.h, a.h_stride, dt, a.cols));
-    const unsigned blocks = run_blocks(a.rows, runs);
+    const unsigned blocks = run_blocks(dt, a.rows, runs);
     if (!blocks) return cudaErrorInvalidValue;
     return by_type(dt, [&](auto t) {
         constexpr int DT = decltype(t)::value;
@@ -340,7 +415,7 @@ cudaError_t launch_pack8(int32_t dt, const void *x, int64_t rows, int64_t cols, 
 {
     if (rows <= 0 || cols <= 0) return cudaSuccess;
     const int64_t runs = (cols + 255) / 256;
-    const unsigned blocks = run_blocks(rows, runs);
+    const unsigned blocks = run_blocks(dt, rows, runs);
     if (!blocks) return cudaErrorInvalidValue;
     const rows::In in = rows::in(x, rows, cols, stride, dt);
     const bool vec = rows_aligned(x, stride, dt, cols);
@@ -357,7 +432,7 @@ cudaError_t launch_unpack8(int32_t dt, const unsigned char *q, int64_t rows, int
 {
     if (rows <= 0 || cols <= 0) return cudaSuccess;
     const int64_t runs = (cols + 255) / 256;
-    const unsigned blocks = run_blocks(rows, runs);
+    const unsigned blocks = run_blocks(dt, rows, runs);
     if (!blocks) return cudaErrorInvalidValue;
     const bool vec = rows_aligned(out, stride, dt, cols);
     return by_type(dt, [&](auto t) {

@@ -253,9 +253,12 @@ static struct {
     __typeof__(&zero_gated) gated;
     __typeof__(&zero_activation_grad) activation_grad;
     __typeof__(&zero_gated_grad) gated_grad;
+    __typeof__(&zero_pack8_bytes) pack8_bytes;
+    __typeof__(&zero_rms_norm_grad_workspace) norm_workspace;
+    __typeof__(&zero_activation_grad_workspace) activation_workspace;
 } layers;
 
-enum { LAYERS = 10, MOST = 28 };
+enum { LAYERS = 13, MOST = 28 };
 
 typedef union {
     void *p;
@@ -375,6 +378,30 @@ static PyObject *gated_grad(PyObject *self, PyObject *const *at, Py_ssize_t n)
                            v[16].p));
 }
 
+static PyObject *pack8_bytes(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "ll", (void *)layers.pack8_bytes, v)) return NULL;
+    SIZE(layers.pack8_bytes(v[0].l, v[1].l));
+}
+
+static PyObject *norm_workspace(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "ll", (void *)layers.norm_workspace, v)) return NULL;
+    SIZE(layers.norm_workspace(v[0].l, v[1].l));
+}
+
+static PyObject *activation_workspace(PyObject *self, PyObject *const *at, Py_ssize_t n)
+{
+    args_t a;
+    slot v[MOST];
+    if (!take(&a, at, n, "ll", (void *)layers.activation_workspace, v)) return NULL;
+    SIZE(layers.activation_workspace(v[0].l, v[1].l));
+}
+
 /* bind_layers(): the addresses of the functions above, in their order. */
 static PyObject *bind_layers(PyObject *self, PyObject *const *at, Py_ssize_t n)
 {
@@ -393,6 +420,9 @@ static PyObject *bind_layers(PyObject *self, PyObject *const *at, Py_ssize_t n)
     layers.gated = (__typeof__(layers.gated))p[7];
     layers.activation_grad = (__typeof__(layers.activation_grad))p[8];
     layers.gated_grad = (__typeof__(layers.gated_grad))p[9];
+    layers.pack8_bytes = (__typeof__(layers.pack8_bytes))p[10];
+    layers.norm_workspace = (__typeof__(layers.norm_workspace))p[11];
+    layers.activation_workspace = (__typeof__(layers.activation_workspace))p[12];
     Py_RETURN_NONE;
 }
 
@@ -411,6 +441,9 @@ static PyMethodDef methods[] = {METHOD(bind),     METHOD(embed),      METHOD(emb
                                 METHOD(gated),
                                 METHOD(activation_grad),
                                 METHOD(gated_grad),
+                                METHOD(pack8_bytes),
+                                METHOD(norm_workspace),
+                                METHOD(activation_workspace),
                                 {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", NULL, -1, methods,

@@ -191,75 +191,96 @@ struct NormGrad {
     float *parts;                                // [blocks][dim], or null
 };
 
-// Blocks stride over the rows; a thread adds up its columns' part of dw in
-// registers, and the block's row groups join theirs at the end.
+// A row's three matrices, a thread's share.
+template <int DT, int G, bool VEC> struct GradRow {
+    rows::Eight<DT, VEC> dy[G], s[G], ds[G];
+    float rstd;
+
+    __device__ __forceinline__ void ask(const NormGrad &a, int64_t row, int64_t first)
+    {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            dy[g].ask(a.dy, row, first + g * 256, a.dim);
+            s[g].ask(a.s, row, first + g * 256, a.dim);
+            if (a.ds.p) ds[g].ask(a.ds, row, first + g * 256, a.dim);
+        }
+        rstd = a.rstd[row];
+    }
+};
+
+// Groups of W warps stride over the rows, the next row on its way while one is worked
+// on; a thread adds up its columns' part of dw in registers, and the block's
+// groups join theirs at the end.
 template <int DT, int W, int G, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(W > 8 ? W * 32 : kThreads)
 norm_grad_kernel(const __grid_constant__ NormGrad a)
 {
-    constexpr int kGroups = kWarps / W;
-    __shared__ float shared[kWarps];
+    constexpr int kAll = W > 8 ? W : 8, kGroups = kAll / W;
+    __shared__ float shared[2][kAll];
     pdl_wait();
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / W;
     const int64_t first = (int64_t)(warp % W) * (G * 256);
-    rows::Eight<DT, VEC> we[G];
+    const float inv_dim = __fdiv_rn(1.0f, (float)a.dim);
     float dw[G][8];
+    rows::Eight<DT, VEC> we[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         we[g].ask(a.w, 0, first + g * 256, a.dim);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[g][e] = 0.0f;
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.n; r0 += (int64_t)gridDim.x * kGroups) {
-        const int64_t row = r0 + warp / W;
-        const bool live = row < a.n;
-        rows::Eight<DT, VEC> dye[G], se[G], dse[G];
-        float rstd = 0.0f, share = 0.0f;
-        if (live) {
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    int64_t row = (int64_t)blockIdx.x * kGroups + group;
+    GradRow<DT, G, VEC> now, next;
+    if (row < a.n) now.ask(a, row, first);
+    for (int turn = 0; row < a.n; row += step, turn ^= 1) {
+        if (row + step < a.n) next.ask(a, row + step, first);
+        const float rstd = now.rstd;
+        float share = 0.0f;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                dye[g].ask(a.dy, row, first + g * 256, a.dim);
-                se[g].ask(a.s, row, first + g * 256, a.dim);
-                if (a.ds.p) dse[g].ask(a.ds, row, first + g * 256, a.dim);
-            }
-            rstd = a.rstd[row];
+        for (int g = 0; g < G; ++g) {
+            float dy[8], n[8], w[8];
+            now.dy[g].take(dy);
+            now.s[g].take(n);
+            we[g].take(w);
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float dy[8], n[8], w[8];
-                dye[g].take(dy);
-                se[g].take(n);
-                we[g].take(w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    n[e] = __fmul_rn(n[e], rstd);
-                    dw[g][e] = __fmaf_rn(dy[e], n[e], dw[g][e]);
-                    share = __fmaf_rn(__fmul_rn(dy[e], w[e]), n[e], share);
-                }
+            for (int e = 0; e < 8; ++e) {
+                n[e] = __fmul_rn(n[e], rstd);
+                dw[g][e] = __fmaf_rn(dy[e], n[e], dw[g][e]);
+                share = __fmaf_rn(__fmul_rn(dy[e], w[e]), n[e], share);
             }
         }
-        share = __fdiv_rn(row_sum<W>(share, shared), (float)a.dim);
-        if (live) {
+        share = rows::warp_sum(share);
+        if constexpr (W > 1) {
+            // (two rows' sums in turn: one barrier of the group a row is enough)
+            if (lane == 0) shared[turn][warp] = share;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(W * 32) : "memory");
+            share = shared[turn][group * W];
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float dy[8], n[8], w[8], d[8];
-                dye[g].take(dy);
-                se[g].take(n);
-                we[g].take(w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    n[e] = __fmul_rn(n[e], rstd);
-                    d[e] = __fmul_rn(rstd, __fmaf_rn(-n[e], share, __fmul_rn(dy[e], w[e])));
-                }
-                if (a.ds.p) {
-                    float f[8];
-                    dse[g].take(f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] = __fadd_rn(d[e], f[e]);
-                }
-                rows::put<DT, VEC>(a.dx, a.dx_stride, row, first + g * 256, a.dim, d);
-            }
+            for (int i = 1; i < W; ++i) share = __fadd_rn(share, shared[turn][group * W + i]);
         }
+        share = __fmul_rn(share, inv_dim);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float dy[8], n[8], w[8], d[8];
+            now.dy[g].take(dy);
+            now.s[g].take(n);
+            we[g].take(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                n[e] = __fmul_rn(n[e], rstd);
+                d[e] = __fmul_rn(rstd, __fmaf_rn(-n[e], share, __fmul_rn(dy[e], w[e])));
+            }
+            if (a.ds.p) {
+                float f[8];
+                now.ds[g].take(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[e] = __fadd_rn(d[e], f[e]);
+            }
+            rows::put<DT, VEC>(a.dx, a.dx_stride, row, first + g * 256, a.dim, d);
+        }
+        now = next;
     }
     if (!a.parts) return;
     float *part = a.parts + (int64_t)blockIdx.x * a.dim;
@@ -273,12 +294,11 @@ norm_grad_kernel(const __grid_constant__ NormGrad a)
             }
     } else {
         __shared__ float joined[kGroups * W * G * 256];
-        __syncthreads();
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                joined[(warp / W) * (W * G * 256) + (int)first + g * 256 + lane * 8 + e] = dw[g][e];
+                joined[group * (W * G * 256) + (int)first + g * 256 + lane * 8 + e] = dw[g][e];
         __syncthreads();
         for (int c = threadIdx.x; c < a.dim; c += kThreads) {
             float v = joined[c];
@@ -370,17 +390,20 @@ norm_grad_strips_kernel(const __grid_constant__ NormGrad a)
     }
 }
 
-constexpr int kMostBlocks = 608;                 // four on each of 152 SMs
+constexpr int kMostBlocks = 304;                 // two on each of 152 SMs
 constexpr int kStripParts = 16;
 
-// Which of a row's forms a width takes: warps a row.
-int row_warps(int64_t dim) { return dim <= 1024 ? 1 : 8; }
+// Warps that share a row of this width, 512 elements each (768 alone in a warp).
+int row_warps(int64_t dim)
+{
+    return dim <= 768 ? 1 : dim <= 1024 ? 2 : dim <= 2048 ? 4 : dim <= 4096 ? 8 : 16;
+}
 
 template <int DT, int W, int G, bool VEC>
 cudaError_t grad_go(const NormGrad &a, int64_t parts, cudaStream_t s)
 {
-    return launch_dependent(norm_grad_kernel<DT, W, G, VEC>, dim3((unsigned)parts), dim3(kThreads),
-                            0, s, a);
+    return launch_dependent(norm_grad_kernel<DT, W, G, VEC>, dim3((unsigned)parts),
+                            dim3(W > 8 ? W * 32 : kThreads), 0, s, a);
 }
 
 template <int DT, bool VEC>
@@ -395,16 +418,19 @@ cudaError_t grad_pick(const NormGrad &a, int64_t parts, cudaStream_t s)
                                 dim3(kThreads), 0, s, a);
     }
     if (a.dim <= 256) return grad_go<DT, 1, 1, VEC>(a, parts, s);
-    if (a.dim <= 1024) return grad_go<DT, 1, 4, VEC>(a, parts, s);
-    if (a.dim <= 2048) return grad_go<DT, 8, 1, VEC>(a, parts, s);
+    if (a.dim <= 512) return grad_go<DT, 1, 2, VEC>(a, parts, s);
+    if (a.dim <= 768) return grad_go<DT, 1, 3, VEC>(a, parts, s);
+    if (a.dim <= 1024) return grad_go<DT, 2, 2, VEC>(a, parts, s);
+    if (a.dim <= 2048) return grad_go<DT, 4, 2, VEC>(a, parts, s);
     if (a.dim <= 4096) return grad_go<DT, 8, 2, VEC>(a, parts, s);
-    return grad_go<DT, 8, 4, VEC>(a, parts, s);
+    return grad_go<DT, 16, 2, VEC>(a, parts, s);
 }
 
 int64_t norm_parts(int64_t n, int64_t dim)
 {
     if (dim > 8192) return (n + 7) / 8 < kStripParts ? (n + 7) / 8 : kStripParts;
-    const int64_t groups = kWarps / row_warps(dim), blocks = (n + groups - 1) / groups;
+    const int64_t warps = row_warps(dim), groups = warps < kWarps ? kWarps / warps : 1;
+    const int64_t blocks = (n + groups - 1) / groups;
     return blocks < kMostBlocks ? blocks : kMostBlocks;
 }
 

@@ -66,6 +66,14 @@ __device__ __forceinline__ void put(void *p, int64_t stride, int64_t r, int64_t 
     }
 }
 
+// Run w of a matrix whose rows have `runs` runs of 256 columns: its row and first column.
+__device__ __forceinline__ void run_at(int64_t w, int64_t runs, int64_t &r, int64_t &c0)
+{
+    if (w < 0x80000000ll && runs < 0x80000000ll) r = (uint32_t)w / (uint32_t)runs;
+    else r = w / runs;
+    c0 = (w - r * runs) * 256;
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

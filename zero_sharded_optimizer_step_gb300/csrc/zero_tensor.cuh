@@ -116,6 +116,14 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank)
     return p;
 }
 
+__device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(addr, rank))
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float4 load_peer4(uint32_t addr, uint32_t rank)
 {
     float4 v;
