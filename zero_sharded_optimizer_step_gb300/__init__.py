@@ -29,7 +29,7 @@ def __getattr__(name):
         from . import optim
         return getattr(optim, name)
     if name in ("embed", "embed_grad", "dropout", "Mx4Matrix", "mx4_quantize", "mx4_matmul",
-                "Mx4Linear"):
+                "Mx4Linear", "Packed8", "pack8", "rms_norm", "matmul", "linear", "gated"):
         from . import layers
         return getattr(layers, name)
     raise AttributeError(name)

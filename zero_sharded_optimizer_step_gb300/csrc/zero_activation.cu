@@ -267,24 +267,25 @@ unpack8_kernel(const __grid_constant__ pack8::View q, int64_t n, int64_t cols, i
 
 // ----------------------------------------------------------------- column sums
 
-// A block takes 32 columns, its warps every eighth of the partial rows, in order.
+// A block takes 32 columns, its warps (up to 32) every so many of the partial rows,
+// in order.
 template <int DT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(1024)
 column_sums_kernel(const float *parts, int64_t n_parts, int64_t cols, void *out, int accumulate)
 {
-    __shared__ float joined[kWarps][32];
+    __shared__ float joined[32][32];
     pdl_wait();
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (c < cols) {
         constexpr int U = 8;
-        for (int64_t p = warp; p < n_parts; p += U * kWarps) {
+        for (int64_t p = warp; p < n_parts; p += U * warps) {
             float f[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                f[u] = p + u * kWarps < n_parts ? parts[(p + u * kWarps) * cols + c] : 0.0f;
+                f[u] = p + u * warps < n_parts ? parts[(p + u * warps) * cols + c] : 0.0f;
 #pragma unroll
             for (int u = 0; u < U; ++u) v = __fadd_rn(v, f[u]);
         }
@@ -292,8 +293,7 @@ column_sums_kernel(const float *parts, int64_t n_parts, int64_t cols, void *out,
     joined[warp][lane] = v;
     __syncthreads();
     if (warp || c >= cols) return;
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) v = __fadd_rn(v, joined[i][lane]);
+    for (int i = 1; i < warps; ++i) v = __fadd_rn(v, joined[i][lane]);
     if (accumulate) v = __fadd_rn(elems::load1<DT>(out, c), v);
     elems::store1<DT>(out, c, v);
 }
@@ -318,10 +318,11 @@ unsigned run_blocks(int32_t dt, int64_t n, int64_t runs)
 cudaError_t launch_column_sums(int32_t dt, const float *parts, int64_t n_parts, int64_t cols,
                                void *out, bool accumulate, cudaStream_t s)
 {
+    const int64_t eights = (n_parts + 7) / 8, warps = eights < 4 ? 4 : eights < 32 ? eights : 32;
     return by_type(dt, [&](auto t) {
         return launch_dependent(column_sums_kernel<decltype(t)::value>,
-                                dim3((unsigned)((cols + 31) / 32)), dim3(kThreads), 0, s, parts,
-                                n_parts, cols, out, accumulate ? 1 : 0);
+                                dim3((unsigned)((cols + 31) / 32)), dim3((unsigned)warps * 32), 0,
+                                s, parts, n_parts, cols, out, accumulate ? 1 : 0);
     });
 }
 

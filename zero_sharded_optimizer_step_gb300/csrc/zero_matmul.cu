@@ -354,44 +354,41 @@ __device__ __forceinline__ void finish_rows(const ProductArgs &a, bool vec, floa
     __syncwarp();
 }
 
-// ------------------------------------------------------- one to four rows
+// ------------------------------------------------------------------- one row
 //
 // The weights' bytes are all there is: a warp reads four rows of B (of both, in a
-// gated block) in the memory's own order, 512 bytes of each at a time, multiplies in fp32 and
-// adds up over its lanes.  A block makes 32 columns of the result; KS warps share a
-// row's length where the blocks are few.  No copy engine and no tensor memory to set
-// up, and rows need no boundary.
-template <int DT, int ODT, bool GATED, int M, int KS, bool VEC>
+// gated block) in the memory's own order, 512 bytes of each at a time, multiplies in
+// fp32 and adds up over its lanes.  A block makes 32 columns of the result; KS warps
+// share a row's length where the blocks are few.  No copy engine and no tensor
+// memory to set up, and rows need no boundary.
+//
+// Measured, the weights not in L2: 2 x 11008 x 4096 29.6 us (6.1 TB/s; asking
+// for twice as much at a time 36.5), through the tensor cores 33; 6400 x 1600 KS = 2 6.3,
+// KS = 1 7.4, tensor cores 7.5; 4096 x 11008 KS = 4 16.1, KS = 2 19.6, tensor cores 18.2.
+// (With four rows of A this way took 2 x 11008 x 4096 46 us, for the arithmetic.)
+template <int DT, int ODT, bool GATED, int KS, bool VEC>
 __global__ void __launch_bounds__(256 * KS)
 matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ rows::In x,
               const __grid_constant__ rows::In w, const __grid_constant__ rows::In w2)
 {
-    constexpr int R = 4, kWeights = GATED ? 2 : 1;
-    __shared__ float part[kWeights][KS][M][32];
+    constexpr int kWeights = GATED ? 2 : 1, R = 4;
+    __shared__ float part[kWeights][KS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp / 8;
     const int64_t j0 = (int64_t)blockIdx.x * 32, first = j0 + (warp % 8) * R;
     pdl_wait();
     pdl_launch_dependents();
-    float acc[kWeights][R][M];
-#pragma unroll
-    for (int g = 0; g < kWeights; ++g)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int t = 0; t < M; ++t) acc[g][r][t] = 0.0f;
-#pragma unroll 2
+    float acc[kWeights][R] = {};
+#pragma unroll 1
     for (int64_t c0 = share * 256; c0 < a.k; c0 += KS * 256) {
-        rows::Eight<DT, VEC> we[kWeights][R], xe[M];
+        rows::Eight<DT, VEC> we[kWeights][R], xe;
 #pragma unroll
         for (int g = 0; g < kWeights; ++g)
 #pragma unroll
             for (int r = 0; r < R; ++r)      // (the last row again past the end: not written)
                 we[g][r].ask(g ? w2 : w, first + r < a.n ? first + r : a.n - 1, c0, a.k);
-#pragma unroll
-        for (int t = 0; t < M; ++t) xe[t].ask(x, t < a.m ? t : 0, c0, a.k);
-        float xv[M][8];
-#pragma unroll
-        for (int t = 0; t < M; ++t) xe[t].take(xv[t]);
+        xe.ask(x, 0, c0, a.k);
+        float xv[8];
+        xe.take(xv);
 #pragma unroll
         for (int g = 0; g < kWeights; ++g)
 #pragma unroll
@@ -399,63 +396,62 @@ matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ row
                 float f[8];
                 we[g][r].take(f);
 #pragma unroll
-                for (int t = 0; t < M; ++t)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        acc[g][r][t] = __fmaf_rn(f[e], xv[t][e], acc[g][r][t]);
+                for (int e = 0; e < 8; ++e) acc[g][r] = __fmaf_rn(f[e], xv[e], acc[g][r]);
             }
     }
 #pragma unroll
     for (int g = 0; g < kWeights; ++g)
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int t = 0; t < M; ++t) {
-                const float v = rows::warp_sum(acc[g][r][t]);
-                if (lane == 0) part[g][share][t][(warp % 8) * R + r] = v;
-            }
+        for (int r = 0; r < R; ++r) {
+            const float v = rows::warp_sum(acc[g][r]);
+            if (lane == 0) part[g][share][(warp % 8) * R + r] = v;
+        }
     __syncthreads();
-    if (warp >= M || warp >= a.m) return;
+    if (warp) return;
     float z[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int g = 0; g < kWeights; ++g) {
-        z[g] = part[g][0][warp][lane];
+        z[g] = part[g][0][lane];
 #pragma unroll
-        for (int s = 1; s < KS; ++s) z[g] = __fadd_rn(z[g], part[g][s][warp][lane]);
+        for (int s = 1; s < KS; ++s) z[g] = __fadd_rn(z[g], part[g][s][lane]);
     }
     const int64_t j = j0 + lane;
     const float bias = a.bias && j < a.n ? elems::load1<DT>(a.bias, j) : 0.0f;
-    finish_lane<DT, ODT, GATED>(a, warp, j, j < a.n, z[0], z[1], bias);
+    finish_lane<DT, ODT, GATED>(a, 0, j, j < a.n, z[0], z[1], bias);
 }
 
 // ------------------------------------------------- few rows, or few tiles
 //
 // The accumulator's 128 lanes are 128 rows of B (128 consecutive columns of
-// the result, so that a warp's stores are contiguous), its columns NT rows of
+// the result, so that a warp's stores are contiguous), its columns up to 128 rows of
 // A: with few tokens the tile is as narrow as they are, and the product reads
 // the weights once.  A gated block has two accumulators, of the same lanes,
 // side by side.  One warp issues the copies, one the products, four write.
 // With fewer tiles than SMs the columns c are split over a cluster of up to 8
 // blocks, whose partial sums join through distributed shared memory in the blocks'
 // order.
-template <int NT, bool GATED> struct Tile {
+template <bool GATED> struct Tile {
     static constexpr int kWeights = GATED ? 2 : 1;
-    static constexpr int kStage = kWeights * kHalf + NT * kLine;
-    static constexpr int kCols = kWeights * NT;
-    static constexpr int kTmem = kCols <= 32 ? 32 : kCols;
-    static constexpr int kMost = (kSmemBlock - 1024) / kStage;
-    static constexpr int kStages = kMost < 8 ? kMost : 8;
+    static constexpr int kStages = 8;                       // at most
+    static __host__ __device__ constexpr int stage(int nt)
+    {
+        return kWeights * kHalf + nt * kLine;
+    }
+    static __host__ __device__ constexpr int tmem(int nt)
+    {
+        const int c = kWeights * nt;
+        return c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : 256;
+    }
     // A block's share of an SM's shared memory is at least its share of the tensor
     // memory, so that no block waits for tensor memory that another one
     // holds: two that wait for their cluster peers so would wait forever.
-    static constexpr int smem(int stages, int span)
+    static int smem(int stages, int nt, int span)
     {
         const int part = kWeights * span * 128 * 4;         // the sums, when they are done
-        const int ring = stages * kStage > part ? stages * kStage : part;
-        const int share = (kSmemSm / (512 / kTmem) + 127) / 128 * 128;
+        const int ring = stages * stage(nt) > part ? stages * stage(nt) : part;
+        const int share = (kSmemSm / (512 / tmem(nt)) + 127) / 128 * 128;
         return ring + 1024 > share ? ring + 1024 : share;
     }
-    static_assert(kStage % 1024 == 0, "stages start on the swizzle's boundary");
 };
 
 constexpr int kOneThreads = 192;
@@ -465,6 +461,7 @@ struct OneArgs {
     CUtensorMap a, b, b2, a2;
     int64_t kt1, kt, tiles_n;            // stages of the first pair of operands, of both
     int32_t splits, stages;
+    int32_t nt;                          // rows of A in a tile, a multiple of 16
     int32_t span;                        // an accumulator's columns in shared memory
     int32_t vec;                         // runs of columns lie on their boundaries
 };
@@ -533,11 +530,13 @@ __device__ __forceinline__ void join(const ProductArgs &a, const float *part, in
     }
 }
 
-template <int DT, int ODT, bool GATED, int NT>
+template <int DT, int ODT, bool GATED>
 __global__ void __launch_bounds__(kOneThreads, kMostBlocks)
 matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ OneArgs g)
 {
-    using Tl = Tile<NT, GATED>;
+    using Tl = Tile<GATED>;
+    const int stage = Tl::stage(g.nt);
+    const uint32_t columns = Tl::tmem(g.nt);
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t bars[2 * Tl::kStages + 1];
     __shared__ uint32_t tmem_base, failed;
@@ -571,7 +570,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
         }
         __syncwarp();
         pdl_wait();
-        const int32_t jx = (int32_t)(tn * 128), ix = (int32_t)(tm * NT);
+        const int32_t jx = (int32_t)(tn * 128), ix = (int32_t)(tm * g.nt);
         auto weights = [&](uint32_t to, const CUtensorMap *map, int32_t c, uint32_t bar) {
             if (a.b_cols) {
                 box_load(to, map, jx, c, bar);
@@ -584,8 +583,8 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
             const int64_t kt = k0 + it;
             const bool second = kt >= g.kt1;
             const int32_t c = (int32_t)((second ? kt - g.kt1 : kt) * kDepth);
-            const uint32_t st = ring + s * Tl::kStage, tok = st + Tl::kWeights * kHalf;
-            bar_expect(full(s), Tl::kStage);
+            const uint32_t st = ring + s * stage, tok = st + Tl::kWeights * kHalf;
+            bar_expect(full(s), (uint32_t)stage);
             weights(st, !GATED && second ? &g.b2 : &g.b, c, full(s));
             if constexpr (GATED) weights(st + kHalf, &g.b2, c, full(s));
             const CUtensorMap *map = second ? &g.a2 : &g.a;
@@ -607,7 +606,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
         }
     } else if (warp == 5) {                                  // the products
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         saddr(&tmem_base)), "r"((uint32_t)Tl::kTmem) : "memory");
+                         saddr(&tmem_base)), "r"(columns) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncthreads();
@@ -615,7 +614,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
         const bool one = elect_one();
         const uint32_t tmem = tmem_base;
         const Layout lb = layout_of(a.b_cols), la = layout_of(0);
-        const uint32_t desc = shape_desc<DT>(a.b_cols, 0) | ((uint32_t)(NT >> 3) << 17) |
+        const uint32_t desc = shape_desc<DT>(a.b_cols, 0) | ((uint32_t)(g.nt >> 3) << 17) |
                               ((128u >> 4) << 24);
         int s = 0;
         uint32_t phase = 0;
@@ -624,7 +623,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if (one) {
-                const uint32_t st = ring + s * Tl::kStage;
+                const uint32_t st = ring + s * stage;
                 const uint64_t db = at(lb, st), da = at(la, st + Tl::kWeights * kHalf);
                 // columns past k are zeros: their products are left out
                 const int64_t kt = k0 + it;
@@ -635,7 +634,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
                     if (q >= steps) break;
                     mma1(tmem, db + q * lb.step, da + q * la.step, desc, it > 0 || q > 0);
                     if constexpr (GATED)
-                        mma1(tmem + NT, db + (kHalf >> 4) + q * lb.step, da + q * la.step, desc,
+                        mma1(tmem + g.nt, db + (kHalf >> 4) + q * lb.step, da + q * la.step, desc,
                              it > 0 || q > 0);
                 }
                 commit(empty(s));
@@ -656,8 +655,8 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
         if (lane == 0) atomicAdd(&g_matmul_timeouts, 1u);
         failed = 1;
     }
-    const int64_t i0 = tm * NT;
-    const int cols = (int)(a.m - i0 < NT ? a.m - i0 : NT);
+    const int64_t i0 = tm * g.nt;
+    const int cols = (int)(a.m - i0 < g.nt ? a.m - i0 : g.nt);
     // The sums go where the stages were, [column][lane]: all copies have landed and
     // all products have read them.  From there all threads write the result,
     // eight consecutive columns of a row each, a split's blocks each a share of the rows.
@@ -669,7 +668,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
 #pragma unroll
             for (int w = 0; w < Tl::kWeights; ++w) {
                 float v[16];
-                load16(lanes + w * NT + c, v);
+                load16(lanes + w * g.nt + c, v);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)                 // (or empty sums)
                     part[(w * g.span + c + e) * 128 + warp * 32 + lane] = g.kt == 0 ? 0.0f : v[e];
@@ -679,7 +678,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
     if (g.splits > 1) cluster_sync();
     else __syncthreads();
     if (!failed)
-        join<DT, ODT, GATED, NT < 64 ? 1 : 2>(a, part, 128, g, rank, i0, tn * 128, cols);
+        join<DT, ODT, GATED, GATED ? 1 : 2>(a, part, 128, g, rank, i0, tn * 128, cols);
     if (g.splits > 1) cluster_sync();       // the peers have read this block's shared memory
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -688,7 +687,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
     __syncthreads();
     if (warp == 5)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
-                     "r"((uint32_t)Tl::kTmem));
+                     "r"(columns));
 }
 
 // ------------------------------------------------------ some rows, few tiles
@@ -875,8 +874,7 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
 // barriers.  Lanes are rows of A, so that a thread holds consecutive columns of a
 // row of the result.  A gated tile has 128 columns of the result: the first block
 // brings the gate's weights, the second the other ones, and the accumulator's
-// columns are 128 sums of either.  The last tile of a row of tiles is
-// as narrow as what is left, in steps of 32 columns.
+// columns are 128 sums of either.
 //
 // The blocks are persistent, with two accumulators of 256 columns (all of the
 // tensor memory): eight warps write one tile's result, in 32 columns at a time,
@@ -894,25 +892,49 @@ struct PairArgs {
     int64_t kt1, kt;                     // stages of the first pair of operands, of both
     int64_t tiles_n, tiles_m;
     int32_t half;                        // rows of B that either block brings, at most 128
+    int32_t cut;                         // parts of a tile from tile `whole` on
+    int64_t whole, steps;                // steps: whole tiles and parts
     int32_t vec;                         // finish_run's boundaries hold
 };
 
-// Tile t of the sweep: bands of 8 tiles of rows of A, so that the blocks at work
-// at one time share both operands in L2.
-__device__ __forceinline__ void pair_tile(const PairArgs &g, int64_t t, int64_t &tn, int64_t &tm)
-{
-    const int64_t band = t / (8 * g.tiles_n), in = t - band * 8 * g.tiles_n;
-    const int64_t wide = g.tiles_m - band * 8 < 8 ? g.tiles_m - band * 8 : 8;
-    tn = in / wide;
-    tm = band * 8 + in - tn * wide;
-}
+// Step t of the sweep: bands of 8 tiles of rows of A (16 of a gated block), so that
+// the blocks at work at one time share both operands in L2 (8192 x 8192 x 8192 at the
+// power limit: bands of 4, 8, 16, 32 660, 648, 663, 698 us; a gated 11008 x 4096 over
+// 8192 rows 909, 881, 863, 939).  The tiles of the last, unfilled turn
+// go in `cut` parts, so that all pairs share them.  Rows from row0 on; `half` rows of
+// B in either block, from row first + rank * half on (a gated block's from first
+// on in both); columns of the result from first on.  The last tile of a row is as
+// narrow as what is left, in steps of 32 columns.
+struct PairTile {
+    int64_t row0, first;
+    int half;                            // 0: nothing left for this part
+};
 
-// Rows of B that either block brings for tile column tn: fewer for the last one.
-template <bool GATED> __device__ __forceinline__ int half_of(const PairArgs &g, int64_t n, int64_t tn)
+template <bool GATED>
+__device__ __forceinline__ PairTile pair_tile(const PairArgs &g, int64_t n, int64_t t)
 {
-    const int64_t left = n - tn * (GATED ? g.half : 2 * g.half);
-    if constexpr (GATED) return left >= g.half ? g.half : (int)((left + 15) / 16 * 16);
-    else return left >= 2 * g.half ? g.half : (int)((left + 31) / 32 * 16);
+    int64_t tile = t;
+    int part = 0, half = g.half;
+    if (t >= g.whole) {
+        tile = g.whole + (t - g.whole) / g.cut;
+        part = (int)((t - g.whole) % g.cut);
+        half /= g.cut;
+    }
+    constexpr int kBand = GATED ? 16 : 8;
+    const int64_t band = tile / (kBand * g.tiles_n), in = tile - band * kBand * g.tiles_n;
+    const int64_t rest = g.tiles_m - band * kBand, wide = rest < kBand ? rest : kBand;
+    const int64_t tn = in / wide, tm = band * kBand + in - tn * wide;
+    const int across = GATED ? 1 : 2;
+    PairTile p;
+    p.row0 = tm * 256;
+    p.first = (tn * g.half + part * half) * across;
+    const int64_t left = n - p.first;
+    if (left < across * half) {
+        if constexpr (GATED) half = left <= 0 ? 0 : (int)((left + 15) / 16 * 16);
+        else half = left <= 0 ? 0 : (int)((left + 31) / 32 * 16);
+    }
+    p.half = half;
+    return p;
 }
 
 template <int DT, int ODT, bool GATED>
@@ -925,7 +947,7 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
     const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int64_t tiles = g.tiles_n * g.tiles_m, step = gridDim.x / 2;
+    const int64_t step = gridDim.x / 2;
     auto full = [&](int s) { return saddr(&bars[s]); };                     // the first block's
     auto empty = [&](int s) { return saddr(&bars[kPairStages + s]); };
     auto done = [&](int b) { return saddr(&bars[2 * kPairStages + b]); };
@@ -959,13 +981,11 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
         const int brought = (a.b_cols ? (g.half + 63) / 64 * 64 : g.half) * kLine;
         int s = 0;
         uint32_t phase = 1;                                  // the stages start empty
-        for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
-            int64_t tn, tm;
-            pair_tile(g, t, tn, tm);
-            const int32_t ix = (int32_t)(tm * 256 + rank * 128);
-            const int32_t jx = GATED ? (int32_t)(tn * g.half)
-                                     : (int32_t)(tn * 2 * g.half +
-                                                 rank * half_of<GATED>(g, a.n, tn));
+        for (int64_t t = blockIdx.x / 2; t < g.steps && ok; t += step) {
+            const PairTile p = pair_tile<GATED>(g, a.n, t);
+            if (p.half == 0) continue;
+            const int32_t ix = (int32_t)(p.row0 + rank * 128);
+            const int32_t jx = (int32_t)(p.first + (GATED ? 0 : rank * p.half));
             for (int64_t kt = 0; kt < g.kt; ++kt) {
                 ok = bar_wait(empty(s), phase);
                 if (!ok) break;
@@ -1002,10 +1022,10 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
             const int last_steps = (int)((a.k - (g.kt1 - 1) * kDepth + 15) / 16);
             int s = 0;
             uint32_t phase = 0, i = 0, drained_phase = 1;    // the accumulators start drained
-            for (int64_t t = blockIdx.x / 2; t < tiles && ok; t += step) {
-                int64_t tn, tm;
-                pair_tile(g, t, tn, tm);
-                const uint32_t desc = shape | ((uint32_t)(2 * half_of<GATED>(g, a.n, tn)) >> 3 << 17);
+            for (int64_t t = blockIdx.x / 2; t < g.steps && ok; t += step) {
+                const PairTile p = pair_tile<GATED>(g, a.n, t);
+                if (p.half == 0) continue;
+                const uint32_t desc = shape | ((uint32_t)(2 * p.half) >> 3 << 17);
                 const uint32_t acc = tmem + i * 256;
                 ok = bar_wait(drained((int)i), drained_phase);
                 if (!ok) break;
@@ -1040,15 +1060,14 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
                                                   kPairStages * kPairStage) +
                         warp * 32 * kStagePad;
         uint32_t b = 0, done_phase = 0;
-        for (int64_t t = blockIdx.x / 2; t < tiles; t += step) {
-            int64_t tn, tm;
-            pair_tile(g, t, tn, tm);
+        for (int64_t t = blockIdx.x / 2; t < g.steps; t += step) {
+            const PairTile p = pair_tile<GATED>(g, a.n, t);
+            if (p.half == 0) continue;
             ok = bar_wait(done((int)b), done_phase);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const int half = half_of<GATED>(g, a.n, tn);
-            const int64_t i0 = tm * 256 + rank * 128 + part * 32;
-            const int64_t j0 = tn * (GATED ? g.half : 2 * g.half);
+            const int half = p.half;
+            const int64_t i0 = p.row0 + rank * 128 + part * 32, j0 = p.first;
             const int wide = GATED ? half : 2 * half;        // columns of the result
 #pragma unroll 1
             for (int c = turn * 32; c < wide; c += 64) {
@@ -1221,8 +1240,15 @@ cudaError_t pair_go(const ProductArgs &a, int sms, cudaStream_t s)
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
     g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
-    const int64_t tiles = g.tiles_n * g.tiles_m;
-    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    // The last turn's tiles, if they leave pairs idle, in halves or quarters (a gated
+    // tile's parts are 32 columns at least, and whole blocks of 32).
+    const int64_t tiles = g.tiles_n * g.tiles_m, left = tiles % (sms / 2);
+    g.cut = 1;
+    for (int cut = 2; cut <= 4; cut *= 2)
+        if (left * cut <= sms / 2 && g.half % (cut * (GATED ? 32 : 16)) == 0) g.cut = cut;
+    g.whole = g.cut > 1 ? tiles - left : tiles;
+    g.steps = g.whole + (tiles - g.whole) * g.cut;
+    const int64_t pairs = g.steps < sms / 2 ? g.steps : sms / 2;
     return launch_dependent(matmul_pair_kernel<DT, ODT, GATED>, dim3((unsigned)(2 * pairs)),
                             dim3(kPairThreads), kSmemBlock, s, a, g);
 }
@@ -1299,29 +1325,34 @@ void choose_split(OneArgs &g, int64_t tiles, int sms, const void *kernel, Room &
     }
 }
 
-template <int DT, int ODT, bool GATED, int NT>
+template <int DT, int ODT, bool GATED>
 cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
-    using Tl = Tile<NT, GATED>;
+    using Tl = Tile<GATED>;
     static std::atomic<uint64_t> done{0};
-    static Room room;
-    const auto kernel = matmul_kernel<DT, ODT, GATED, NT>;
+    static Room room[8];                              // for each width of a tile
+    const auto kernel = matmul_kernel<DT, ODT, GATED>;
     cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSmemBlock, done);
     if (e != cudaSuccess) return e;
     OneArgs g;
-    e = operand_maps(a, g, NT, 128);
+    const int64_t tiles_m = (a.m + 127) / 128;
+    g.nt = (int)((a.m + tiles_m * 16 - 1) / (tiles_m * 16) * 16);
+    g.span = g.nt;
+    e = operand_maps(a, g, g.nt, 128);
     if (e != cudaSuccess) return e;
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
     g.tiles_n = (a.n + 127) / 128;
     g.vec = runs_aligned(a, ODT == F32 ? 16 : 8, ODT == F32 ? 4 : 2);
-    g.span = a.m < NT ? (int)((a.m + 15) / 16 * 16) : NT;
-    const int64_t tiles = g.tiles_n * ((a.m + NT - 1) / NT);
-    choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room, Tl::kStages,
-                 kMostBlocks, [&](int stages) { return Tl::smem(stages, g.span); });
+    const int64_t tiles = g.tiles_n * tiles_m;
+    int most = (kSmemBlock - 1024) / Tl::stage(g.nt);
+    if (most > Tl::kStages) most = Tl::kStages;
+    auto smem = [&](int stages) { return Tl::smem(stages, g.nt, g.span); };
+    choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room[g.nt / 16 - 1], most,
+                 kMostBlocks, smem);
     const int64_t blocks = tiles * g.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    Clusters c(blocks, g.splits, Tl::smem(g.stages, g.span), s);
+    Clusters c(blocks, g.splits, smem(g.stages), s);
     return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
 }
 
@@ -1339,7 +1370,7 @@ template <int DT, int ODT> cudaError_t mid_go(const ProductArgs &a, int sms, cud
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
     g.tiles_n = (a.n + 127) / 128;
     g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
-    g.span = 128;
+    g.nt = g.span = 128;
     const int64_t tiles = g.tiles_n * ((a.m + 127) / 128);
     choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room, kMidStages, 2,
                  mid_smem);
@@ -1349,54 +1380,47 @@ template <int DT, int ODT> cudaError_t mid_go(const ProductArgs &a, int sms, cud
     return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
 }
 
-// Whether the rows of A are so few that matvec_kernel takes the product.
-bool few_rows(const ProductArgs &a)
+// Whether matvec_kernel takes the product.
+bool one_row(const ProductArgs &a)
 {
-    return a.m <= 4 && a.k > 0 && !a.a_cols && !a.b_cols && !a.a2;
+    return a.m == 1 && a.k > 0 && !a.a_cols && !a.b_cols && !a.a2;
 }
 
-template <int DT, int ODT, bool GATED, int M>
+template <int DT, int ODT, bool GATED>
 cudaError_t matvec_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
-    const rows::In x = rows::in(a.a, a.m, a.k, a.a_stride, DT);
+    const rows::In x = rows::in(a.a, 1, a.k, a.a_stride, DT);
     const rows::In w = rows::in(a.b, a.n, a.k, a.b_stride, DT);
     const rows::In w2 = rows::in(a.b2, a.n, a.k, a.b2_stride, DT);
-    const bool vec = rows_aligned(a.a, a.a_stride, DT, a.k) &&
-                     rows_aligned(a.b, a.b_stride, DT, a.k) &&
+    const bool vec = rows_aligned(a.a, 0, DT, a.k) && rows_aligned(a.b, a.b_stride, DT, a.k) &&
                      (!a.b2 || rows_aligned(a.b2, a.b2_stride, DT, a.k));
     const int64_t blocks = (a.n + 31) / 32;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    // 16 warps an SM or more, as long as each has a few strides of its row
-    const int ks = blocks * 8 >= (int64_t)sms * 16 || a.k < 1024 ? 1
-                   : blocks * 16 >= (int64_t)sms * 16 || a.k < 2048 ? 2 : 4;
+    // warps that read 20 rows' strides at once on every SM, as long as a row is long
+    // enough to share
+    const int64_t strides = blocks * 8 * (GATED ? 2 : 1), want = (int64_t)sms * 20;
+    const int ks = strides >= want || a.k <= 512 ? 1 : strides * 2 >= want || a.k <= 1024 ? 2 : 4;
     auto go = [&](auto k, int threads) {
         return launch_dependent(k, dim3((unsigned)blocks), dim3(threads), 0, s, a, x, w, w2);
     };
-    if (!vec) return ks == 1 ? go(matvec_kernel<DT, ODT, GATED, M, 1, false>, 256)
-                             : go(matvec_kernel<DT, ODT, GATED, M, 2, false>, 512);
-    if (ks == 1) return go(matvec_kernel<DT, ODT, GATED, M, 1, true>, 256);
-    if constexpr (M == 1)
-        if (ks == 4) return go(matvec_kernel<DT, ODT, GATED, M, 4, true>, 1024);
-    return go(matvec_kernel<DT, ODT, GATED, M, 2, true>, 512);
+    if (!vec) return ks == 1 ? go(matvec_kernel<DT, ODT, GATED, 1, false>, 256)
+                             : go(matvec_kernel<DT, ODT, GATED, 2, false>, 512);
+    return ks == 1 ? go(matvec_kernel<DT, ODT, GATED, 1, true>, 256)
+           : ks == 2 ? go(matvec_kernel<DT, ODT, GATED, 2, true>, 512)
+                     : go(matvec_kernel<DT, ODT, GATED, 4, true>, 1024);
 }
 
 template <int DT, int ODT, bool GATED>
 cudaError_t pick(const ProductArgs &a, int sms, cudaStream_t s)
 {
-    if (few_rows(a))
-        return a.m == 1 ? matvec_go<DT, ODT, GATED, 1>(a, sms, s)
-                        : matvec_go<DT, ODT, GATED, 4>(a, sms, s);
+    if (one_row(a)) return matvec_go<DT, ODT, GATED>(a, sms, s);
     // Few rows, or no more tiles of 128 by 128 than SMs: the single blocks, whose
     // columns c can be split.  Beyond that the pairs.
     const int64_t tiles = ((a.n + 127) / 128) * ((a.m + 127) / 128);
     if (a.k > 0 && a.m > 64 && tiles > sms) return pair_go<DT, ODT, GATED>(a, sms, s);
-    if constexpr (GATED) {
-        if (a.m > 64) return one_go<DT, ODT, GATED, 128>(a, sms, s);
-    } else {
+    if constexpr (!GATED)
         if (a.k > 0 && (a.m > 64 || a.a_cols)) return mid_go<DT, ODT>(a, sms, s);
-    }
-    return a.m <= 16 ? one_go<DT, ODT, GATED, 16>(a, sms, s)
-                     : one_go<DT, ODT, GATED, 64>(a, sms, s);
+    return one_go<DT, ODT, GATED>(a, sms, s);
 }
 
 // An operand's place in the workspace, if it needs one: bytes.
@@ -1417,7 +1441,7 @@ bool on_boundaries(const void *p, int64_t rows, int64_t stride)
 
 int64_t product_workspace(const ProductArgs &a)
 {
-    if (few_rows(a)) return 0;
+    if (one_row(a)) return 0;
     int64_t need = 0;
     auto add = [&](const void *p, int64_t rows, int32_t cols, int64_t stride) {
         const Place at = cols ? Place{a.k, rows, stride} : Place{rows, a.k, stride};
@@ -1434,7 +1458,7 @@ cudaError_t launch_product(int32_t dt, int32_t odt, ProductArgs a, void *workspa
                            cudaStream_t s)
 {
     if (a.m <= 0 || a.n <= 0) return cudaSuccess;
-    if (a.k > 0 && !few_rows(a)) {
+    if (a.k > 0 && !one_row(a)) {
         char *room = static_cast<char *>(workspace);
         cudaError_t e = cudaSuccess;
         auto settle = [&](const void *&p, int64_t rows, int32_t cols, int64_t &stride) {

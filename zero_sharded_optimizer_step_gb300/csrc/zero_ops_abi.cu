@@ -413,9 +413,9 @@ int zero_matmul(const void *a, int32_t a_cols, int64_t a_stride, const void *b, 
     };
     ZERO_TRY(operand("a", a, m, a_cols, a_stride));
     ZERO_TRY(operand("b", b, n, b_cols, b_stride));
-    if ((a2 != nullptr) != (b2 != nullptr))
+    if (m > 0 && n > 0 && k > 0 && (a2 != nullptr) != (b2 != nullptr))   // empty ones have no place
         return report(ZERO_EINVAL, "a2 and b2 are given together");
-    if (a2) {
+    if (a2 && b2) {
         ZERO_TRY(operand("a2", a2, m, a_cols, a2_stride));
         ZERO_TRY(operand("b2", b2, n, b_cols, b2_stride));
     }
