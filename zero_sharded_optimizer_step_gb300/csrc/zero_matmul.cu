@@ -125,47 +125,6 @@ __device__ __forceinline__ void finish_lane(const ProductArgs &a, int64_t i, int
     }
 }
 
-// Elements e < valid of the four from element `at` on; `vec`: they lie on a
-// boundary of four.
-template <int DT>
-__device__ __forceinline__ void load_four(const void *p, int64_t at, bool vec, int valid,
-                                          float (&f)[4])
-{
-    using T = typename elems::El<DT>::T;
-    if (vec && valid == 4) {
-        if constexpr (DT == F32) {
-            const float4 v = *reinterpret_cast<const float4 *>(static_cast<const T *>(p) + at);
-            f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const T *>(p) + at);
-            elems::widen2<DT>(v.x, f[0], f[1]);
-            elems::widen2<DT>(v.y, f[2], f[3]);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = e < valid ? elems::load1<DT>(p, at + e) : 0.0f;
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ void store_four(void *p, int64_t at, bool vec, int valid,
-                                           const float (&f)[4])
-{
-    using T = typename elems::El<DT>::T;
-    if (vec && valid == 4) {
-        if constexpr (DT == F32)
-            *reinterpret_cast<float4 *>(static_cast<T *>(p) + at) =
-                make_float4(f[0], f[1], f[2], f[3]);
-        else
-            *reinterpret_cast<uint2 *>(static_cast<T *>(p) + at) =
-                make_uint2(elems::narrow2<DT>(f[0], f[1]), elems::narrow2<DT>(f[2], f[3]));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < valid) elems::store1<DT>(p, at + e, f[e]);
-    }
-}
-
 // The activation of an array.
 template <int U, int N> __device__ __forceinline__ void activate(float (&z)[U][N], int32_t kind)
 {
@@ -178,81 +137,40 @@ template <int U, int N> __device__ __forceinline__ void activate(float (&z)[U][N
     });
 }
 
-// Four columns from j on of the U rows i[u], `valid` of them the result's, by a
-// thread whose seven neighbours hold the rest of 32 from a multiple of 32 on.  The
-// whole warp comes here together; a row that is not `there` is left out.  Step by
-// step for all rows, so that their latencies overlap.
-template <int DT, int ODT, bool GATED, int U>
-__device__ __forceinline__ void finish_fours(const ProductArgs &a, const int64_t (&i)[U],
-                                             const bool (&there)[U], int64_t j, bool vec,
-                                             int valid, float (&z)[U][4], float (&z2)[U][4],
-                                             const float (&bias)[4])
+// What is added to 32 columns of a row, on 32-byte boundaries: asked for before the sums
+// are there.  (The residual may be the result's own place: a thread's elements are its own.)
+template <int DT, int ODT, bool GATED> struct Beside {
+    elems::Raw<DT> bias[4];
+    elems::Raw<ODT> residual[4];
+
+    __device__ __forceinline__ void ask(const ProductArgs &a, int64_t i, int64_t j)
+    {
+        if constexpr (!GATED) {
+            if (a.bias) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) bias[u].load(a.bias, j + 8 * u);
+            }
+            if (a.residual) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    residual[u].load(a.residual, i * a.residual_stride + j + 8 * u);
+            }
+        }
+    }
+};
+
+template <class R> __device__ __forceinline__ void add_run(const R (&r)[4], float (&z)[32])
 {
-    float r[U][4];
-    if (a.residual) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            load_four<ODT>(a.residual, i[u] * a.residual_stride + j, vec, there[u] ? valid : 0,
-                           r[u]);
+    for (int u = 0; u < 4; ++u) {
+        float f[8];
+        r[u].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[8 * u + e] = __fadd_rn(z[8 * u + e], f[e]);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[u][e] = __fadd_rn(z[u][e], bias[e]);
-    if (a.kept) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            store_four<DT>(a.kept, i[u] * a.kept_stride + j, vec, there[u] ? valid : 0, z[u]);
-            if constexpr (GATED)
-                store_four<DT>(a.kept2, i[u] * a.kept_stride + j, vec, there[u] ? valid : 0,
-                               z2[u]);
-        }
-    }
-    if (a.kept_q) {
-        const pack8::View q = pack8::view(a.kept_q, a.m, a.n);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e >= valid) z[u][e] = z2[u][e] = 0.0f;
-            pack8::put_four(q, i[u], j, there[u] && j < q.wide, z[u]);
-            if constexpr (GATED)
-                pack8::put_four(pack8::view(a.kept2_q, a.m, a.n), i[u], j,
-                                there[u] && j < q.wide, z2[u]);
-        }
-    }
-    activate(z, a.act);
-    if constexpr (GATED) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[u][e] = __fmul_rn(z[u][e], z2[u][e]);
-    }
-    if (a.residual) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[u][e] = __fadd_rn(z[u][e], r[u][e]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        store_four<ODT>(a.out, i[u] * a.stride + j, vec, there[u] ? valid : 0, z[u]);
 }
 
 // 16 columns of a row on 32-byte boundaries.
-template <int DT> __device__ __forceinline__ void load_run(const void *p, int64_t at, float *f)
-{
-    elems::Raw<DT> r;
-    float h[8];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        r.load(p, at + 8 * u);
-        r.get(h);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[8 * u + e] = h[e];
-    }
-}
-
 template <int DT> __device__ __forceinline__ void store_run(void *p, int64_t at, const float *f)
 {
     using T = typename elems::El<DT>::T;
@@ -275,16 +193,11 @@ template <int DT> __device__ __forceinline__ void store_run(void *p, int64_t at,
 // sums, z2 the second ones of a gated block.
 template <int DT, int ODT, bool GATED>
 __device__ __forceinline__ void finish_run(const ProductArgs &a, int64_t i, int64_t j,
-                                           float (&z)[32], float (&z2)[32])
+                                           const Beside<DT, ODT, GATED> &beside, float (&z)[32],
+                                           float (&z2)[32])
 {
-    if (a.bias) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float b[16];
-            load_run<DT>(a.bias, j + 16 * h, b);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) z[16 * h + e] = __fadd_rn(z[16 * h + e], b[e]);
-        }
+    if constexpr (!GATED) {
+        if (a.bias) add_run(beside.bias, z);
     }
     if (a.kept) {
         store_run<DT>(a.kept, i * a.kept_stride + j, z);
@@ -302,55 +215,64 @@ __device__ __forceinline__ void finish_run(const ProductArgs &a, int64_t i, int6
     if constexpr (GATED) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) z[e] = __fmul_rn(z[e], z2[e]);
+    } else {
+        if (a.residual) add_run(beside.residual, z);
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (a.residual) {
-            float r[16];
-            load_run<ODT>(a.residual, i * a.residual_stride + j + 16 * h, r);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) z[16 * h + e] = __fadd_rn(z[16 * h + e], r[e]);
-        }
-        store_run<ODT>(a.out, i * a.stride + j + 16 * h, z + 16 * h);
-    }
+    store_run<ODT>(a.out, i * a.stride + j, z);
+    store_run<ODT>(a.out, i * a.stride + j + 16, z + 16);
 }
 
-// 32 columns from j on of 32 rows from i0 on, a row a lane.  Rows off the
-// boundaries and ragged ends go through the warp's shared memory (`staged`, 32 by
-// kStagePad floats), so that its accesses are consecutive.
+// 32 columns from j on of 32 rows from i0 on (those below `end`), a row a lane.  Rows off
+// the boundaries and ragged ends go through the warp's shared memory (`staged`, 32 by
+// kStagePad floats, ONCE: twice that for a gated block), so that its accesses are
+// consecutive.  ONCE: for kernels whose blocks come here a few times only, where
+// fetching code costs more than running it: that way is a loop.
 constexpr int kStagePad = 33;
 
-template <int DT, int ODT, bool GATED>
+template <int DT, int ODT, bool GATED, bool ONCE>
 __device__ __forceinline__ void finish_rows(const ProductArgs &a, bool vec, float *staged,
-                                            int64_t i0, int64_t j, float (&z)[32],
+                                            int64_t i0, int64_t end, int64_t j,
+                                            const Beside<DT, ODT, GATED> &beside, float (&z)[32],
                                             float (&z2)[32])
 {
     const int lane = threadIdx.x & 31;
-    if (j >= a.n || i0 >= a.m) return;
+    if (j >= a.n || i0 >= end) return;
     if (vec && j + 32 <= a.n) {
-        if (i0 + lane < a.m) finish_run<DT, ODT, GATED>(a, i0 + lane, j, z, z2);
+        if (i0 + lane < end) finish_run<DT, ODT, GATED>(a, i0 + lane, j, beside, z, z2);
         return;
     }
-    const float bias = a.bias && j + lane < a.n ? elems::load1<DT>(a.bias, j + lane) : 0.0f;
-    const int64_t rows = a.m - i0 < 32 ? a.m - i0 : 32;
+    const bool in = j + lane < a.n;
+    const float bias = a.bias && in ? elems::load1<DT>(a.bias, j + lane) : 0.0f;
+    const int rows = end - i0 < 32 ? (int)(end - i0) : 32;
     float w2[32];
     __syncwarp();
     if constexpr (GATED) {
+        float *second = ONCE ? staged + 32 * kStagePad : staged;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) staged[lane * kStagePad + e] = z2[e];
-        __syncwarp();
+        for (int e = 0; e < 32; ++e) second[lane * kStagePad + e] = z2[e];
+        if constexpr (!ONCE) {
+            __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w2[e] = staged[e * kStagePad + lane];
-        __syncwarp();
+            for (int e = 0; e < 32; ++e) w2[e] = staged[e * kStagePad + lane];
+            __syncwarp();
+        }
     }
 #pragma unroll
     for (int e = 0; e < 32; ++e) staged[lane * kStagePad + e] = z[e];
     __syncwarp();
+    if constexpr (ONCE) {
+#pragma unroll 1
+        for (int e = 0; e < rows; ++e)
+            finish_lane<DT, ODT, GATED>(a, i0 + e, j + lane, in, staged[e * kStagePad + lane],
+                                        GATED ? staged[(32 + e) * kStagePad + lane] : 0.0f, bias);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-        if (e < rows)
-            finish_lane<DT, ODT, GATED>(a, i0 + e, j + lane, j + lane < a.n,
-                                        staged[e * kStagePad + lane], GATED ? w2[e] : 0.0f, bias);
+        for (int e = 0; e < 32; ++e)
+            if (e < rows)
+                finish_lane<DT, ODT, GATED>(a, i0 + e, j + lane, in,
+                                            staged[e * kStagePad + lane], GATED ? w2[e] : 0.0f,
+                                            bias);
+    }
     __syncwarp();
 }
 
@@ -426,10 +348,13 @@ matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ row
 // the result, so that a warp's stores are contiguous), its columns up to 128 rows of
 // A: with few tokens the tile is as narrow as they are, and the product reads
 // the weights once.  A gated block has two accumulators, of the same lanes,
-// side by side.  One warp issues the copies, one the products, four write.
+// side by side.  One warp issues the copies, one the products, eight write.
 // With fewer tiles than SMs the columns c are split over a cluster of up to 8
 // blocks, whose partial sums join through distributed shared memory in the blocks'
 // order.
+__host__ __device__ constexpr int split_floats(int weights, int span, int splits);
+constexpr int staged_floats(int weights);
+
 template <bool GATED> struct Tile {
     static constexpr int kWeights = GATED ? 2 : 1;
     static constexpr int kStages = 8;                       // at most
@@ -445,23 +370,26 @@ template <bool GATED> struct Tile {
     // A block's share of an SM's shared memory is at least its share of the tensor
     // memory, so that no block waits for tensor memory that another one
     // holds: two that wait for their cluster peers so would wait forever.
-    static int smem(int stages, int nt, int span)
+    static int smem(int stages, int nt, int splits, bool staged)
     {
-        const int part = kWeights * span * 128 * 4;         // the sums, when they are done
+        // the sums, when they are done, a split's shares of them, and room to reorder
+        const int part =
+            (split_floats(kWeights, nt, splits) + (staged ? staged_floats(kWeights) : 0)) * 4;
         const int ring = stages * stage(nt) > part ? stages * stage(nt) : part;
         const int share = (kSmemSm / (512 / tmem(nt)) + 127) / 128 * 128;
         return ring + 1024 > share ? ring + 1024 : share;
     }
 };
 
-constexpr int kOneThreads = 192;
-constexpr int kMostBlocks = 3;                         // of an SM
+constexpr int kOneWarps = 8;                           // of results, before copies and products
+constexpr int kOneThreads = (kOneWarps + 2) * 32;
+constexpr int kMostBlocks = 2;                         // of an SM
 
 struct OneArgs {
     CUtensorMap a, b, b2, a2;
     int64_t kt1, kt, tiles_n;            // stages of the first pair of operands, of both
     int32_t splits, stages;
-    int32_t nt;                          // rows of A in a tile, a multiple of 16
+    int32_t nt, wide;                    // rows of A in a tile, a multiple of 16; of B
     int32_t span;                        // an accumulator's columns in shared memory
     int32_t vec;                         // runs of columns lie on their boundaries
 };
@@ -471,63 +399,145 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// Four consecutive partial sums, of this block or added up over a split's blocks
-// in their order; all of a split's are asked for before the first is used.
-__device__ __forceinline__ float4 sum4(const float *at, int splits)
+// ---- joining a split
+//
+// Every block of a split has partial sums of the whole tile, rows of 128 columns of the
+// result (kPitch floats apart, a gated block's second ones `span` rows
+// later) in its shared memory.  The rows are shared out; each block sends every other
+// one's share there by one bulk copy and adds up what it receives in the blocks' order.
+constexpr int kPitch = 132;                  // a lane a row: no two of eight on one bank
+
+struct Split {
+    static constexpr int pitch = kPitch;
+    int rows, span, weights, splits;
+    uint32_t rank;
+
+    __device__ __forceinline__ int first(uint32_t q) const { return rows * (int)q / splits; }
+    __device__ __forceinline__ int share() const { return (span + splits - 1) / splits; }
+    // where block q's sums for this block arrive, behind its own
+    __device__ __forceinline__ int slot(uint32_t q, int w) const
+    {
+        return (weights * span + ((int)q * weights + w) * share()) * pitch;
+    }
+    __device__ __forceinline__ uint32_t bytes(uint32_t q) const
+    {
+        return (uint32_t)((first(q + 1) - first(q)) * pitch * 4);
+    }
+    // by one thread, before the first cluster_arrive()
+    __device__ __forceinline__ void expect(uint32_t bar) const
+    {
+        bar_init(bar, 1);
+        bar_expect(bar, (uint32_t)((splits - 1) * weights) * bytes(rank));
+    }
+};
+
+// Floats of shared memory that a split's block needs.
+__host__ __device__ constexpr int split_floats(int weights, int span, int splits)
 {
-    if (splits == 1) return *reinterpret_cast<const float4 *>(at);
-    float4 v[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        if (q < splits) v[q] = load_peer4(saddr(at), q);
-    float4 sum = v[0];
-#pragma unroll
-    for (int q = 1; q < 8; ++q)
-        if (q < splits) {
-            sum.x = __fadd_rn(sum.x, v[q].x);
-            sum.y = __fadd_rn(sum.y, v[q].y);
-            sum.z = __fadd_rn(sum.z, v[q].z);
-            sum.w = __fadd_rn(sum.w, v[q].w);
-        }
-    return sum;
+    return (weights * span + (splits > 1 ? splits * weights * ((span + splits - 1) / splits) : 0)) *
+           kPitch;
 }
 
-// Adds up the splits' partial sums, rows of 128 columns of the result (`pitch`
-// floats apart) in every block's shared memory, and writes the result.  A warp
-// takes whole rows, four columns a lane, so that what it reads from a peer is consecutive: U of the rows
-// that fall to its block at a time.
-template <int DT, int ODT, bool GATED, int U>
-__device__ __forceinline__ void join(const ProductArgs &a, const float *part, int pitch,
-                                     const OneArgs &g, uint32_t rank, int64_t i0, int64_t j0,
-                                     int rows)
+// By one thread, once every block's sums and barrier are there.
+__device__ __forceinline__ void send_shares(const Split &t, const float *part, uint32_t bar)
 {
-    constexpr int kWarps = kOneThreads / 32;
-    const int splits = g.splits, warp = threadIdx.x >> 5, lane4 = (threadIdx.x & 31) * 4;
-    const int64_t j = j0 + lane4, left = a.n - j;
-    const int valid = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-    float bias[4] = {0, 0, 0, 0};
-    if (a.bias) load_four<DT>(a.bias, j, g.vec != 0, valid, bias);
-#pragma unroll 1
-    for (int r0 = (int)rank + warp * splits; r0 < rows; r0 += U * kWarps * splits) {
-        int64_t i[U];
-        bool there[U];
-        float z[U][4], z2[U][4];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * kWarps * splits;
-            there[u] = r < rows;
-            i[u] = i0 + r;
-            float4 s = make_float4(0, 0, 0, 0), s2 = s;
-            const float *at = part + r * pitch + lane4;
-            if (there[u]) {
-                s = sum4(at, splits);
-                if constexpr (GATED) s2 = sum4(at + g.span * pitch, splits);
-            }
-            z[u][0] = s.x, z[u][1] = s.y, z[u][2] = s.z, z[u][3] = s.w;
-            z2[u][0] = s2.x, z2[u][1] = s2.y, z2[u][2] = s2.z, z2[u][3] = s2.w;
-        }
-        finish_fours<DT, ODT, GATED, U>(a, i, there, j, g.vec != 0, valid, z, z2, bias);
+    for (int d = 1; d < t.splits; ++d) {
+        const uint32_t q = (t.rank + d) % t.splits, bytes = t.bytes(q);
+        if (!bytes) continue;
+        for (int w = 0; w < t.weights; ++w)
+            asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes"
+                         " [%0], [%1], %2, [%3];" ::"r"(
+                             peer_addr(saddr(part + t.slot(t.rank, w)), q)),
+                         "r"(saddr(part + (w * t.span + t.first(q)) * t.pitch)), "r"(bytes),
+                         "r"(peer_addr(bar, q)) : "memory");
     }
+}
+
+// 32 columns from c on of row r, which is in this block's share, added up.
+__device__ __forceinline__ void sum32(const Split &t, const float *part, int r, int w, int c,
+                                      float (&z)[32])
+{
+    const float *own = part + (w * t.span + r) * kPitch + c;
+    const float *in = part + t.slot(0, w) + (r - t.first(t.rank)) * kPitch + c;
+    const int step = t.slot(1, w) - t.slot(0, w);
+    const float4 *first = reinterpret_cast<const float4 *>(t.rank == 0 ? own : in);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float4 f = first[e];
+        z[4 * e] = f.x, z[4 * e + 1] = f.y, z[4 * e + 2] = f.z, z[4 * e + 3] = f.w;
+    }
+    in += step;
+#pragma unroll 1
+    for (int q = 1; q < t.splits; ++q, in += step) {
+        const float4 *v = reinterpret_cast<const float4 *>((uint32_t)q == t.rank ? own : in);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float4 f = v[e];
+            z[4 * e] = __fadd_rn(z[4 * e], f.x);
+            z[4 * e + 1] = __fadd_rn(z[4 * e + 1], f.y);
+            z[4 * e + 2] = __fadd_rn(z[4 * e + 2], f.z);
+            z[4 * e + 3] = __fadd_rn(z[4 * e + 3], f.w);
+        }
+    }
+}
+
+constexpr int staged_floats(int weights)
+{
+    return kOneThreads / 32 * weights * 32 * kStagePad;
+}
+
+// Writes the result of this block's share of the rows: the warps take 32 rows by 32
+// columns in turn, a row a lane.  (Four columns of a row a lane, a row a warp,
+// took 550 clocks a row: it is the instructions that count here.)
+template <int DT, int ODT, bool GATED>
+__device__ __forceinline__ bool join(const ProductArgs &a, const Split &t, float *part,
+                                     uint32_t bar, bool vec, int64_t i0, int64_t j0)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int from = t.first(t.rank), end = t.first(t.rank + 1);
+    float *staged = part + split_floats(t.weights, t.span, t.splits) +
+                    warp * (GATED ? 2 : 1) * 32 * kStagePad;
+#pragma unroll 1
+    for (int item = warp; item < (end - from + 31) / 32 * 4; item += kOneThreads / 32) {
+        const int r0 = from + (item >> 2) * 32, c = (item & 3) * 32;
+        const int r = r0 + lane < end ? r0 + lane : end - 1;
+        Beside<DT, ODT, GATED> beside;
+        if (vec && j0 + c + 32 <= a.n) beside.ask(a, i0 + r, j0 + c);
+        if (t.splits > 1 && !bar_wait(bar, 0)) return false;
+        float z[32], z2[32];
+        sum32(t, part, r, 0, c, z);
+        if constexpr (GATED) sum32(t, part, r, 1, c, z2);
+        finish_rows<DT, ODT, GATED, true>(a, vec, staged, i0 + r0, i0 + end, j0 + c, beside, z,
+                                          z2);
+    }
+    return true;
+}
+
+// The end of a tile whose sums lie in shared memory: sends and receives the shares
+// and writes the result.  The whole block comes here, after cluster_arrive() where its
+// ring was free for what the others send; `failed` blocks take part in the barriers
+// alone.
+template <int DT, int ODT, bool GATED>
+__device__ __forceinline__ void settle(const ProductArgs &a, const Split &t, float *part,
+                                       uint32_t bar, const uint32_t &failed, bool vec, int64_t i0,
+                                       int64_t j0)
+{
+    if (t.splits > 1) {
+        // what the copies read was written by this block's threads
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        cluster_wait();
+        if (threadIdx.x == 0 && !failed) send_shares(t, part, bar);
+        __syncwarp();
+    } else {
+        __syncthreads();
+    }
+    if (failed) {
+        if (t.splits > 1) bar_wait(bar, 0);      // what is on its way lands before the block ends
+    } else if (!join<DT, ODT, GATED>(a, t, part, bar, vec, i0, j0) && (threadIdx.x & 31) == 0) {
+        atomicAdd(&g_matmul_timeouts, 1u);
+    }
+    if (t.splits > 1) cluster_meet();       // the peers have received what this block sent
 }
 
 template <int DT, int ODT, bool GATED>
@@ -538,7 +548,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
     const int stage = Tl::stage(g.nt);
     const uint32_t columns = Tl::tmem(g.nt);
     extern __shared__ unsigned char dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * Tl::kStages + 1];
+    __shared__ __align__(8) uint64_t bars[2 * Tl::kStages + 2];
     __shared__ uint32_t tmem_base, failed;
     const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -547,12 +557,16 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
     const int64_t tn = tile % g.tiles_n, tm = tile / g.tiles_n;
     const int64_t k0 = g.kt * rank / g.splits, k1 = g.kt * (rank + 1) / g.splits;
     const int rounds = (int)(k1 - k0);
-    const uint32_t done_bar = saddr(&bars[2 * Tl::kStages]);
+    const uint32_t done_bar = saddr(&bars[2 * Tl::kStages]), join_bar = done_bar + 8;
     auto full = [&](int s) { return saddr(&bars[s]); };
     auto empty = [&](int s) { return saddr(&bars[Tl::kStages + s]); };
 
+    const int64_t i0 = tm * g.nt;
+    const int cols = (int)(a.m - i0 < g.nt ? a.m - i0 : g.nt);
+    const Split split = {cols, g.span, Tl::kWeights, g.splits, rank};
+
     bool ok = true;
-    if (warp == 4) {                                         // the copies
+    if (warp == kOneWarps) {                                         // the copies
         const bool one = elect_one();
         if (one) {
             for (int s = 0; s < Tl::kStages; ++s) {
@@ -560,6 +574,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
                 bar_init(empty(s), 1);
             }
             bar_init(done_bar, 1);
+            split.expect(join_bar);
             failed = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -604,7 +619,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
             __syncwarp();
             if (++s == g.stages) s = 0, phase ^= 1;
         }
-    } else if (warp == 5) {                                  // the products
+    } else if (warp == kOneWarps + 1) {                                  // the products
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          saddr(&tmem_base)), "r"(columns) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -655,37 +670,29 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
         if (lane == 0) atomicAdd(&g_matmul_timeouts, 1u);
         failed = 1;
     }
-    const int64_t i0 = tm * g.nt;
-    const int cols = (int)(a.m - i0 < g.nt ? a.m - i0 : g.nt);
+    if (g.splits > 1) cluster_arrive();                      // the ring is free
     // The sums go where the stages were, [column][lane]: all copies have landed and
-    // all products have read them.  From there all threads write the result,
-    // eight consecutive columns of a row each, a split's blocks each a share of the rows.
+    // all products have read them.  From there the block writes the result.
     float *part = reinterpret_cast<float *>(dyn + (ring - saddr(dyn)));
-    if (warp < 4 && ok) {
-        const uint32_t lanes = tmem_base + ((uint32_t)(warp * 32) << 16);
+    if (warp < kOneWarps && ok) {
+        const uint32_t lanes = tmem_base + ((uint32_t)(warp % 4 * 32) << 16);
 #pragma unroll 1
-        for (int c = 0; c < g.span; c += 16) {
+        for (int c = warp / 4 * 16; c < Tl::kWeights * g.nt; c += kOneWarps / 4 * 16) {
+            float v[16];                                     // (the second sums follow the first)
+            load16(lanes + c, v);
+            float *to = part + c * kPitch + warp % 4 * 32 + lane;
 #pragma unroll
-            for (int w = 0; w < Tl::kWeights; ++w) {
-                float v[16];
-                load16(lanes + w * g.nt + c, v);
-#pragma unroll
-                for (int e = 0; e < 16; ++e)                 // (or empty sums)
-                    part[(w * g.span + c + e) * 128 + warp * 32 + lane] = g.kt == 0 ? 0.0f : v[e];
-            }
+            for (int e = 0; e < 16; ++e) to[e * kPitch] = g.kt == 0 ? 0.0f : v[e];   // empty sums
         }
     }
-    if (g.splits > 1) cluster_sync();
-    else __syncthreads();
-    if (!failed)
-        join<DT, ODT, GATED, GATED ? 1 : 2>(a, part, 128, g, rank, i0, tn * 128, cols);
-    if (g.splits > 1) cluster_sync();       // the peers have read this block's shared memory
+    settle<DT, ODT, GATED>(a, split, part, join_bar, failed, g.vec != 0, i0,
+                                          tn * 128);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
         for (int s = 0; s < g.stages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
     __syncthreads();
-    if (warp == 5)
+    if (warp == kOneWarps + 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(columns));
 }
@@ -693,28 +700,31 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
 // ------------------------------------------------------ some rows, few tiles
 //
 // Products of more than 64 rows that are too small for the pairs: tiles of 128
-// by 128, a block each or, split along c, a cluster of blocks.  Lanes are rows of A, so
-// that a thread holds 32 consecutive columns of a row of the result at a time.  Both
-// operands in either order.
-constexpr int kMidStage = 2 * kHalf;
+// by 128 (128 by 64 where there is little to do but to begin and to end), a block each
+// or, split along c, a cluster of blocks.  Both operands in either order.  A whole
+// block's warps write the result from the tensor memory, a row a lane.
+//
+// What bounds it: the shared memory, which takes in and gives out 32 KB a stage: 437
+// clocks against the 256 of its products.
 constexpr int kMidStages = 7;
-constexpr int kMidPad = 132;                             // floats of a row of partial sums
-constexpr int kMidPart = 128 * kMidPad * 4;
-constexpr int kMidStaged = (kOneThreads / 32) * 32 * kStagePad * 4;
 
-constexpr int mid_smem(int stages)
+__host__ __device__ constexpr int mid_stage(int wide) { return kHalf + wide * kLine; }
+
+constexpr int mid_smem(int stages, int wide, int splits, bool staged)
 {
-    const int ring = stages * kMidStage;
-    return (ring > kMidPart + kMidStaged ? ring : kMidPart + kMidStaged) + 1024;
+    const int ring = stages * mid_stage(wide);
+    const int part = ((splits > 1 ? split_floats(1, 128, splits) : 0) +
+                      (staged ? staged_floats(1) : 0)) * 4;
+    return (ring > part ? ring : part) + 1024;
 }
-static_assert(mid_smem(kMidStages) <= kSmemBlock, "one block's shared memory");
+static_assert(mid_smem(kMidStages, 128, 8, true) <= kSmemBlock, "one block's shared memory");
 
 template <int DT, int ODT>
 __global__ void __launch_bounds__(kOneThreads, 2)
 matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ OneArgs g)
 {
     extern __shared__ unsigned char dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * kMidStages + 1];
+    __shared__ __align__(8) uint64_t bars[2 * kMidStages + 2];
     __shared__ uint32_t tmem_base, failed;
     const uint32_t ring = saddr(dyn) + ((1024 - (saddr(dyn) & 1023)) & 1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -723,12 +733,17 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     const int64_t tn = tile % g.tiles_n, tm = tile / g.tiles_n;
     const int64_t k0 = g.kt * rank / g.splits, k1 = g.kt * (rank + 1) / g.splits;
     const int rounds = (int)(k1 - k0);
-    const uint32_t done_bar = saddr(&bars[2 * kMidStages]);
+    const uint32_t done_bar = saddr(&bars[2 * kMidStages]), join_bar = done_bar + 8;
     auto full = [&](int s) { return saddr(&bars[s]); };
     auto empty = [&](int s) { return saddr(&bars[kMidStages + s]); };
 
+    const int64_t i0 = tm * 128, j0 = tn * g.wide;
+    const int stage = mid_stage(g.wide);
+    const int rows = (int)(a.m - i0 < 128 ? a.m - i0 : 128);
+    const Split split = {rows, 128, 1, g.splits, rank};
+
     bool ok = true;
-    if (warp == 4) {                                         // the copies
+    if (warp == kOneWarps) {                                         // the copies
         const bool one = elect_one();
         if (one) {
             for (int s = 0; s < kMidStages; ++s) {
@@ -736,6 +751,7 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
                 bar_init(empty(s), 1);
             }
             bar_init(done_bar, 1);
+            split.expect(join_bar);
             failed = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -744,12 +760,12 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
         }
         __syncwarp();
         pdl_wait();
-        const int32_t ix = (int32_t)(tm * 128), jx = (int32_t)(tn * 128);
+        const int32_t ix = (int32_t)i0, jx = (int32_t)j0;
         auto half = [&](uint32_t to, const CUtensorMap *map, int32_t cols, int32_t x, int32_t c,
-                        uint32_t bar) {
+                        int rows, uint32_t bar) {
             if (cols) {
                 box_load(to, map, x, c, bar);
-                box_load(to + kHalf / 2, map, x + 64, c, bar);
+                if (rows > 64) box_load(to + kHalf / 2, map, x + 64, c, bar);
             } else {
                 box_load(to, map, c, x, bar);
             }
@@ -758,10 +774,10 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
             const int64_t kt = k0 + it;
             const bool second = kt >= g.kt1;
             const int32_t c = (int32_t)((second ? kt - g.kt1 : kt) * kDepth);
-            const uint32_t st = ring + s * kMidStage;
-            bar_expect(full(s), kMidStage);
-            half(st, second ? &g.a2 : &g.a, a.a_cols, ix, c, full(s));
-            half(st + kHalf, second ? &g.b2 : &g.b, a.b_cols, jx, c, full(s));
+            const uint32_t st = ring + s * stage;
+            bar_expect(full(s), (uint32_t)stage);
+            half(st, second ? &g.a2 : &g.a, a.a_cols, ix, c, 128, full(s));
+            half(st + kHalf, second ? &g.b2 : &g.b, a.b_cols, jx, c, g.wide, full(s));
         };
         const int ahead = rounds < g.stages ? rounds : g.stages;
         for (int it = 0; it < ahead; ++it)
@@ -776,7 +792,7 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
             __syncwarp();
             if (++s == g.stages) s = 0, phase ^= 1;
         }
-    } else if (warp == 5) {                                  // the products
+    } else if (warp == kOneWarps + 1) {                                  // the products
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          saddr(&tmem_base)), "r"(128u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -786,7 +802,7 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
         const bool one = elect_one();
         const uint32_t tmem = tmem_base;
         const Layout la = layout_of(a.a_cols), lb = layout_of(a.b_cols);
-        const uint32_t desc = shape_desc<DT>(a.a_cols, a.b_cols) | ((128u >> 3) << 17) |
+        const uint32_t desc = shape_desc<DT>(a.a_cols, a.b_cols) | ((uint32_t)(g.wide >> 3) << 17) |
                               ((128u >> 4) << 24);
         int s = 0;
         uint32_t phase = 0;
@@ -795,8 +811,8 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if (one) {
-                const uint64_t da = at(la, ring + s * kMidStage);
-                const uint64_t db = at(lb, ring + s * kMidStage + kHalf);
+                const uint64_t da = at(la, ring + s * stage);
+                const uint64_t db = at(lb, ring + s * stage + kHalf);
                 const int64_t kt = k0 + it;
                 const int64_t left = a.k - (kt >= g.kt1 ? kt - g.kt1 : kt) * kDepth;
                 const int steps = left >= kDepth ? 4 : (int)((left + 15) / 16);
@@ -823,45 +839,48 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
         if (lane == 0) atomicAdd(&g_matmul_timeouts, 1u);
         failed = 1;
     }
-    __syncwarp();
-    const int64_t i0 = tm * 128, j0 = tn * 128;
+    if (g.splits > 1) cluster_arrive();                      // the ring is free
     // all copies have landed and all products have read them: the stages' place is free
     float *part = reinterpret_cast<float *>(dyn + (ring - saddr(dyn)));
-    float *staged = part + kMidPart / 4 + warp * 32 * kStagePad;
-    if (warp < 4 && ok) {
-        const uint32_t lanes = tmem_base + ((uint32_t)(warp * 32) << 16);
+    const int row = warp % 4 * 32;
+    const uint32_t lanes = tmem_base + ((uint32_t)row << 16);
+    if (g.splits == 1) {
+        if (warp < kOneWarps && ok && i0 + row < a.m) {
+            float *staged = part + warp * 32 * kStagePad;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-            if (j0 + c >= a.n) break;
-            uint32_t r[32];
-            load32(lanes + c, r);
-            if (g.splits == 1) {
+            for (int c = warp / 4 * 32; c < g.wide; c += kOneWarps / 4 * 32) {
+                Beside<DT, ODT, false> beside;
+                if (g.vec && j0 + c + 32 <= a.n && i0 + row + lane < a.m)
+                    beside.ask(a, i0 + row + lane, j0 + c);
+                uint32_t r[32];
+                load32(lanes + c, r);
                 float z[32], z2[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(r[e]), z2[e] = 0.0f;
-                finish_rows<DT, ODT, false>(a, g.vec != 0, staged, i0 + warp * 32, j0 + c, z, z2);
-            } else {
-                float4 *row = reinterpret_cast<float4 *>(part + (warp * 32 + lane) * kMidPad + c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    row[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                         __uint_as_float(r[4 * e + 2]),
-                                         __uint_as_float(r[4 * e + 3]));
+                finish_rows<DT, ODT, false, true>(a, g.vec != 0, staged, i0 + row, a.m, j0 + c,
+                                                  beside, z, z2);
             }
         }
-    }
-    if (g.splits > 1) {
-        cluster_sync();
-        const int rows = (int)(a.m - i0 < 128 ? a.m - i0 : 128);
-        if (!failed) join<DT, ODT, false, 4>(a, part, kMidPad, g, rank, i0, j0, rows);
-        cluster_sync();       // the peers have read this block's shared memory
+    } else {
+        if (warp < kOneWarps && ok) {
+#pragma unroll 1
+            for (int c = warp / 4 * 16; c < 128; c += kOneWarps / 4 * 16) {
+                float v[16];
+                load16(lanes + c, v);
+                float4 *to = reinterpret_cast<float4 *>(part + (row + lane) * kPitch + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+        }
+        settle<DT, ODT, false>(a, split, part, join_bar, failed, g.vec != 0, i0, j0);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
         for (int s = 0; s < g.stages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
     __syncthreads();
-    if (warp == 5)
+    if (warp == kOneWarps + 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(128u));
 }
@@ -1072,6 +1091,9 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
 #pragma unroll 1
             for (int c = turn * 32; c < wide; c += 64) {
                 const uint32_t from = tmem + lanes + b * 256 + c;
+                Beside<DT, ODT, GATED> beside;
+                if (g.vec && j0 + c + 32 <= a.n && i0 + lane < a.m)
+                    beside.ask(a, i0 + lane, j0 + c);
                 uint32_t r[32], r2[32];
                 load32(from, r);
                 if constexpr (GATED) load32(from + half, r2);
@@ -1081,7 +1103,8 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
                     z[e] = __uint_as_float(r[e]);
                     z2[e] = GATED ? __uint_as_float(r2[e]) : 0.0f;
                 }
-                finish_rows<DT, ODT, GATED>(a, g.vec != 0, staged, i0, j0 + c, z, z2);
+                finish_rows<DT, ODT, GATED, false>(a, g.vec != 0, staged, i0, a.m, j0 + c, beside, z,
+                                                   z2);
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
@@ -1296,7 +1319,7 @@ struct Room {
 
 // The split and the ring's length that leave the fullest SM the fewest stages, a join
 // counting as kJoin of them, as long as all clusters find a place at once.
-// `smem(stages)`: a block's shared memory; `most`: stages of the longest ring.
+// `smem(stages, splits)`: a block's shared memory; `most`: stages of the longest ring.
 template <class Smem>
 void choose_split(OneArgs &g, int64_t tiles, int sms, const void *kernel, Room &room, int most,
                   int blocks_sm, Smem smem)
@@ -1305,7 +1328,7 @@ void choose_split(OneArgs &g, int64_t tiles, int sms, const void *kernel, Room &
     auto ring = [&](int splits, int per_sm) {
         const int64_t rounds = (g.kt + splits - 1) / splits;
         int st = rounds < 1 ? 1 : rounds < most ? (int)rounds : most;
-        while (st > 0 && (smem(st) + 1024) * per_sm > kSmemSm) --st;
+        while (st > 0 && (smem(st, splits) + 1024) * per_sm > kSmemSm) --st;
         return st;
     };
     g.splits = 1;
@@ -1318,7 +1341,7 @@ void choose_split(OneArgs &g, int64_t tiles, int sms, const void *kernel, Room &
         if (cost >= least) continue;
         // (blocks that share an SM want three stages at least to keep their copies coming)
         const int st = ring(n, (int)per_sm);
-        if (st < 1 || (st < 3 && st < rounds) || room.of(kernel, n, st, smem(st)) < tiles) continue;
+        if (st < 1 || (st < 3 && st < rounds) || room.of(kernel, n, st, smem(st, n)) < tiles) continue;
         least = cost;
         g.splits = n;
         g.stages = st;
@@ -1330,7 +1353,7 @@ cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
     using Tl = Tile<GATED>;
     static std::atomic<uint64_t> done{0};
-    static Room room[8];                              // for each width of a tile
+    static Room room[2][8];                           // for each width of a tile
     const auto kernel = matmul_kernel<DT, ODT, GATED>;
     cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSmemBlock, done);
     if (e != cudaSuccess) return e;
@@ -1343,40 +1366,50 @@ cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
     g.tiles_n = (a.n + 127) / 128;
-    g.vec = runs_aligned(a, ODT == F32 ? 16 : 8, ODT == F32 ? 4 : 2);
+    g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
     const int64_t tiles = g.tiles_n * tiles_m;
     int most = (kSmemBlock - 1024) / Tl::stage(g.nt);
     if (most > Tl::kStages) most = Tl::kStages;
-    auto smem = [&](int stages) { return Tl::smem(stages, g.nt, g.span); };
-    choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room[g.nt / 16 - 1], most,
+    const bool staged = !g.vec || a.n % 32;           // finish_rows may need its room
+    auto smem = [&](int stages, int splits) { return Tl::smem(stages, g.nt, splits, staged); };
+    choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room[staged][g.nt / 16 - 1], most,
                  kMostBlocks, smem);
     const int64_t blocks = tiles * g.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    Clusters c(blocks, g.splits, smem(g.stages), s);
+    Clusters c(blocks, g.splits, smem(g.stages, g.splits), s);
     return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
 }
 
 template <int DT, int ODT> cudaError_t mid_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
-    static Room room;
+    static Room room[2];
     const auto kernel = matmul_mid_kernel<DT, ODT>;
     cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSmemBlock, done);
     if (e != cudaSuccess) return e;
     OneArgs g;
-    e = operand_maps(a, g, 128, 128);
-    if (e != cudaSuccess) return e;
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
-    g.tiles_n = (a.n + 127) / 128;
+    // (100 x 256 by 64 columns c: with 64 columns of the result a block XX us, with 128 XX)
+    g.wide = g.kt <= 16 && ((a.n + 63) / 64) * ((a.m + 127) / 128) <= sms ? 64 : 128;
+    e = operand_maps(a, g, 128, g.wide);
+    if (e != cudaSuccess) return e;
+    g.tiles_n = (a.n + g.wide - 1) / g.wide;
     g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
     g.nt = g.span = 128;
+    const bool staged = !g.vec || a.n % 32;
+    auto smem = [&](int stages, int splits) { return mid_smem(stages, g.wide, splits, staged); };
     const int64_t tiles = g.tiles_n * ((a.m + 127) / 128);
-    choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room, kMidStages, 2,
-                 mid_smem);
+    if (g.wide == 128) {
+        choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room[staged],
+                     kMidStages, 2, smem);
+    } else {
+        g.splits = 1;
+        g.stages = g.kt < kMidStages ? (int)g.kt : kMidStages;
+    }
     const int64_t blocks = tiles * g.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    Clusters c(blocks, g.splits, mid_smem(g.stages), s);
+    Clusters c(blocks, g.splits, smem(g.stages, g.splits), s);
     return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
 }
 
