@@ -347,34 +347,27 @@ matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ row
 // The accumulator's 128 lanes are 128 rows of B (128 consecutive columns of
 // the result, so that a warp's stores are contiguous), its columns up to 128 rows of
 // A: with few tokens the tile is as narrow as they are, and the product reads
-// the weights once.  A gated block has two accumulators, of the same lanes,
-// side by side.  One warp issues the copies, one the products, eight write.
+// the weights once.  A gated block's lanes are 64 rows of B and the same 64 of B2.  One warp issues the copies, one the products, eight write.
 // With fewer tiles than SMs the columns c are split over a cluster of up to 8
 // blocks, whose partial sums join through distributed shared memory in the blocks'
 // order.
-__host__ __device__ constexpr int split_floats(int weights, int span, int splits);
-constexpr int staged_floats(int weights);
+__host__ __device__ constexpr int split_floats(int span, int splits);
+constexpr int staged_floats(bool gated);
 
-template <bool GATED> struct Tile {
-    static constexpr int kWeights = GATED ? 2 : 1;
+struct Tile {
     static constexpr int kStages = 8;                       // at most
-    static __host__ __device__ constexpr int stage(int nt)
-    {
-        return kWeights * kHalf + nt * kLine;
-    }
+    static __host__ __device__ constexpr int stage(int nt) { return kHalf + nt * kLine; }
     static __host__ __device__ constexpr int tmem(int nt)
     {
-        const int c = kWeights * nt;
-        return c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : 256;
+        return nt <= 32 ? 32 : nt <= 64 ? 64 : 128;
     }
     // A block's share of an SM's shared memory is at least its share of the tensor
     // memory, so that no block waits for tensor memory that another one
     // holds: two that wait for their cluster peers so would wait forever.
-    static int smem(int stages, int nt, int splits, bool staged)
+    static int smem(int stages, int nt, int splits, bool staged, bool gated)
     {
         // the sums, when they are done, a split's shares of them, and room to reorder
-        const int part =
-            (split_floats(kWeights, nt, splits) + (staged ? staged_floats(kWeights) : 0)) * 4;
+        const int part = (split_floats(nt, splits) + (staged ? staged_floats(gated) : 0)) * 4;
         const int ring = stages * stage(nt) > part ? stages * stage(nt) : part;
         const int share = (kSmemSm / (512 / tmem(nt)) + 127) / 128 * 128;
         return ring + 1024 > share ? ring + 1024 : share;
@@ -402,22 +395,22 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 // ---- joining a split
 //
 // Every block of a split has partial sums of the whole tile, rows of 128 columns of the
-// result (kPitch floats apart, a gated block's second ones `span` rows
-// later) in its shared memory.  The rows are shared out; each block sends every other
+// result (kPitch floats apart; of a gated block 64 and their 64 second ones) in its
+// shared memory.  The rows are shared out; each block sends every other
 // one's share there by one bulk copy and adds up what it receives in the blocks' order.
 constexpr int kPitch = 132;                  // a lane a row: no two of eight on one bank
 
 struct Split {
     static constexpr int pitch = kPitch;
-    int rows, span, weights, splits;
+    int rows, span, splits;
     uint32_t rank;
 
     __device__ __forceinline__ int first(uint32_t q) const { return rows * (int)q / splits; }
     __device__ __forceinline__ int share() const { return (span + splits - 1) / splits; }
     // where block q's sums for this block arrive, behind its own
-    __device__ __forceinline__ int slot(uint32_t q, int w) const
+    __device__ __forceinline__ int slot(uint32_t q) const
     {
-        return (weights * span + ((int)q * weights + w) * share()) * pitch;
+        return (span + (int)q * share()) * pitch;
     }
     __device__ __forceinline__ uint32_t bytes(uint32_t q) const
     {
@@ -427,15 +420,14 @@ struct Split {
     __device__ __forceinline__ void expect(uint32_t bar) const
     {
         bar_init(bar, 1);
-        bar_expect(bar, (uint32_t)((splits - 1) * weights) * bytes(rank));
+        bar_expect(bar, (uint32_t)(splits - 1) * bytes(rank));
     }
 };
 
 // Floats of shared memory that a split's block needs.
-__host__ __device__ constexpr int split_floats(int weights, int span, int splits)
+__host__ __device__ constexpr int split_floats(int span, int splits)
 {
-    return (weights * span + (splits > 1 ? splits * weights * ((span + splits - 1) / splits) : 0)) *
-           kPitch;
+    return (span + (splits > 1 ? splits * ((span + splits - 1) / splits) : 0)) * kPitch;
 }
 
 // By one thread, once every block's sums and barrier are there.
@@ -444,22 +436,20 @@ __device__ __forceinline__ void send_shares(const Split &t, const float *part, u
     for (int d = 1; d < t.splits; ++d) {
         const uint32_t q = (t.rank + d) % t.splits, bytes = t.bytes(q);
         if (!bytes) continue;
-        for (int w = 0; w < t.weights; ++w)
-            asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes"
-                         " [%0], [%1], %2, [%3];" ::"r"(
-                             peer_addr(saddr(part + t.slot(t.rank, w)), q)),
-                         "r"(saddr(part + (w * t.span + t.first(q)) * t.pitch)), "r"(bytes),
-                         "r"(peer_addr(bar, q)) : "memory");
+        asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes"
+                     " [%0], [%1], %2, [%3];" ::"r"(peer_addr(saddr(part + t.slot(t.rank)), q)),
+                     "r"(saddr(part + t.first(q) * t.pitch)), "r"(bytes), "r"(peer_addr(bar, q))
+                     : "memory");
     }
 }
 
 // 32 columns from c on of row r, which is in this block's share, added up.
-__device__ __forceinline__ void sum32(const Split &t, const float *part, int r, int w, int c,
+__device__ __forceinline__ void sum32(const Split &t, const float *part, int r, int c,
                                       float (&z)[32])
 {
-    const float *own = part + (w * t.span + r) * kPitch + c;
-    const float *in = part + t.slot(0, w) + (r - t.first(t.rank)) * kPitch + c;
-    const int step = t.slot(1, w) - t.slot(0, w);
+    const float *own = part + r * kPitch + c;
+    const float *in = part + t.slot(0) + (r - t.first(t.rank)) * kPitch + c;
+    const int step = t.slot(1) - t.slot(0);
     const float4 *first = reinterpret_cast<const float4 *>(t.rank == 0 ? own : in);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -481,9 +471,9 @@ __device__ __forceinline__ void sum32(const Split &t, const float *part, int r, 
     }
 }
 
-constexpr int staged_floats(int weights)
+constexpr int staged_floats(bool gated)
 {
-    return kOneThreads / 32 * weights * 32 * kStagePad;
+    return kOneThreads / 32 * (gated ? 2 : 1) * 32 * kStagePad;
 }
 
 // Writes the result of this block's share of the rows: the warps take 32 rows by 32
@@ -495,18 +485,18 @@ __device__ __forceinline__ bool join(const ProductArgs &a, const Split &t, float
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int from = t.first(t.rank), end = t.first(t.rank + 1);
-    float *staged = part + split_floats(t.weights, t.span, t.splits) +
-                    warp * (GATED ? 2 : 1) * 32 * kStagePad;
+    float *staged = part + split_floats(t.span, t.splits) + warp * (GATED ? 2 : 1) * 32 * kStagePad;
+    constexpr int kAcross = GATED ? 2 : 4;
 #pragma unroll 1
-    for (int item = warp; item < (end - from + 31) / 32 * 4; item += kOneThreads / 32) {
-        const int r0 = from + (item >> 2) * 32, c = (item & 3) * 32;
+    for (int item = warp; item < (end - from + 31) / 32 * kAcross; item += kOneThreads / 32) {
+        const int r0 = from + item / kAcross * 32, c = item % kAcross * 32;
         const int r = r0 + lane < end ? r0 + lane : end - 1;
         Beside<DT, ODT, GATED> beside;
         if (vec && j0 + c + 32 <= a.n) beside.ask(a, i0 + r, j0 + c);
         if (t.splits > 1 && !bar_wait(bar, 0)) return false;
         float z[32], z2[32];
-        sum32(t, part, r, 0, c, z);
-        if constexpr (GATED) sum32(t, part, r, 1, c, z2);
+        sum32(t, part, r, c, z);
+        if constexpr (GATED) sum32(t, part, r, 64 + c, z2);
         finish_rows<DT, ODT, GATED, true>(a, vec, staged, i0 + r0, i0 + end, j0 + c, beside, z,
                                           z2);
     }
@@ -544,7 +534,8 @@ template <int DT, int ODT, bool GATED>
 __global__ void __launch_bounds__(kOneThreads, kMostBlocks)
 matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ OneArgs g)
 {
-    using Tl = Tile<GATED>;
+    using Tl = Tile;
+    constexpr int kAcross = GATED ? 64 : 128;                // columns of the result
     const int stage = Tl::stage(g.nt);
     const uint32_t columns = Tl::tmem(g.nt);
     extern __shared__ unsigned char dyn[];
@@ -563,7 +554,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
 
     const int64_t i0 = tm * g.nt;
     const int cols = (int)(a.m - i0 < g.nt ? a.m - i0 : g.nt);
-    const Split split = {cols, g.span, Tl::kWeights, g.splits, rank};
+    const Split split = {cols, g.span, g.splits, rank};
 
     bool ok = true;
     if (warp == kOneWarps) {                                         // the copies
@@ -585,25 +576,27 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
         }
         __syncwarp();
         pdl_wait();
-        const int32_t jx = (int32_t)(tn * 128), ix = (int32_t)(tm * g.nt);
-        auto weights = [&](uint32_t to, const CUtensorMap *map, int32_t c, uint32_t bar) {
-            if (a.b_cols) {
-                box_load(to, map, jx, c, bar);
-                box_load(to + kHalf / 2, map, jx + 64, c, bar);
-            } else {
-                box_load(to, map, c, jx, bar);
-            }
-        };
+        const int32_t jx = (int32_t)(tn * kAcross), ix = (int32_t)(tm * g.nt);
         auto load = [&](int it, int s) {
             const int64_t kt = k0 + it;
             const bool second = kt >= g.kt1;
             const int32_t c = (int32_t)((second ? kt - g.kt1 : kt) * kDepth);
-            const uint32_t st = ring + s * stage, tok = st + Tl::kWeights * kHalf;
+            const uint32_t st = ring + s * stage;
             bar_expect(full(s), (uint32_t)stage);
-            weights(st, !GATED && second ? &g.b2 : &g.b, c, full(s));
-            if constexpr (GATED) weights(st + kHalf, &g.b2, c, full(s));
+            if constexpr (GATED) {
+                box_load(st, &g.b, c, jx, full(s));
+                box_load(st + kHalf / 2, &g.b2, c, jx, full(s));
+            } else {
+                const CUtensorMap *b = second ? &g.b2 : &g.b;
+                if (a.b_cols) {
+                    box_load(st, b, jx, c, full(s));
+                    box_load(st + kHalf / 2, b, jx + 64, c, full(s));
+                } else {
+                    box_load(st, b, c, jx, full(s));
+                }
+            }
             const CUtensorMap *map = second ? &g.a2 : &g.a;
-            box_load(tok, map, c, ix, full(s));
+            box_load(st + kHalf, map, c, ix, full(s));
         };
         // the first stages' copies need not wait for the other warps
         const int ahead = rounds < g.stages ? rounds : g.stages;
@@ -639,7 +632,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if (one) {
                 const uint32_t st = ring + s * stage;
-                const uint64_t db = at(lb, st), da = at(la, st + Tl::kWeights * kHalf);
+                const uint64_t db = at(lb, st), da = at(la, st + kHalf);
                 // columns past k are zeros: their products are left out
                 const int64_t kt = k0 + it;
                 const int64_t left = a.k - (kt >= g.kt1 ? kt - g.kt1 : kt) * kDepth;
@@ -648,9 +641,6 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
                 for (int q = 0; q < 4; ++q) {
                     if (q >= steps) break;
                     mma1(tmem, db + q * lb.step, da + q * la.step, desc, it > 0 || q > 0);
-                    if constexpr (GATED)
-                        mma1(tmem + g.nt, db + (kHalf >> 4) + q * lb.step, da + q * la.step, desc,
-                             it > 0 || q > 0);
                 }
                 commit(empty(s));
             }
@@ -677,8 +667,8 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
     if (warp < kOneWarps && ok) {
         const uint32_t lanes = tmem_base + ((uint32_t)(warp % 4 * 32) << 16);
 #pragma unroll 1
-        for (int c = warp / 4 * 16; c < Tl::kWeights * g.nt; c += kOneWarps / 4 * 16) {
-            float v[16];                                     // (the second sums follow the first)
+        for (int c = warp / 4 * 16; c < g.nt; c += kOneWarps / 4 * 16) {
+            float v[16];
             load16(lanes + c, v);
             float *to = part + c * kPitch + warp % 4 * 32 + lane;
 #pragma unroll
@@ -686,7 +676,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
         }
     }
     settle<DT, ODT, GATED>(a, split, part, join_bar, failed, g.vec != 0, i0,
-                                          tn * 128);
+                                          tn * kAcross);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
@@ -713,8 +703,8 @@ __host__ __device__ constexpr int mid_stage(int wide) { return kHalf + wide * kL
 constexpr int mid_smem(int stages, int wide, int splits, bool staged)
 {
     const int ring = stages * mid_stage(wide);
-    const int part = ((splits > 1 ? split_floats(1, 128, splits) : 0) +
-                      (staged ? staged_floats(1) : 0)) * 4;
+    const int part = ((splits > 1 ? split_floats(128, splits) : 0) +
+                      (staged ? staged_floats(false) : 0)) * 4;
     return (ring > part ? ring : part) + 1024;
 }
 static_assert(mid_smem(kMidStages, 128, 8, true) <= kSmemBlock, "one block's shared memory");
@@ -740,7 +730,7 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     const int64_t i0 = tm * 128, j0 = tn * g.wide;
     const int stage = mid_stage(g.wide);
     const int rows = (int)(a.m - i0 < 128 ? a.m - i0 : 128);
-    const Split split = {rows, 128, 1, g.splits, rank};
+    const Split split = {rows, 128, g.splits, rank};
 
     bool ok = true;
     if (warp == kOneWarps) {                                         // the copies
@@ -1331,9 +1321,10 @@ void choose_split(OneArgs &g, int64_t tiles, int sms, const void *kernel, Room &
         while (st > 0 && (smem(st, splits) + 1024) * per_sm > kSmemSm) --st;
         return st;
     };
+    const int64_t deep = (tiles + sms - 1) / sms;        // whole tiles of the fullest SM
     g.splits = 1;
-    g.stages = ring(1, 1);
-    int64_t least = (tiles + sms - 1) / sms * g.kt;
+    g.stages = ring(1, deep < blocks_sm ? (int)deep : blocks_sm);
+    int64_t least = deep * g.kt;
     for (int n = 2; n <= 8 && g.kt >= 2 * n; ++n) {
         const int64_t per_sm = (tiles * n + sms - 1) / sms;
         if (per_sm > blocks_sm) break;
@@ -1351,7 +1342,8 @@ void choose_split(OneArgs &g, int64_t tiles, int sms, const void *kernel, Room &
 template <int DT, int ODT, bool GATED>
 cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
-    using Tl = Tile<GATED>;
+    using Tl = Tile;
+    constexpr int kAcross = GATED ? 64 : 128;
     static std::atomic<uint64_t> done{0};
     static Room room[2][8];                           // for each width of a tile
     const auto kernel = matmul_kernel<DT, ODT, GATED>;
@@ -1361,17 +1353,19 @@ cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
     const int64_t tiles_m = (a.m + 127) / 128;
     g.nt = (int)((a.m + tiles_m * 16 - 1) / (tiles_m * 16) * 16);
     g.span = g.nt;
-    e = operand_maps(a, g, g.nt, 128);
+    e = operand_maps(a, g, g.nt, kAcross);
     if (e != cudaSuccess) return e;
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
-    g.tiles_n = (a.n + 127) / 128;
+    g.tiles_n = (a.n + kAcross - 1) / kAcross;
     g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
     const int64_t tiles = g.tiles_n * tiles_m;
     int most = (kSmemBlock - 1024) / Tl::stage(g.nt);
     if (most > Tl::kStages) most = Tl::kStages;
     const bool staged = !g.vec || a.n % 32;           // finish_rows may need its room
-    auto smem = [&](int stages, int splits) { return Tl::smem(stages, g.nt, splits, staged); };
+    auto smem = [&](int stages, int splits) { 
+        return Tl::smem(stages, g.nt, splits, staged, GATED);
+    };
     choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room[staged][g.nt / 16 - 1], most,
                  kMostBlocks, smem);
     const int64_t blocks = tiles * g.splits;
