@@ -19,12 +19,16 @@ namespace act {
 constexpr float kTwoA = 1.5957691216057308f;          // 2 sqrt(2 / pi)
 constexpr float kCube = 0.044715f;
 
-__device__ __forceinline__ float exp_of(float v)
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float power_of_2(float v)
 {
     float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(v, 1.4426950408889634f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v));
     return e;
 }
+
+__device__ __forceinline__ float exp_of(float v) { return power_of_2(__fmul_rn(v, kLog2e)); }
 
 __device__ __forceinline__ float inverse(float v)
 {
@@ -33,17 +37,17 @@ __device__ __forceinline__ float inverse(float v)
     return r;
 }
 
-// 1 / (1 + exp(-v)).  Where exp(-v) overflows it is 0.
-__device__ __forceinline__ float logistic(float v)
+// p = 1 / (1 + 2^-u).  Where the power overflows it is 0.
+__device__ __forceinline__ float logistic(float u)
 {
-    return inverse(__fadd_rn(1.0f, exp_of(-v)));
+    return inverse(__fadd_rn(1.0f, power_of_2(-u)));
 }
 
-// p = 1 / (1 + exp(-v)) and q = p (1 - p).
-__device__ __forceinline__ void logistic2(float v, float &p, float &q)
+// p and q = p (1 - p).
+__device__ __forceinline__ void logistic2(float u, float &p, float &q)
 {
-    const float e = exp_of(-fabsf(v)), r = inverse(__fadd_rn(1.0f, e)), s = __fmul_rn(e, r);
-    p = v < 0.0f ? s : r;
+    const float e = power_of_2(-fabsf(u)), r = inverse(__fadd_rn(1.0f, e)), s = __fmul_rn(e, r);
+    p = u < 0.0f ? s : r;
     q = __fmul_rn(s, r);
 }
 
@@ -71,9 +75,10 @@ __device__ __forceinline__ float normal(float v)
     return v < 0.0f ? q : __fsub_rn(1.0f, q);
 }
 
-__device__ __forceinline__ float tanh_arg(float v)     // twice tanh's argument
+// (1 + tanh(a (v + c v^3))) / 2 is the logistic of this, for 2 to its power.
+__device__ __forceinline__ float tanh_arg(float v, float v2)
 {
-    return __fmul_rn(__fmul_rn(kTwoA, v), __fmaf_rn(kCube, __fmul_rn(v, v), 1.0f));
+    return __fmul_rn(v, __fmaf_rn(kTwoA * kLog2e * kCube, v2, kTwoA * kLog2e));
 }
 
 __device__ __forceinline__ float value(float v, int32_t kind)
@@ -81,8 +86,8 @@ __device__ __forceinline__ float value(float v, int32_t kind)
     switch (kind) {
     case kActRelu: return v < 0.0f ? 0.0f : v;
     case kActGelu: return __fmul_rn(v, normal(v));
-    case kActGeluTanh: return __fmul_rn(v, logistic(tanh_arg(v)));
-    case kActSilu: return __fmul_rn(v, logistic(v));
+    case kActGeluTanh: return __fmul_rn(v, logistic(tanh_arg(v, __fmul_rn(v, v))));
+    case kActSilu: return __fmul_rn(v, logistic(__fmul_rn(v, kLog2e)));
     default: return v;
     }
 }
@@ -104,15 +109,15 @@ __device__ __forceinline__ void both(float v, int32_t kind, float &y, float &slo
         return;
     }
     case kActGeluTanh: {
-        logistic2(tanh_arg(v), p, q);
+        const float v2 = __fmul_rn(v, v);
+        logistic2(tanh_arg(v, v2), p, q);
         y = __fmul_rn(v, p);
         // q is 0 long before v^2 is held back, which keeps 0 times an overflow out
-        const float v2 = fminf(__fmul_rn(v, v), 1e9f);
-        slope = __fmaf_rn(__fmul_rn(__fmul_rn(v, q), kTwoA), __fmaf_rn(3.0f * kCube, v2, 1.0f), p);
+        slope = __fmaf_rn(__fmul_rn(v, q), __fmaf_rn(3.0f * kCube * kTwoA, fminf(v2, 1e9f), kTwoA), p);
         return;
     }
     case kActSilu:
-        logistic2(v, p, q);
+        logistic2(__fmul_rn(v, kLog2e), p, q);
         y = __fmul_rn(v, p);
         slope = __fmaf_rn(v, q, p);
         return;

@@ -22,7 +22,7 @@ constexpr int kWarps = kThreads / 32;
 template <int DT, bool VEC, bool PACKED> struct Kept {
     rows::Eight<DT, VEC> e;
     uint2 codes;
-    float up;
+    uint32_t scale;
 
     __device__ __forceinline__ void ask(const rows::In &m, const pack8::View &q, int64_t r,
                                         int64_t c0, int64_t cols)
@@ -30,10 +30,10 @@ template <int DT, bool VEC, bool PACKED> struct Kept {
         if constexpr (PACKED) {
             const int64_t c = c0 + 8 * (threadIdx.x & 31);
             codes = make_uint2(0, 0);
-            up = 0.0f;
+            scale = 0;
             if (c < q.wide) {
                 codes = *reinterpret_cast<const uint2 *>(q.codes + r * q.wide + c);
-                up = pack8::up(q.scales[r * (q.wide / pack8::kBlock) + c / pack8::kBlock]);
+                scale = q.scales[r * (q.wide / pack8::kBlock) + c / pack8::kBlock];
             }
         } else {
             e.ask(m, r, c0, cols);
@@ -43,8 +43,7 @@ template <int DT, bool VEC, bool PACKED> struct Kept {
     __device__ __forceinline__ void take(float (&f)[8]) const
     {
         if constexpr (PACKED) {
-            pack8::values4(codes.x, up, pack8::most<DT>(), f);
-            pack8::values4(codes.y, up, pack8::most<DT>(), f + 4);
+            pack8::values8<DT>(codes, scale, f);
         } else {
             e.take(f);
         }
@@ -77,7 +76,7 @@ __device__ __forceinline__ void put_sum(void *out, int32_t dt, int64_t c, float 
 // ONE: a strip's blocks are a cluster, whose first block adds up the sums of all through
 // distributed shared memory, in their order; otherwise a second kernel does.
 template <int DT, bool VEC, bool PACKED, bool ONE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, VEC ? 4 : 1)
 activation_grad_kernel(const __grid_constant__ ActGrad a)
 {
     __shared__ float joined[kWarps][256];

@@ -55,25 +55,31 @@ __device__ __forceinline__ uint32_t codes4(const float *v, float d)
     return codes2(v[0], v[1], d) | codes2(v[2], v[3], d) << 16;
 }
 
-// The values of four codes, no larger than `most`: rounding up to a code
-// must not make an infinity of a finite element.
-__device__ __forceinline__ void values4(uint32_t c, float u, float most, float *v)
-{
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> (16 * h)),
-                                                         __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r));
-        const float x = __fmul_rn(f.x, u), y = __fmul_rn(f.y, u);
-        // (a comparison, not fminf, so that NaN stays NaN)
-        v[2 * h] = fabsf(x) > most ? copysignf(most, x) : x;
-        v[2 * h + 1] = fabsf(y) > most ? copysignf(most, y) : y;
-    }
-}
-
 template <int DT> __device__ __forceinline__ float most()
 {
     return DT == F32 ? 3.4028234663852886e38f : DT == BF16 ? 3.3895313892515355e38f : 65504.0f;
+}
+
+// The values of eight codes of a block with the scale exponent e, none larger than the
+// type's largest: rounding up to a code must not make an infinity of a finite
+// element.  Only blocks whose scale times 448 is beyond that are looked at.
+template <int DT>
+__device__ __forceinline__ void values8(uint2 c, uint32_t e, float (&v)[8])
+{
+    const float u = up(e);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const uint32_t two = (h < 2 ? c.x : c.y) >> (16 * (h & 1));
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r));
+        v[2 * h] = __fmul_rn(f.x, u);
+        v[2 * h + 1] = __fmul_rn(f.y, u);
+    }
+    if (e >= (DT == F16 ? 127 + 8 : 127 + 119)) {        // 448 * 2^8 > 65504, 448 * 2^119 > 2^127
+#pragma unroll
+        for (int i = 0; i < 8; ++i)                      // (a comparison: NaN stays NaN)
+            v[i] = fabsf(v[i]) > most<DT>() ? copysignf(most<DT>(), v[i]) : v[i];
+    }
 }
 
 // A matrix in 8 bits.
@@ -131,29 +137,6 @@ __device__ __forceinline__ void put_eight(const View &q, int64_t r, int64_t j, b
     *reinterpret_cast<uint2 *>(q.codes + r * q.wide + j) = make_uint2(codes4(v, d),
                                                                       codes4(v + 4, d));
     if ((threadIdx.x & 3) == 0) q.scales[r * (q.wide / kBlock) + j / kBlock] = (unsigned char)e;
-}
-
-// Eight neighbouring lanes hold them, 4 each: lane l's from column j on.
-__device__ __forceinline__ void put_four(const View &q, int64_t r, int64_t j, bool in,
-                                         const float (&v)[4])
-{
-    uint32_t top = max(max(magnitude(v[0]), magnitude(v[1])), max(magnitude(v[2]), magnitude(v[3])));
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (!in) return;
-    const uint32_t e = exponent(top);
-    *reinterpret_cast<uint32_t *>(q.codes + r * q.wide + j) = codes4(v, down(e));
-    if ((threadIdx.x & 7) == 0) q.scales[r * (q.wide / kBlock) + j / kBlock] = (unsigned char)e;
-}
-
-// Eight elements of row r from column j on (a whole eight below the pitch).
-template <int DT>
-__device__ __forceinline__ void get_eight(const View &q, int64_t r, int64_t j, float (&v)[8])
-{
-    const uint2 c = *reinterpret_cast<const uint2 *>(q.codes + r * q.wide + j);
-    const float u = up(q.scales[r * (q.wide / kBlock) + j / kBlock]);
-    values4(c.x, u, most<DT>(), v);
-    values4(c.y, u, most<DT>(), v + 4);
 }
 
 }  // namespace pack8
