@@ -21,32 +21,23 @@ constexpr int kWarps = kThreads / 32;
 // Values kept in the type or in 8 bits.
 template <int DT, bool VEC, bool PACKED> struct Kept {
     rows::Eight<DT, VEC> e;
-    uint2 codes;
-    uint32_t scale;
-
-    __device__ __forceinline__ void ask(const rows::In &m, const pack8::View &q, int64_t r,
+    __device__ __forceinline__ void ask(const rows::In &m, const pack8::View &, int64_t r,
                                         int64_t c0, int64_t cols)
     {
-        if constexpr (PACKED) {
-            const int64_t c = c0 + 8 * (threadIdx.x & 31);
-            codes = make_uint2(0, 0);
-            scale = 0;
-            if (c < q.wide) {
-                codes = *reinterpret_cast<const uint2 *>(q.codes + r * q.wide + c);
-                scale = q.scales[r * (q.wide / pack8::kBlock) + c / pack8::kBlock];
-            }
-        } else {
-            e.ask(m, r, c0, cols);
-        }
+        e.ask(m, r, c0, cols);
     }
-
-    __device__ __forceinline__ void take(float (&f)[8]) const
+    __device__ __forceinline__ void take(float *, float (&f)[8]) const { e.take(f); }
+};
+template <int DT, bool VEC> struct Kept<DT, VEC, true> {
+    rows::Packed<DT, VEC> e;
+    __device__ __forceinline__ void ask(const rows::In &, const pack8::View &q, int64_t r,
+                                        int64_t c0, int64_t)
     {
-        if constexpr (PACKED) {
-            pack8::values8<DT>(codes, scale, f);
-        } else {
-            e.take(f);
-        }
+        e.ask(q, r, c0);
+    }
+    __device__ __forceinline__ void take(float *shared, float (&f)[8]) const
+    {
+        e.take(shared, f);
     }
 };
 
@@ -79,10 +70,10 @@ template <int DT, bool VEC, bool PACKED, bool ONE>
 __global__ void __launch_bounds__(kThreads, VEC ? 4 : 1)
 activation_grad_kernel(const __grid_constant__ ActGrad a)
 {
-    __shared__ float joined[kWarps][256];
+    __shared__ float joined[kWarps][256];        // (until the end, room to turn values)
     pdl_wait();
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const int64_t c0 = (int64_t)blockIdx.x * 256, step = (int64_t)gridDim.y * kWarps;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     constexpr int U = DT == F32 ? 1 : 2;         // rows on their way together
@@ -104,7 +95,7 @@ activation_grad_kernel(const __grid_constant__ ActGrad a)
             dye[u].take(d);
             if (a.act != kActNone) {
                 float z[8];
-                ze[u].take(z);
+                ze[u].take(joined[warp], z);
                 act::with_kind(a.act, [&](auto kind) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -121,7 +112,7 @@ activation_grad_kernel(const __grid_constant__ ActGrad a)
     }
     if (!a.parts && !a.dbias) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) joined[warp][lane * 8 + e] = sum[e];
+    for (int e = 0; e < 8; ++e) joined[warp][rows::column<VEC>(e)] = sum[e];
     __syncthreads();
     const int64_t c = c0 + threadIdx.x;
     float v = joined[0][threadIdx.x];
@@ -174,9 +165,11 @@ __global__ void __launch_bounds__(kThreads)
 gated_grad_kernel(const __grid_constant__ GatedGrad a)
 {
     constexpr int U = kRuns<DT>;
+    __shared__ float turned[PACKED && !VEC ? kWarps : 1][256];
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t w = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * U;
+    const int warp = threadIdx.x >> 5;
+    const int64_t w = ((int64_t)blockIdx.x * kWarps + warp) * U;
     int64_t r[U], c0[U];
     rows::Eight<DT, VEC> dhe[U];
     Kept<DT, VEC, PACKED> ge[U], ue[U];
@@ -193,8 +186,8 @@ gated_grad_kernel(const __grid_constant__ GatedGrad a)
         if (r[k] >= a.n) break;
         float dh[8], g[8], u[8], f[8], d[8];
         dhe[k].take(dh);
-        ge[k].take(g);
-        ue[k].take(u);
+        ge[k].take(turned[PACKED && !VEC ? warp : 0], g);
+        ue[k].take(turned[PACKED && !VEC ? warp : 0], u);
         act::with_kind(a.act, [&](auto kind) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -219,9 +212,11 @@ pack8_kernel(const __grid_constant__ rows::In x, const __grid_constant__ pack8::
              int64_t n, int64_t cols, int64_t runs)
 {
     constexpr int U = kRuns<DT>;
+    __shared__ float turned[VEC ? 1 : kWarps][256];
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t w = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * U;
+    const int warp = threadIdx.x >> 5;
+    const int64_t w = ((int64_t)blockIdx.x * kWarps + warp) * U;
     int64_t r[U], c0[U];
     rows::Eight<DT, VEC> e[U];
 #pragma unroll
@@ -234,8 +229,7 @@ pack8_kernel(const __grid_constant__ rows::In x, const __grid_constant__ pack8::
         if (r[k] >= n) break;
         float f[8];
         e[k].take(f);
-        const int64_t c = c0[k] + 8 * (threadIdx.x & 31);
-        pack8::put_eight(q, r[k], c, c < q.wide, f);
+        rows::pack<VEC>(q, r[k], c0[k], turned[VEC ? 0 : warp], f);
     }
 }
 
@@ -245,21 +239,23 @@ unpack8_kernel(const __grid_constant__ pack8::View q, int64_t n, int64_t cols, i
                void *out, int64_t stride)
 {
     constexpr int U = kRuns<DT>;
+    __shared__ float turned[VEC ? 1 : kWarps][256];
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t w = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * U;
+    const int warp = threadIdx.x >> 5;
+    const int64_t w = ((int64_t)blockIdx.x * kWarps + warp) * U;
     int64_t r[U], c0[U];
-    Kept<DT, VEC, true> e[U];
+    rows::Packed<DT, VEC> e[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         rows::run_at(w + k, runs, r[k], c0[k]);
-        if (r[k] < n) e[k].ask(rows::In{}, q, r[k], c0[k], cols);
+        if (r[k] < n) e[k].ask(q, r[k], c0[k]);
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         if (r[k] >= n) break;
         float f[8];
-        e[k].take(f);
+        e[k].take(turned[VEC ? 0 : warp], f);
         rows::put<DT, VEC>(out, stride, r[k], c0[k], cols, f);
     }
 }
@@ -337,8 +333,8 @@ cudaError_t launch_activation_grad(int32_t dt, int32_t bdt, const ActGradArgs &a
     const int64_t parts = act_parts(a.rows, a.cols);
     if (a.rows > 0) {
         const bool one = a.dbias && a.rows <= kOneRows;
-        ActGrad g = {rows::in(a.dy, a.rows, a.cols, a.dy_stride, dt),
-                     rows::in(a.kept, a.rows, a.cols, a.kept_stride, dt),
+        ActGrad g = {rows::in(a.dy, a.dy_stride),
+                     rows::in(a.kept, a.kept_stride),
                      pack8::view(a.kept_q, a.rows, a.cols), a.rows, a.cols, a.act, a.dz,
                      a.dz_stride, a.dbias && !one ? workspace : nullptr,
                      one ? a.dbias : nullptr, bdt, a.accumulate};
@@ -382,9 +378,9 @@ cudaError_t launch_gated_grad(int32_t dt, const GatedGradArgs &a, cudaStream_t s
 {
     if (a.rows <= 0 || a.cols <= 0) return cudaSuccess;
     const int64_t runs = (a.cols + 255) / 256;
-    GatedGrad g = {rows::in(a.dh, a.rows, a.cols, a.dh_stride, dt),
-                   rows::in(a.gate, a.rows, a.cols, a.kept_stride, dt),
-                   rows::in(a.up, a.rows, a.cols, a.kept_stride, dt),
+    GatedGrad g = {rows::in(a.dh, a.dh_stride),
+                   rows::in(a.gate, a.kept_stride),
+                   rows::in(a.up, a.kept_stride),
                    pack8::view(a.gate_q, a.rows, a.cols), pack8::view(a.up_q, a.rows, a.cols),
                    a.rows, a.cols, runs, a.act, a.dgate, a.dup, a.h, a.grad_stride, a.h_stride};
     const bool vec = rows_aligned(a.dh, a.dh_stride, dt, a.cols) &&
@@ -417,7 +413,7 @@ cudaError_t launch_pack8(int32_t dt, const void *x, int64_t rows, int64_t cols, 
     const int64_t runs = (cols + 255) / 256;
     const unsigned blocks = run_blocks(dt, rows, runs);
     if (!blocks) return cudaErrorInvalidValue;
-    const rows::In in = rows::in(x, rows, cols, stride, dt);
+    const rows::In in = rows::in(x, stride);
     const bool vec = rows_aligned(x, stride, dt, cols);
     return by_type(dt, [&](auto t) {
         constexpr int DT = decltype(t)::value;
