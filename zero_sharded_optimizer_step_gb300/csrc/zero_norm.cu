@@ -41,9 +41,21 @@ template <int W> __device__ __forceinline__ float row_sum(float v, float *shared
     return v;
 }
 
-__device__ __forceinline__ float rstd_of(float squares, int64_t dim, float eps)
+// 1 / sqrt(v) in two floats: the nearest one, and what it is off by, from v r^2 - 1,
+// whose first terms are exact.  An element's product with the weight is exact too (16-bit
+// types), so that the norm is off by little more than its last rounding: what is
+// packed goes to the code that it should but next to a border.
+struct Rstd {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Rstd rstd_of(float squares, int64_t dim, float eps)
 {
-    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(squares, (float)dim), eps)));
+    const float v = __fadd_rn(__fdiv_rn(squares, (float)dim), eps);
+    const float r = __frcp_rn(__fsqrt_rn(v)), t = __fmul_rn(v, r);
+    const float off = __fmaf_rn(-__fmaf_rn(v, r, -t), r, __fmaf_rn(-t, r, 1.0f));
+    const float lo = __fmul_rn(__fmul_rn(0.5f, r), off);
+    return {r, fabsf(lo) < r ? lo : 0.0f};       // (v of 0, infinity or NaN: r alone says it)
 }
 
 // x + r rounded to the type, as it is kept.
@@ -64,14 +76,17 @@ __device__ __forceinline__ void total(bool add, const rows::Eight<DT, VEC> &x,
 }
 
 template <int DT, bool VEC>
-__device__ __forceinline__ void finish(const Norm &a, int64_t row, int64_t c0, float rstd,
+__device__ __forceinline__ void finish(const Norm &a, int64_t row, int64_t c0, Rstd rstd,
                                        const rows::Eight<DT, VEC> &weight, float *turned,
                                        float (&s)[8])
 {
     float w[8];
     weight.take(w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = __fmul_rn(__fmul_rn(s[e], rstd), w[e]);
+    for (int e = 0; e < 8; ++e) {
+        const float p = __fmul_rn(s[e], w[e]);
+        s[e] = __fmaf_rn(p, rstd.hi, __fmul_rn(p, rstd.lo));
+    }
     if (a.y) rows::put<DT, VEC>(a.y, a.y_stride, row, c0, a.dim, s);
     if (a.q) rows::pack<VEC>(pack8::view(a.q, a.n, a.dim), row, c0, turned, s);
 }
@@ -115,9 +130,9 @@ norm_kernel(const __grid_constant__ Norm a)
             for (int e = 0; e < 8; ++e) squares = __fmaf_rn(s[g][e], s[g][e], squares);
         }
     }
-    const float rstd = rstd_of(row_sum<W>(squares, shared), a.dim, a.eps);
+    const Rstd rstd = rstd_of(row_sum<W>(squares, shared), a.dim, a.eps);
     if (!live) return;
-    if (a.rstd && warp % W == 0 && (threadIdx.x & 31) == 0) a.rstd[row] = rstd;
+    if (a.rstd && warp % W == 0 && (threadIdx.x & 31) == 0) a.rstd[row] = rstd.hi;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         if (kCut && first + g * (W * 256) >= a.dim) break;
@@ -145,8 +160,8 @@ norm_long_kernel(const __grid_constant__ Norm a)
 #pragma unroll
         for (int e = 0; e < 8; ++e) squares = __fmaf_rn(s[e], s[e], squares);
     }
-    const float rstd = rstd_of(row_sum<kWarps>(squares, shared), a.dim, a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    const Rstd rstd = rstd_of(row_sum<kWarps>(squares, shared), a.dim, a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd.hi;
     __syncwarp();
     const bool again = !a.sum && a.residual.p;   // the sum was not stored: it is made again
     const rows::In from = a.sum ? rows::In{a.sum, a.sum_stride} : a.x;
