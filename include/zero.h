@@ -818,9 +818,9 @@ int zero_rms_norm_grad(const void *dy, int64_t dy_stride, const void *dsum, int6
  * A is m by k, B n by k, out m by n of out_dtype (`dtype` or fp32).  a_cols != 0:
  * `a` (and a2) lies as the transpose, k rows of m; b_cols likewise, k rows of n.
  * a2 and b2 are both given or both NULL.  bias: [n] of `dtype`, or NULL;
- * residual: m by n of out_dtype, or NULL (NULL with accumulate); it may be out itself.  z, before
- * the activation, is kept in `kept` (`dtype`) or kept_q (packed from fp32).  A
- * linear layer y = act(x W^T + b) and its gradients, dz being dy through the
+ * residual: m by n of out_dtype, or NULL (NULL with accumulate); it may be out
+ * itself.  z, before the activation, is kept in `kept` (`dtype`) or kept_q (packed
+ * from fp32).  A linear layer y = act(x W^T + b) and its gradients, dz being dy through the
  * activation:
  *   zero_matmul(x, 0, W, 0, m, n, k, b, act)   -> y
  *   zero_matmul(dz, 0, W, 1, m, k, n)          -> dx
@@ -863,8 +863,9 @@ int zero_gated(const void *x, int64_t x_stride, const void *w_gate, int64_t gate
 /* The gradient through an activation and of a bias:
  *   dz = dy activation'(z),  dbias = sum over rows of dz (or += that)
  * z is read from `kept` or kept_q (neither is needed for ZERO_ACT_NONE).  dz
- * (`dtype`; it may be dy itself, with dy's stride) and dbias (bias_dtype) may be NULL, not both.  dbias sums dz
- * before its rounding, in fp32, in an order that depends on the sizes alone.
+ * (`dtype`; it may be dy itself, with dy's stride) and dbias (bias_dtype) may be
+ * NULL, not both.  dbias sums dz before its rounding, in fp32, in an order that depends
+ * on the sizes alone.
  * workspace: zero_activation_grad_workspace(rows, cols) bytes (-1 on a bad argument), 16-byte
  * aligned; not needed without dbias. */
 int64_t zero_activation_grad_workspace(int64_t rows, int64_t cols);

@@ -1,6 +1,7 @@
 """The norm, linear layers and gated blocks as torch functions (layers.py): values and
 gradients against autograd in 64 bits at what is kept, refusals, streams, graphs, and
 a block of them together."""
+import gc
 import threading
 
 import pytest
@@ -208,6 +209,44 @@ def test_gradients_of_awkward_shapes():
     assert not nw.grad.any()
     xt = randn(g, 72, 6).t()                                      # rows that are not runs
     assert torch.equal(z.linear(xt, w.detach()), z.linear(xt.contiguous(), w.detach()))
+
+
+def test_rows_of_nothing():
+    """No columns to go through: a product is its bias, a norm has no elements."""
+    g = gen(17)
+    x = torch.empty(2, 3, 0, dtype=BF, device=DEV, requires_grad=True)
+    w = torch.empty(40, 0, dtype=BF, device=DEV, requires_grad=True)
+    b = randn(g, 40, grad=True)
+    y = z.linear(x, w, b, "relu")
+    assert torch.equal(y, b.detach().relu().expand(2, 3, 40))
+    y.sum().backward()
+    assert x.grad.shape == x.shape and w.grad.shape == w.shape
+    assert torch.equal(b.grad, 6 * (b.detach() > 0).to(BF))
+    assert not z.gated(x, w, w).any()
+    nw = torch.empty(0, dtype=BF, device=DEV, requires_grad=True)
+    y, total, q = z.rms_norm(x, nw, residual=x, packed=True)
+    assert y.shape == total.shape == x.shape and (q.rows, q.cols) == (6, 0)
+    (y.sum() + total.sum()).backward()
+    assert nw.grad.shape == (0,)
+    assert z.linear(randn(g, 5, 64), torch.empty(0, 64, dtype=BF, device=DEV)).shape == (5, 0)
+
+
+@pytest.mark.parametrize("keep8", [False, True])
+def test_what_is_kept_is_freed_with_the_output(keep8):
+    """At once, without the collector: no reference goes round in a circle."""
+    p = params(gen(18))
+    h = randn(gen(19), 70, 64)
+    block(p, h, keep8)                           # what the first calls make is there
+    gc.collect()
+    gc.disable()
+    try:
+        before = torch.cuda.memory_allocated()
+        y = block(p, h, keep8)
+        assert torch.cuda.memory_allocated() > before
+        del y
+        assert torch.cuda.memory_allocated() == before
+    finally:
+        gc.enable()
 
 
 def test_second_derivatives_are_refused():

@@ -7,6 +7,12 @@
 //
 // z, g and u are read in the type or in 8 bits, straight from what the forward
 // pass kept.  Every matrix is read or written once, 256 columns of a row a warp.
+//
+// What bounds it: memory, where values are in the type (the gated gradient of 8192 x
+// 11008 131 us, 902 MB at 6.9 TB/s; 6400 columns through RELU with the bias's
+// 58, 315 MB at 5.4); else the instructions: GELU's normal
+// distribution function (76 us), taking values out of 8 bits (135) and packing them (54 for
+// 8192 x 11008, 273 MB).
 #include "zero_act.cuh"
 #include "zero_ops.h"
 #include "zero_pack8.cuh"

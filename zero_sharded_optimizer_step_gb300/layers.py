@@ -11,6 +11,11 @@ a rank's gradient buffer, or `embed_grad` and `Mx4Linear.weight_grad` write them
 there directly.  The lookup and dropout can be differentiated any number of
 times, everything else once: an attempt at more raises.
 
+Forward and backward can be captured in a CUDA graph.  As with any torch function, no
+eager graph of the same leaves may still be alive then (an output that was not
+freed, say): torch remembers its stream for the leaves and would draw that stream into the
+capture, which fails inside torch's engine.
+
 A product whose waits on the device run out stores nothing, and its call
 has long returned: where a program reads its losses it also asks for the counts
 (`zero_mx4_timeouts()` for the 4-bit ones, `zero_matmul_timeouts()` for the others, 0 when all is
@@ -30,6 +35,8 @@ and a block in 16 bits, what its backward pass needs kept in 8:
     h = linear(y, w_down, residual=h, keep8=True)
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -380,7 +387,7 @@ def _last(name, grads, *links):
 
 def _rows(x: torch.Tensor, k: int) -> torch.Tensor:
     """x's rows of k elements as a matrix that the library can take."""
-    rows = x.reshape(-1, k)
+    rows = x.reshape(math.prod(x.shape[:-1]), k)
     return rows if _rows_apart(rows) else rows.contiguous()
 
 
