@@ -103,6 +103,32 @@ def test_tiles_in_parts(a_cols, b_cols, m, n, k):
         assert out.untouched()
 
 
+# tiles of 192, 160, 176 and 240 rows of A, split over blocks, and what splits too little
+# once the rows of the result need a place to be turned in
+WIDE = [(384, 4096, 2112), (300, 4000, 2112), (333, 1600, 6400), (230, 6397, 1800)]
+
+
+@pytest.mark.parametrize("m,n,k", WIDE)
+@pytest.mark.parametrize("pad,offset", [(0, 0), (16, 16), (1, 1)])
+def test_wide_tiles_with_everything(m, n, k, pad, offset):
+    test_split_sums_with_everything(m, n, k, pad, offset)
+
+
+@pytest.mark.parametrize("m,n,k", [(384, 4096, 1090), (333, 1600, 3208)])
+def test_wide_tiles_of_two_pairs(m, n, k):
+    g = gen(m)
+    a, a2 = (randn(g, m, k, dtype=BF) for _ in range(2))
+    b, b2 = (randn(g, n, k, dtype=BF) for _ in range(2))
+    want, err = F.product(torch.cat([a, a2], 1).double(), torch.cat([b, b2], 1).double())
+    for b_cols in (False, True):
+        for pad in (0, 1):
+            out = space(m, n, BF)
+            product(as_lies(a, False, pad), False, as_lies(b, b_cols), b_cols, out,
+                    as_lies(a2, False), as_lies(b2, b_cols, pad))
+            F.within(out.t, want, err)
+            assert out.untouched()
+
+
 @pytest.mark.parametrize("m,n,k", [(2560, 1024, 72), (2560, 1000, 40), (6400, 800, 32),
                                    (6400, 801, 40), (5000, 600, 72)])
 def test_gated_tiles_in_parts(m, n, k):

@@ -386,8 +386,8 @@ matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ row
 //
 // The accumulator's 128 lanes are 128 rows of B (128 consecutive columns of
 // the result, so that a warp's stores are contiguous), its columns up to 128 rows of
-// A: with few tokens the tile is as narrow as they are, and the product reads
-// the weights once.  A gated block's lanes are 64 rows of B and the same 64 of B2.
+// A (256 in pick()'s wide tiles): with few tokens the tile is as narrow as they are,
+// and the product reads the weights once.  A gated block's lanes are 64 rows of B and the same 64 of B2.
 // One warp issues the copies, one the products, eight write.  With fewer tiles
 // than SMs the columns c are split over a cluster of up to 8 blocks, whose partial sums
 // join through distributed shared memory in the blocks' order.
@@ -403,7 +403,7 @@ struct Tile {
     static __host__ __device__ constexpr int stage(int nt) { return kHalf + nt * kLine; }
     static __host__ __device__ constexpr int tmem(int nt)
     {
-        return nt <= 32 ? 32 : nt <= 64 ? 64 : 128;
+        return nt <= 32 ? 32 : nt <= 64 ? 64 : nt <= 128 ? 128 : 256;
     }
     // A block's share of an SM's shared memory is at least its share of the tensor
     // memory, so that no block waits for tensor memory that another one
@@ -736,8 +736,7 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
 // block's warps write the result from the tensor memory, a row a lane.
 //
 // What bounds it: the shared memory, which takes in and gives out 32 KB a stage: 437
-// clocks against the 256 of its products.  333 rows by 1600 x 6400: 13.8 us with
-// bias, GELU and residual.
+// clocks against the 256 of its products.  256 x 4096 x 4096: 14 us.
 constexpr int kMidStages = 7;
 
 __host__ __device__ constexpr int mid_stage(int wide) { return kHalf + wide * kLine; }
@@ -1263,14 +1262,15 @@ cudaError_t operand_maps(const ProductArgs &a, G &g, int rows_a, int rows_b)
     return e;
 }
 
-// Whether runs of so many bytes of a row of everything that is written beside
-// the result, and of what is added, lie on their boundaries.
-bool runs_aligned(const ProductArgs &a, int64_t bytes, int out_size)
+// Whether runs of 32 bytes of a row of everything that is written beside the
+// result, and of what is added, lie on their boundaries.
+template <int ODT> bool in_runs(const ProductArgs &a)
 {
-    auto rows = [&](const void *p, int64_t stride, int es) {
-        return !p || ((uintptr_t)p % bytes == 0 && stride * es % bytes == 0);
+    constexpr int kOut = ODT == F32 ? 4 : 2;
+    auto rows = [](const void *p, int64_t stride, int es) {
+        return !p || ((uintptr_t)p % 32 == 0 && stride * es % 32 == 0);
     };
-    return rows(a.out, a.stride, out_size) && rows(a.residual, a.residual_stride, out_size) &&
+    return rows(a.out, a.stride, kOut) && rows(a.residual, a.residual_stride, kOut) &&
            rows(a.kept, a.kept_stride, 2) && rows(a.kept2, a.kept_stride, 2) &&
            ((uintptr_t)a.bias & 15) == 0;
 }
@@ -1303,7 +1303,7 @@ cudaError_t pair_go(const ProductArgs &a, int sms, cudaStream_t s)
     if (e != cudaSuccess) return e;
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
-    g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
+    g.vec = in_runs<ODT>(a);
     // The last turn's tiles, if they leave pairs idle, in halves or quarters (a gated
     // tile's parts are 32 columns at least, and whole blocks of 32).
     const int64_t tiles = g.tiles_n * g.tiles_m, left = tiles % (sms / 2);
@@ -1358,101 +1358,149 @@ struct Room {
     }
 };
 
-// The split and the ring's length that leave the fullest SM the fewest stages, a join
+// A split, the ring's length, and the stages of the fullest SM.
+struct Cut {
+    int splits, stages;
+    int64_t least;
+};
+
+// The split that leaves the fullest SM the fewest of the kt stages, a join
 // counting as kJoin of them, as long as all clusters find a place at once.
 // `smem(stages, splits)`: a block's shared memory; `most`: stages of the longest ring.
 template <class Smem>
-void choose_split(OneArgs &g, int64_t tiles, int sms, const void *kernel, Room &room, int most,
-                  int blocks_sm, Smem smem)
+Cut choose_split(int64_t kt, int64_t tiles, int sms, const void *kernel, Room &room, int most,
+                 int blocks_sm, Smem smem)
 {
     constexpr int kJoin = 4;
     auto ring = [&](int splits, int per_sm) {
-        const int64_t rounds = (g.kt + splits - 1) / splits;
+        const int64_t rounds = (kt + splits - 1) / splits;
         int st = rounds < 1 ? 1 : rounds < most ? (int)rounds : most;
         while (st > 0 && (smem(st, splits) + 1024) * per_sm > kSmemSm) --st;
         return st;
     };
     const int64_t deep = (tiles + sms - 1) / sms;        // whole tiles of the fullest SM
-    g.splits = 1;
-    g.stages = ring(1, deep < blocks_sm ? (int)deep : blocks_sm);
-    int64_t least = deep * g.kt;
-    for (int n = 2; n <= 8 && g.kt >= 2 * n; ++n) {
+    Cut c = {1, ring(1, deep < blocks_sm ? (int)deep : blocks_sm), deep * kt};
+    for (int n = 2; n <= 8 && kt >= 2 * n; ++n) {
         const int64_t per_sm = (tiles * n + sms - 1) / sms;
         if (per_sm > blocks_sm) break;
-        const int64_t rounds = (g.kt + n - 1) / n, cost = per_sm * rounds + kJoin;
-        if (cost >= least) continue;
+        const int64_t rounds = (kt + n - 1) / n, cost = per_sm * rounds + kJoin;
+        if (cost >= c.least) continue;
         // (blocks that share an SM want three stages at least to keep their copies coming)
         const int st = ring(n, (int)per_sm);
-        if (st < 1 || (st < 3 && st < rounds) || room.of(kernel, n, st, smem(st, n)) < tiles) continue;
-        least = cost;
-        g.splits = n;
-        g.stages = st;
+        if (st < 1 || (st < 3 && st < rounds) || room.of(kernel, n, st, smem(st, n)) < tiles)
+            continue;
+        c = {n, st, cost};
     }
+    return c;
 }
 
+int64_t stages_of(const ProductArgs &a)
+{
+    return (a.k + kDepth - 1) / kDepth * (a.a2 ? 2 : 1);
+}
+
+template <int ODT> bool needs_staging(const ProductArgs &a)       // finish_rows does
+{
+    return !in_runs<ODT>(a) || a.n % 32;
+}
+
+// (The device's answer on room depends on what a kernel is allowed: asked first.)
+template <int DT, int ODT, bool GATED> cudaError_t allow_one()
+{
+    static std::atomic<uint64_t> done{0};
+    return allow_shared(reinterpret_cast<const void *>(matmul_kernel<DT, ODT, GATED>), kSmemBlock,
+                        done);
+}
+
+template <int DT, int ODT> cudaError_t allow_mid()
+{
+    static std::atomic<uint64_t> done{0};
+    return allow_shared(reinterpret_cast<const void *>(matmul_mid_kernel<DT, ODT>), kSmemBlock,
+                        done);
+}
+
+// matmul_kernel with `tiles_m` tiles of rows of A, as equal as multiples of 16 can be.
 template <int DT, int ODT, bool GATED>
-cudaError_t one_go(const ProductArgs &a, int sms, cudaStream_t s)
+Cut one_cut(const ProductArgs &a, int64_t tiles_m, int nt, int sms)
 {
     using Tl = Tile;
     constexpr int kAcross = GATED ? 64 : 128;
-    static std::atomic<uint64_t> done{0};
-    static Room room[2][8];                           // for each width of a tile
+    static Room room[2][16];                          // for each width of a tile
+    const bool staged = needs_staging<ODT>(a);
+    int most = (kSmemBlock - 1024) / Tl::stage(nt);
+    if (most > Tl::kStages) most = Tl::kStages;
+    return choose_split(stages_of(a), (a.n + kAcross - 1) / kAcross * tiles_m, sms,
+                        reinterpret_cast<const void *>(matmul_kernel<DT, ODT, GATED>),
+                        room[staged][nt / 16 - 1], most, kMostBlocks, [&](int stages, int splits) {
+                            return Tl::smem(stages, nt, splits, staged);
+                        });
+}
+
+int width(int64_t m, int64_t tiles_m) { return (int)((m + tiles_m * 16 - 1) / (tiles_m * 16) * 16); }
+
+template <int DT, int ODT, bool GATED>
+cudaError_t one_go(const ProductArgs &a, int64_t tiles_m, int sms, cudaStream_t s)
+{
+    using Tl = Tile;
+    constexpr int kAcross = GATED ? 64 : 128;
     const auto kernel = matmul_kernel<DT, ODT, GATED>;
-    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSmemBlock, done);
+    cudaError_t e = allow_one<DT, ODT, GATED>();
     if (e != cudaSuccess) return e;
     OneArgs g;
-    const int64_t tiles_m = (a.m + 127) / 128;
-    g.nt = (int)((a.m + tiles_m * 16 - 1) / (tiles_m * 16) * 16);
-    g.span = g.nt;
+    g.nt = g.span = width(a.m, tiles_m);
     e = operand_maps(a, g, g.nt, kAcross);
     if (e != cudaSuccess) return e;
     g.kt1 = (a.k + kDepth - 1) / kDepth;
-    g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
+    g.kt = stages_of(a);
     g.tiles_n = (a.n + kAcross - 1) / kAcross;
-    g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
-    const int64_t tiles = g.tiles_n * tiles_m;
-    int most = (kSmemBlock - 1024) / Tl::stage(g.nt);
-    if (most > Tl::kStages) most = Tl::kStages;
-    const bool staged = !g.vec || a.n % 32;           // finish_rows may need its room
-    auto smem = [&](int stages, int splits) { return Tl::smem(stages, g.nt, splits, staged); };
-    choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel),
-                 room[staged][g.nt / 16 - 1], most, kMostBlocks, smem);
-    const int64_t blocks = tiles * g.splits;
+    g.vec = in_runs<ODT>(a);
+    const Cut cut = one_cut<DT, ODT, GATED>(a, tiles_m, g.nt, sms);
+    g.splits = cut.splits, g.stages = cut.stages;
+    const int64_t blocks = g.tiles_n * tiles_m * g.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    Clusters c(blocks, g.splits, smem(g.stages, g.splits), s);
+    Clusters c(blocks, g.splits, Tl::smem(g.stages, g.nt, g.splits, needs_staging<ODT>(a)), s);
     return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
+}
+
+// matmul_mid_kernel: tiles of 128 by 128, or, `wide`, 64.
+template <int DT, int ODT> Cut mid_cut(const ProductArgs &a, int wide, int sms)
+{
+    static Room room[2];
+    const bool staged = needs_staging<ODT>(a);
+    const int64_t kt = stages_of(a);
+    if (wide < 128) return {1, kt < kMidStages ? (int)kt : kMidStages, 0};
+    return choose_split(kt, (a.n + wide - 1) / wide * ((a.m + 127) / 128), sms,
+                        reinterpret_cast<const void *>(matmul_mid_kernel<DT, ODT>), room[staged],
+                        kMidStages, 2, [&](int stages, int splits) {
+                            return mid_smem(stages, wide, splits, staged);
+                        });
+}
+
+// (100 x 256 by 64 columns c: with 64 columns of the result a block 2.7 us, with 128 3.1)
+int mid_width(const ProductArgs &a, int sms)
+{
+    return stages_of(a) <= 16 && (a.n + 63) / 64 * ((a.m + 127) / 128) <= sms ? 64 : 128;
 }
 
 template <int DT, int ODT> cudaError_t mid_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
-    static std::atomic<uint64_t> done{0};
-    static Room room[2];
     const auto kernel = matmul_mid_kernel<DT, ODT>;
-    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSmemBlock, done);
+    cudaError_t e = allow_mid<DT, ODT>();
     if (e != cudaSuccess) return e;
     OneArgs g;
     g.kt1 = (a.k + kDepth - 1) / kDepth;
-    g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
-    // (100 x 256 by 64 columns c: with 64 columns of the result a block 2.7 us, with 128 3.1)
-    g.wide = g.kt <= 16 && ((a.n + 63) / 64) * ((a.m + 127) / 128) <= sms ? 64 : 128;
+    g.kt = stages_of(a);
+    g.wide = mid_width(a, sms);
     e = operand_maps(a, g, 128, g.wide);
     if (e != cudaSuccess) return e;
     g.tiles_n = (a.n + g.wide - 1) / g.wide;
-    g.vec = runs_aligned(a, 32, ODT == F32 ? 4 : 2);
+    g.vec = in_runs<ODT>(a);
     g.nt = g.span = 128;
-    const bool staged = !g.vec || a.n % 32;
-    auto smem = [&](int stages, int splits) { return mid_smem(stages, g.wide, splits, staged); };
-    const int64_t tiles = g.tiles_n * ((a.m + 127) / 128);
-    if (g.wide == 128) {
-        choose_split(g, tiles, sms, reinterpret_cast<const void *>(kernel), room[staged],
-                     kMidStages, 2, smem);
-    } else {
-        g.splits = 1;
-        g.stages = g.kt < kMidStages ? (int)g.kt : kMidStages;
-    }
-    const int64_t blocks = tiles * g.splits;
+    const Cut cut = mid_cut<DT, ODT>(a, g.wide, sms);
+    g.splits = cut.splits, g.stages = cut.stages;
+    const int64_t blocks = g.tiles_n * ((a.m + 127) / 128) * g.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    Clusters c(blocks, g.splits, smem(g.stages, g.splits), s);
+    Clusters c(blocks, g.splits, mid_smem(g.stages, g.wide, g.splits, needs_staging<ODT>(a)), s);
     return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
 }
 
@@ -1491,13 +1539,33 @@ cudaError_t pick(const ProductArgs &a, int sms, cudaStream_t s)
 {
     if (one_row(a)) return matvec_go<DT, ODT, GATED>(a, sms, s);
     // Few rows, or no more tiles of 128 by 128 than SMs: the single blocks, whose
-    // columns c can be split.  Beyond that the pairs (333 x 1600 x 6400, 39 tiles:
-    // 14 us in single blocks, split three ways).
+    // columns c can be split.  Beyond that the pairs.
     const int64_t tiles = ((a.n + 127) / 128) * ((a.m + 127) / 128);
     if (a.k > 0 && a.m > 64 && tiles > sms) return pair_go<DT, ODT, GATED>(a, sms, s);
-    if constexpr (!GATED)
+    if constexpr (!GATED) {
+        if (a.k > 0 && a.m > 128 && !a.a_cols && mid_width(a, sms) == 128) {
+            // Tiles of up to 256 rows of A by 128 of B, where they leave clearly less to
+            // the fullest SM, a stage's time being that of its rows: 384 x 4096 x 4096
+            // 18.2 us in tiles of 128 by 128, 16.6 in tiles of 192; 333 x 1600 x 6400
+            // 13.9 and 13.6.  With 5% less to do they are behind (1024 x 1024 x 4096, 3
+            // blocks a tile for 2: 13.2 us and 14.5).
+            cudaError_t e = allow_one<DT, ODT, false>();
+            if (e == cudaSuccess) e = allow_mid<DT, ODT>();
+            if (e != cudaSuccess) return e;
+            const int64_t few = (a.m + 255) / 256;
+            int64_t best = 0, least = mid_cut<DT, ODT>(a, 128, sms).least * 256 / 8 * 7;
+            for (int64_t tiles_m = few; tiles_m < few + 3; ++tiles_m) {
+                const int nt = width(a.m, tiles_m);
+                const Cut c = one_cut<DT, ODT, false>(a, tiles_m, nt, sms);
+                if (c.stages < 1 || c.least * (128 + nt) >= least) continue;
+                least = c.least * (128 + nt);
+                best = tiles_m;
+            }
+            if (best) return one_go<DT, ODT, false>(a, best, sms, s);
+        }
         if (a.k > 0 && (a.m > 64 || a.a_cols)) return mid_go<DT, ODT>(a, sms, s);
-    return one_go<DT, ODT, GATED>(a, sms, s);
+    }
+    return one_go<DT, ODT, GATED>(a, (a.m + 127) / 128, sms, s);
 }
 
 // An operand's place in the workspace, if it needs one: bytes.
