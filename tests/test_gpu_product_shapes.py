@@ -129,6 +129,13 @@ def test_wide_tiles_of_two_pairs(m, n, k):
             assert out.untouched()
 
 
+@pytest.mark.parametrize("m,n,k", [(2, 9801, 72), (77, 9900, 136), (128, 16001, 72),
+                                   (300, 4096, 200), (130, 6000, 500)])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (16, 16), (1, 1)])
+def test_gated_in_one_tile_a_sm(m, n, k, pad, offset):
+    test_split_gated(m, n, k, pad, offset)
+
+
 @pytest.mark.parametrize("m,n,k", [(2560, 1024, 72), (2560, 1000, 40), (6400, 800, 32),
                                    (6400, 801, 40), (5000, 600, 72)])
 def test_gated_tiles_in_parts(m, n, k):

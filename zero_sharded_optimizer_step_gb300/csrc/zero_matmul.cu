@@ -393,8 +393,8 @@ matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ row
 // join through distributed shared memory in the blocks' order.
 //
 // What bounds it: the weights' bytes.  77 rows gated, 2 x 11008 x 4096 values of
-// weights, take 35.8 us (180 MB at 5.0 TB/s); with 128 rows of either weight a tile, in
-// two accumulators, 37.1.
+// weights, took 35.8 us (180 MB at 5.0 TB/s) in its 172 tiles before matmul_mid_kernel
+// had them; with 128 rows of either weight a tile, in two accumulators, 37.1.
 __host__ __device__ constexpr int split_floats(int span, int splits);
 constexpr int staged_floats();
 
@@ -737,9 +737,17 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
 //
 // What bounds it: the shared memory, which takes in and gives out 32 KB a stage: 437
 // clocks against the 256 of its products.  256 x 4096 x 4096: 14 us.
+//
+// A gated block's tile has up to 128 rows of A in the lanes, as many rows of A in a stage as
+// there are, and `wide` rows of either weight, whose sums are the accumulator's columns
+// beside one another: tiles of 64, 96 or 128, so that each SM has one.
 constexpr int kMidStages = 7;
 
 __host__ __device__ constexpr int mid_stage(int wide) { return kHalf + wide * kLine; }
+__host__ __device__ constexpr int mid_gated_stage(int nt, int wide)
+{
+    return (nt + 2 * wide) * kLine;
+}
 
 constexpr int mid_smem(int stages, int wide, int splits, bool staged)
 {
@@ -750,8 +758,16 @@ constexpr int mid_smem(int stages, int wide, int splits, bool staged)
 }
 static_assert(mid_smem(kMidStages, 128, 8, true) <= kSmemBlock, "one block's shared memory");
 
-template <int DT, int ODT>
-__global__ void __launch_bounds__(kOneThreads, 2)
+// (its share of an SM's at least, half, as its tensor memory is: see Tile)
+constexpr int mid_gated_smem(int stages, int nt, int wide)
+{
+    const int ring = stages * mid_gated_stage(nt, wide);
+    const int most = ring > staged_floats() * 4 ? ring : staged_floats() * 4;
+    return most + 1024 > kSmemSm / 2 ? most + 1024 : kSmemSm / 2;
+}
+
+template <int DT, int ODT, bool GATED>
+__global__ void __launch_bounds__(kOneThreads, GATED ? 1 : 2)
 matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ OneArgs g)
 {
     extern __shared__ unsigned char dyn[];
@@ -769,7 +785,9 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     auto empty = [&](int s) { return saddr(&bars[kMidStages + s]); };
 
     const int64_t i0 = tm * 128, j0 = tn * g.wide;
-    const int stage = mid_stage(g.wide);
+    const int stage = GATED ? mid_gated_stage(g.nt, g.wide) : mid_stage(g.wide);
+    const int b_at = GATED ? g.nt * kLine : kHalf;       // B in a stage
+    constexpr uint32_t kColumns = GATED ? 256 : 128;     // of tensor memory
     const int rows = (int)(a.m - i0 < 128 ? a.m - i0 : 128);
     const Split split = {rows, 128, g.splits, rank};
 
@@ -807,6 +825,12 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
             const int32_t c = (int32_t)((second ? kt - g.kt1 : kt) * kDepth);
             const uint32_t st = ring + s * stage;
             bar_expect(full(s), (uint32_t)stage);
+            if constexpr (GATED) {
+                box_load(st, &g.a, c, ix, full(s));
+                box_load(st + b_at, &g.b, c, jx, full(s));
+                box_load(st + b_at + g.wide * kLine, &g.b2, c, jx, full(s));
+                return;
+            }
             half(st, second ? &g.a2 : &g.a, a.a_cols, ix, c, 128, full(s));
             half(st + kHalf, second ? &g.b2 : &g.b, a.b_cols, jx, c, g.wide, full(s));
         };
@@ -825,7 +849,7 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
         }
     } else if (warp == kOneWarps + 1) {                                  // the products
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         saddr(&tmem_base)), "r"(128u) : "memory");
+                         saddr(&tmem_base)), "r"(kColumns) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncthreads();
@@ -833,7 +857,9 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
         const bool one = elect_one();
         const uint32_t tmem = tmem_base;
         const Layout la = layout_of(a.a_cols), lb = layout_of(a.b_cols);
-        const uint32_t desc = shape_desc<DT>(a.a_cols, a.b_cols) | ((uint32_t)(g.wide >> 3) << 17) |
+        // (a gated block's lanes past its rows of A hold what follows them, which nothing reads)
+        const uint32_t desc = shape_desc<DT>(a.a_cols, a.b_cols) |
+                              ((uint32_t)((GATED ? 2 : 1) * g.wide >> 3) << 17) |
                               ((128u >> 4) << 24);
         int s = 0;
         uint32_t phase = 0;
@@ -843,7 +869,7 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if (one) {
                 const uint64_t da = at(la, ring + s * stage);
-                const uint64_t db = at(lb, ring + s * stage + kHalf);
+                const uint64_t db = at(lb, ring + s * stage + b_at);
                 const int64_t kt = k0 + it;
                 const int64_t left = a.k - (kt >= g.kt1 ? kt - g.kt1 : kt) * kDepth;
                 const int steps = left >= kDepth ? 4 : (int)((left + 15) / 16);
@@ -880,19 +906,23 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
             float *staged = part + warp * 32 * kStagePad;
 #pragma unroll 1
             for (int c = warp / 4 * 32; c < g.wide; c += kOneWarps / 4 * 32) {
-                Beside<DT, ODT, false> beside;
+                Beside<DT, ODT, GATED> beside;
                 if (g.vec && j0 + c + 32 <= a.n && i0 + row + lane < a.m)
                     beside.ask(a, i0 + row + lane, j0 + c);
-                uint32_t r[32];
+                uint32_t r[32], r2[32];
                 load32(lanes + c, r);
+                if constexpr (GATED) load32(lanes + g.wide + c, r2);
                 float z[32], z2[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(r[e]), z2[e] = 0.0f;
-                finish_rows<DT, ODT, false>(a, g.vec != 0, staged, i0 + row, a.m, j0 + c,
+                for (int e = 0; e < 32; ++e) {
+                    z[e] = __uint_as_float(r[e]);
+                    z2[e] = GATED ? __uint_as_float(r2[e]) : 0.0f;
+                }
+                finish_rows<DT, ODT, GATED>(a, g.vec != 0, staged, i0 + row, a.m, j0 + c,
                                                   beside, z, z2);
             }
         }
-    } else {
+    } else if constexpr (!GATED) {
         if (warp < kOneWarps && ok) {
 #pragma unroll 1
             for (int c = warp / 4 * 16; c < 128; c += kOneWarps / 4 * 16) {
@@ -913,7 +943,7 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     __syncthreads();
     if (warp == kOneWarps + 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
-                     "r"(128u));
+                     "r"(kColumns));
 }
 
 // ------------------------------------------------------------ the pair kernel
@@ -1415,8 +1445,8 @@ template <int DT, int ODT, bool GATED> cudaError_t allow_one()
 template <int DT, int ODT> cudaError_t allow_mid()
 {
     static std::atomic<uint64_t> done{0};
-    return allow_shared(reinterpret_cast<const void *>(matmul_mid_kernel<DT, ODT>), kSmemBlock,
-                        done);
+    return allow_shared(reinterpret_cast<const void *>(matmul_mid_kernel<DT, ODT, false>),
+                        kSmemBlock, done);
 }
 
 // matmul_kernel with `tiles_m` tiles of rows of A, as equal as multiples of 16 can be.
@@ -1470,8 +1500,8 @@ template <int DT, int ODT> Cut mid_cut(const ProductArgs &a, int wide, int sms)
     const int64_t kt = stages_of(a);
     if (wide < 128) return {1, kt < kMidStages ? (int)kt : kMidStages, 0};
     return choose_split(kt, (a.n + wide - 1) / wide * ((a.m + 127) / 128), sms,
-                        reinterpret_cast<const void *>(matmul_mid_kernel<DT, ODT>), room[staged],
-                        kMidStages, 2, [&](int stages, int splits) {
+                        reinterpret_cast<const void *>(matmul_mid_kernel<DT, ODT, false>),
+                        room[staged], kMidStages, 2, [&](int stages, int splits) {
                             return mid_smem(stages, wide, splits, staged);
                         });
 }
@@ -1484,7 +1514,7 @@ int mid_width(const ProductArgs &a, int sms)
 
 template <int DT, int ODT> cudaError_t mid_go(const ProductArgs &a, int sms, cudaStream_t s)
 {
-    const auto kernel = matmul_mid_kernel<DT, ODT>;
+    const auto kernel = matmul_mid_kernel<DT, ODT, false>;
     cudaError_t e = allow_mid<DT, ODT>();
     if (e != cudaSuccess) return e;
     OneArgs g;
@@ -1501,6 +1531,30 @@ template <int DT, int ODT> cudaError_t mid_go(const ProductArgs &a, int sms, cud
     const int64_t blocks = g.tiles_n * ((a.m + 127) / 128) * g.splits;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     Clusters c(blocks, g.splits, mid_smem(g.stages, g.wide, g.splits, needs_staging<ODT>(a)), s);
+    return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
+}
+
+// A gated block in one tile a SM, rows of A in the lanes.
+template <int DT> cudaError_t mid_gated_go(const ProductArgs &a, int wide, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = matmul_mid_kernel<DT, DT, true>;
+    cudaError_t e = allow_shared(reinterpret_cast<const void *>(kernel), kSmemBlock, done);
+    if (e != cudaSuccess) return e;
+    OneArgs g;
+    g.nt = a.m < 128 ? width(a.m, 1) : 128;
+    g.wide = wide;
+    e = operand_maps(a, g, g.nt, wide);
+    if (e != cudaSuccess) return e;
+    g.kt = g.kt1 = stages_of(a);
+    g.tiles_n = (a.n + wide - 1) / wide;
+    g.vec = in_runs<DT>(a);
+    g.splits = 1;
+    g.span = 128;
+    const int most = (kSmemBlock - 1024) / mid_gated_stage(g.nt, wide);
+    g.stages = most < kMidStages ? most : kMidStages;
+    if (g.kt < g.stages) g.stages = (int)g.kt;
+    Clusters c(g.tiles_n * ((a.m + 127) / 128), 1, mid_gated_smem(g.stages, g.nt, wide), s);
     return cudaLaunchKernelEx(&c.cfg, kernel, a, g);
 }
 
@@ -1564,6 +1618,21 @@ cudaError_t pick(const ProductArgs &a, int sms, cudaStream_t s)
             if (best) return one_go<DT, ODT, false>(a, best, sms, s);
         }
         if (a.k > 0 && (a.m > 64 || a.a_cols)) return mid_go<DT, ODT>(a, sms, s);
+    } else if (a.k > 0) {
+        // One tile a SM, as narrow as that allows, against tiles of 64 that may be split
+        // or be two on some SMs: by the bytes of the fullest SM.  (2 x 11008 x 4096, 115
+        // tiles of 96 and 172 of 64: 16 rows 31.4 us and 34.8, 77 rows 32.5 and 34.4; 256
+        // rows of 2 x 6400 x 1600 12.3 and 15.5.)
+        const int64_t tiles_m = (a.m + 127) / 128;
+        int wide = 64;
+        while (wide < 128 && (a.n + wide - 1) / wide * tiles_m > sms) wide += 32;
+        const int nt = a.m < 128 ? width(a.m, 1) : 128, one = width(a.m, tiles_m);
+        const cudaError_t e = allow_one<DT, ODT, true>();
+        if (e != cudaSuccess) return e;
+        if ((a.n + wide - 1) / wide * tiles_m <= sms &&
+            stages_of(a) * (nt + 2 * wide) * 8 <
+                one_cut<DT, ODT, true>(a, tiles_m, one, sms).least * (128 + one) * 7)
+            return mid_gated_go<DT>(a, wide, s);
     }
     return one_go<DT, ODT, GATED>(a, (a.m + 127) / 128, sms, s);
 }
