@@ -53,22 +53,29 @@ def value_error(z, dz, kind):
     The exponential's relative error is at most (2 + 1.2 |w|) spacings, w its
     argument, whose own relative error of a few roundings multiplies by |w| again;
     a logistic's is no larger, and the quotient and the product add a few.  So
-    (8 + 4 |w|) spacings of the value, and dz times the largest slope, 1.13."""
+    (8 + 4 |w|) spacings of the value, and dz times the largest slope, 1.13.  An
+    exponential below 2^-126 is 0, which is off by less than that and comes to the value
+    times |z|."""
     if kind == NONE:
         return dz
     if kind == RELU:
         return dz
-    return 1.13 * dz + (8 + 4 * argument(z, kind)) * ULP * activation(z, kind)[0].abs()
+    return (1.13 * dz + (8 + 4 * argument(z, kind)) * ULP * activation(z, kind)[0].abs()
+            + 2.0 ** -126 * z.abs())
 
 
 def slope_error(z, kind):
-    """The same of its slope at an exact z: of both terms' magnitudes."""
+    """The same of its slope at an exact z: of both terms' magnitudes.  An
+    exponential that is 0 for less than 2^-126 comes to the first term as it is and to the
+    second times |z| and w's slope: at the tanh's, where w is 87 there, by 2^8 in all."""
     if kind in (NONE, RELU):
         return torch.zeros_like(z)
     y, slope = activation(z, kind)
     first = torch.sigmoid(z) if kind == SILU else activation(z, GELU_TANH)[0] / torch.where(
         z == 0, 1.0, z) if kind == GELU_TANH else normal(z)
-    return (12 + 4 * argument(z, kind)) * ULP * (first.abs() + (slope - first).abs()) + 2.0 ** -126
+    rise = 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z) if kind == GELU_TANH else 1.0
+    return ((12 + 4 * argument(z, kind)) * ULP * (first.abs() + (slope - first).abs())
+            + 2.0 ** -126 * (1 + z.abs() * rise))
 
 
 def product(a, b):

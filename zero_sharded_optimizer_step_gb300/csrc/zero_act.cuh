@@ -1,7 +1,7 @@
 // The activations of linear layers and their slopes, in fp32.
 //
 // Exponentials and reciprocals are the hardware's (a few units in the last place,
-// subnormal results 0).  Differences of nearly equal numbers are avoided:
+// subnormal results 0: a slope below 2^-118 may come out as 0).  Differences of nearly equal numbers are avoided:
 // p (1 - p) of a logistic p is e / (1 + e)^2, and the normal distribution
 // function is made from its small side.
 #pragma once
