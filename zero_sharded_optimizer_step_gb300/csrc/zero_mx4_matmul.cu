@@ -325,7 +325,7 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
-        for (int s = 0; s < sp.stages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
+        for (int s = 0; s < sp.stages; ++s) bar_wait_alone(full(s), 0), bar_wait_alone(full(s), 1);
     __syncthreads();
     if (warp == 5)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
@@ -654,7 +654,7 @@ mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ 
     __syncthreads();
     // copies still in flight land before either block ends
     if (failed && threadIdx.x == 0 && rank == 0)
-        for (int s = 0; s < kPairStages; ++s) bar_wait(full(s), 0), bar_wait(full(s), 1);
+        for (int s = 0; s < kPairStages; ++s) bar_wait_alone(full(s), 0), bar_wait_alone(full(s), 1);
     __syncthreads();
     cluster_sync();             // nothing of either block is still in use by the other
     if (warp == 5)

@@ -26,20 +26,36 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
                  : "memory");
 }
 
+__device__ __forceinline__ bool bar_poll(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n"
+                 " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
+// A wait by all lanes of a warp, which get one answer: were it each lane's own, some
+// could give up in the poll in which others succeed, and the two would then wait for
+// one another at the warp's next barrier or shuffle.  A phase that has ended stays so
+// until this warp has gone on, so that every poll after that one is unanimous.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
 {
-    for (long long i = 0; i < kPolls; ++i) {
-        uint32_t done;
-        asm volatile("{\n .reg .pred p;\n"
-                     " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                     " selp.u32 %0, 1, 0, p;\n}"
-                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-        if (done) return true;
-    }
+    for (long long i = 0; i < kPolls; ++i)
+        if (__all_sync(0xffffffffu, bar_poll(bar, parity))) return true;
     return false;
 }
 
-// Both barriers' phases; the two polls' latencies overlap.
+// A wait by a single thread.
+__device__ __forceinline__ bool bar_wait_alone(uint32_t bar, uint32_t parity)
+{
+    for (long long i = 0; i < kPolls; ++i)
+        if (bar_poll(bar, parity)) return true;
+    return false;
+}
+
+// Both barriers' phases, by a warp; the two polls' latencies overlap.
 __device__ __forceinline__ bool bar_wait_both(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1)
 {
     for (long long i = 0; i < kPolls; ++i) {
@@ -49,7 +65,7 @@ __device__ __forceinline__ bool bar_wait_both(uint32_t b0, uint32_t p0, uint32_t
                      " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n"
                      " and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}"
                      : "=r"(done) : "r"(b0), "r"(p0), "r"(b1), "r"(p1) : "memory");
-        if (done) return true;
+        if (__all_sync(0xffffffffu, done)) return true;
     }
     return false;
 }
