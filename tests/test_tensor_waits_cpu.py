@@ -70,3 +70,24 @@ def test_a_single_threads_wait_does_not_ask_its_warp(file):
             alone += len(re.findall(r"\bbar_wait_alone\(", statement))
     assert alone == len(re.findall(r"\bbar_wait_alone\(", text)) > 0
     assert len(re.findall(r"\bbar_wait\(", text)) > 5
+
+
+@pytest.mark.parametrize("name", ["load16", "load32"])
+def test_a_warp_converges_before_it_reads_tensor_memory(name):
+    """tcgen05.ld is .aligned: lanes that stored more than others before may be behind."""
+    body = function(source("zero_tensor.cuh"), name)
+    assert "__syncwarp();" in body[:body.index("tcgen05.ld")], body
+
+
+@pytest.mark.parametrize("file", PRODUCTS)
+def test_a_warp_converges_before_it_frees_tensor_memory(file):
+    text = source(file)
+    found = [m.start() for m in re.finditer(r"tcgen05\.dealloc", text)]
+    assert found
+    for at in found:
+        assert re.search(r"__syncwarp\(\);\s*asm volatile\(\"$", text[:at]), text[at - 200:at]
+
+
+@pytest.mark.parametrize("file", PRODUCTS)
+def test_tensor_memory_is_read_through_the_helpers_alone(file):
+    assert "tcgen05.ld." not in source(file)

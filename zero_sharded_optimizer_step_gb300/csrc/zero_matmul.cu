@@ -723,9 +723,11 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
     if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
         for (int s = 0; s < g.stages; ++s) bar_wait_alone(full(s), 0), bar_wait_alone(full(s), 1);
     __syncthreads();
-    if (warp == kOneWarps + 1)
+    if (warp == kOneWarps + 1) {
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(columns));
+    }
 }
 
 // ------------------------------------------------------ some rows, few tiles
@@ -941,9 +943,11 @@ matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
         for (int s = 0; s < g.stages; ++s) bar_wait_alone(full(s), 0), bar_wait_alone(full(s), 1);
     __syncthreads();
-    if (warp == kOneWarps + 1)
+    if (warp == kOneWarps + 1) {
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(kColumns));
+    }
 }
 
 // ------------------------------------------------------------ the pair kernel
@@ -1190,9 +1194,11 @@ matmul_pair_kernel(const __grid_constant__ ProductArgs a, const __grid_constant_
         for (int s = 0; s < kPairStages; ++s) bar_wait_alone(full(s), 0), bar_wait_alone(full(s), 1);
     __syncthreads();
     cluster_sync();             // nothing of either block is still in use by the other
-    if (warp == kPairWarps + 1)
+    if (warp == kPairWarps + 1) {
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(512u));
+    }
 }
 
 // ------------------------------------------------------- rows onto boundaries

@@ -327,9 +327,11 @@ mx4_matmul_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant_
     if (failed && threadIdx.x == 0)       // copies still in flight land before the block ends
         for (int s = 0; s < sp.stages; ++s) bar_wait_alone(full(s), 0), bar_wait_alone(full(s), 1);
     __syncthreads();
-    if (warp == 5)
+    if (warp == 5) {
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"((uint32_t)Tl::kTmem));
+    }
 }
 
 // ------------------------------------------------------------ the pair kernel
@@ -657,9 +659,11 @@ mx4_pair_kernel(const __grid_constant__ MxMatmulArgs a, const __grid_constant__ 
         for (int s = 0; s < kPairStages; ++s) bar_wait_alone(full(s), 0), bar_wait_alone(full(s), 1);
     __syncthreads();
     cluster_sync();             // nothing of either block is still in use by the other
-    if (warp == 5)
+    if (warp == 5) {
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(512u));
+    }
 }
 
 // A quantised matrix as a tensor of 128-byte lines, copied `box` at a time.

@@ -96,9 +96,12 @@ __device__ __forceinline__ void commit(uint32_t bar)
                      "r"(bar) : "memory");
 }
 
+// 16 columns of tensor memory, the warp's 32 lanes.  (The .aligned instructions want
+// the warp converged, which it need not be after a store that some of its lanes made.)
 __device__ __forceinline__ void load16(uint32_t tmem, float (&v)[16])
 {
     uint32_t r[16];
+    __syncwarp();
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32"
                  " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
@@ -184,8 +187,10 @@ __device__ __forceinline__ void commit2(uint32_t bar)             // at both blo
                  ".multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((uint16_t)3) : "memory");
 }
 
+// 32 columns, as load16.
 __device__ __forceinline__ void load32(uint32_t tmem, uint32_t (&r)[32])
 {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32"
         " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
