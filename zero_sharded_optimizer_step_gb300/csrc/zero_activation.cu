@@ -117,6 +117,7 @@ activation_grad_kernel(const __grid_constant__ ActGrad a)
         }
     }
     if (!a.parts && !a.dbias) return;
+    __syncwarp();                                // all lanes have read what was turned there
 #pragma unroll
     for (int e = 0; e < 8; ++e) joined[warp][rows::column<VEC>(e)] = sum[e];
     __syncthreads();
