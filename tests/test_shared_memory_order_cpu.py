@@ -18,3 +18,9 @@ def test_turning_begins_when_the_warp_is_there():
     first, second = [m.start() for m in re.finditer(r"__syncwarp\(\);", body)]
     write, read = body.index("shared[column<!BACK>(e)] ="), body.index("= shared[column<BACK>(e)]")
     assert first < write < second < read
+
+
+def test_a_warp_converges_before_a_barrier_of_its_group():
+    """bar.sync is .aligned, and stands behind a store by one lane."""
+    body = function(source("zero_norm.cu"), "norm_grad_kernel")
+    assert re.search(r"__syncwarp\(\);\s*asm volatile\(\"bar\.sync", body)

@@ -282,6 +282,7 @@ norm_grad_kernel(const __grid_constant__ NormGrad a)
         if constexpr (W > 1) {
             // (two rows' sums in turn: one barrier of the group a row is enough)
             if (lane == 0) shared[turn][warp] = share;
+            __syncwarp();                        // (the barrier wants it converged)
             asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(W * 32) : "memory");
             share = shared[turn][group * W];
 #pragma unroll
