@@ -91,3 +91,17 @@ def test_a_warp_converges_before_it_frees_tensor_memory(file):
 @pytest.mark.parametrize("file", PRODUCTS)
 def test_tensor_memory_is_read_through_the_helpers_alone(file):
     assert "tcgen05.ld." not in source(file)
+
+
+def test_a_warp_converges_before_a_cluster_barrier():
+    """barrier.cluster is .aligned too, wherever it stands."""
+    found = 0
+    for file in sorted(os.listdir(CSRC)):
+        text = source(file)
+        for m in re.finditer(r'asm volatile\("barrier\.cluster\.(arrive|wait)', text):
+            before = text[:m.start()].rstrip()
+            # the other half, which is .aligned itself, or the warp's own barrier
+            assert re.search(r'(__syncwarp\(\)|asm volatile\("barrier\.cluster\.arrive'
+                             r'[\w.]*;" ::: "memory"\));$', before), (file, before[-200:])
+            found += 1
+    assert found > 4

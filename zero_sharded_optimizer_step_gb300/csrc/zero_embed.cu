@@ -338,13 +338,17 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+// (The barrier's instructions want their warp converged, also after stores that only
+// some lanes make.)
 __device__ __forceinline__ void cluster_arrive()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_wait()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
