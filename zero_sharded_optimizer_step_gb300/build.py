@@ -25,7 +25,8 @@ SOURCES = ["zero_abi.cu", "zero_step_kernels.cu", "zero_gather.cu", "zero_advanc
            "zero_matmul.cu", "zero_norm.cu", "zero_activation.cu", "zero_ops_abi.cu"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 HEADERS = ["zero_internal.h", "zero_ops.h", "zero_row_copy.cuh", "zero_elems.cuh",
-           "zero_tensor.cuh", "zero_act.cuh", "zero_pack8.cuh", "zero_rows.cuh", os.path.join("..", "..", "include", "zero.h")]
+           "zero_tensor.cuh", "zero_act.cuh", "zero_pack8.cuh", "zero_rows.cuh",
+           "zero_product_sizes.h", os.path.join("..", "..", "include", "zero.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

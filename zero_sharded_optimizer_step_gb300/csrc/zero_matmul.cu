@@ -24,17 +24,16 @@
 #include "zero_elems.cuh"
 #include "zero_ops.h"
 #include "zero_pack8.cuh"
+#include "zero_product_sizes.h"
 #include "zero_rows.cuh"
 #include "zero_tensor.cuh"
 
 namespace zgb {
 namespace {
 
-__device__ unsigned int g_matmul_timeouts;
+using namespace product;
 
-constexpr int kDepth = 64;                       // columns c of a stage: 128 bytes
-constexpr int kLine = 128;
-constexpr int kHalf = 128 * kLine;               // 128 rows of an operand in a stage
+__device__ unsigned int g_matmul_timeouts;
 
 // An operand's stage as the tensor cores read it.  Rows of c lie as lines of 128
 // bytes (64 c), eight lines a swizzle atom; the transpose as chunks of 64
@@ -225,7 +224,6 @@ __device__ __forceinline__ void finish_run(const ProductArgs &a, int64_t i, int6
 // Rows off the boundaries, and ragged ends: 32 rows by 32 columns, a row a lane,
 // change places with a row a step through the warp's shared memory (`staged`, 32 by
 // kStagePad floats), so that its accesses are consecutive.
-constexpr int kStagePad = 33;
 
 // v into rows i0 .. i0 + rows of p from column j on; `in`: column j + lane is the matrix's.
 template <int DT>
@@ -395,33 +393,6 @@ matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ row
 // What bounds it: the weights' bytes.  77 rows gated, 2 x 11008 x 4096 values of
 // weights, took 35.8 us (180 MB at 5.0 TB/s) in its 172 tiles before matmul_mid_kernel
 // had them; with 128 rows of either weight a tile, in two accumulators, 37.1.
-__host__ __device__ constexpr int split_floats(int span, int splits);
-constexpr int staged_floats();
-
-struct Tile {
-    static constexpr int kStages = 8;                       // at most
-    static __host__ __device__ constexpr int stage(int nt) { return kHalf + nt * kLine; }
-    static __host__ __device__ constexpr int tmem(int nt)
-    {
-        return nt <= 32 ? 32 : nt <= 64 ? 64 : nt <= 128 ? 128 : 256;
-    }
-    // A block's share of an SM's shared memory is at least its share of the tensor
-    // memory, so that no block waits for tensor memory that another one
-    // holds: two that wait for their cluster peers so would wait forever.
-    static int smem(int stages, int nt, int splits, bool staged)
-    {
-        // the sums, when they are done, a split's shares of them, and room to reorder
-        const int part = (split_floats(nt, splits) + (staged ? staged_floats() : 0)) * 4;
-        const int ring = stages * stage(nt) > part ? stages * stage(nt) : part;
-        const int share = (kSmemSm / (512 / tmem(nt)) + 127) / 128 * 128;
-        return ring + 1024 > share ? ring + 1024 : share;
-    }
-};
-
-constexpr int kOneWarps = 8;                           // of results, before copies and products
-constexpr int kOneThreads = (kOneWarps + 2) * 32;
-constexpr int kMostBlocks = 2;                         // of an SM
-
 struct OneArgs {
     CUtensorMap a, b, b2, a2;
     int64_t kt1, kt, tiles_n;            // stages of the first pair of operands, of both
@@ -442,7 +413,6 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 // result (kPitch floats apart; of a gated block 64 and their 64 second ones) in its
 // shared memory.  The rows are shared out; each block sends every other
 // one's share there by one bulk copy and adds up what it receives in the blocks' order.
-constexpr int kPitch = 132;                  // a lane a row: no two of eight on one bank
 
 struct Split {
     static constexpr int pitch = kPitch;
@@ -467,12 +437,6 @@ struct Split {
         bar_expect(bar, (uint32_t)(splits - 1) * bytes(rank));
     }
 };
-
-// Floats of shared memory that a split's block needs.
-__host__ __device__ constexpr int split_floats(int span, int splits)
-{
-    return (span + (splits > 1 ? splits * ((span + splits - 1) / splits) : 0)) * kPitch;
-}
 
 // By one thread, once every block's sums and barrier are there.
 __device__ __forceinline__ void send_shares(const Split &t, const float *part, uint32_t bar)
@@ -514,8 +478,6 @@ __device__ __forceinline__ void sum32(const Split &t, const float *part, int r, 
         }
     }
 }
-
-constexpr int staged_floats() { return kOneThreads / 32 * 32 * kStagePad; }
 
 // Writes the result of this block's share of the rows: the warps take 32 rows by 32
 // columns in turn, a row a lane.  (Four columns of a row a lane, a row a warp,
@@ -743,31 +705,6 @@ matmul_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ One
 // A gated block's tile has up to 128 rows of A in the lanes, as many rows of A in a stage as
 // there are, and `wide` rows of either weight, whose sums are the accumulator's columns
 // beside one another: tiles of 64, 96 or 128, so that each SM has one.
-constexpr int kMidStages = 7;
-
-__host__ __device__ constexpr int mid_stage(int wide) { return kHalf + wide * kLine; }
-__host__ __device__ constexpr int mid_gated_stage(int nt, int wide)
-{
-    return (nt + 2 * wide) * kLine;
-}
-
-constexpr int mid_smem(int stages, int wide, int splits, bool staged)
-{
-    const int ring = stages * mid_stage(wide);
-    const int part = ((splits > 1 ? split_floats(128, splits) : 0) +
-                      (staged ? staged_floats() : 0)) * 4;
-    return (ring > part ? ring : part) + 1024;
-}
-static_assert(mid_smem(kMidStages, 128, 8, true) <= kSmemBlock, "one block's shared memory");
-
-// (its share of an SM's at least, half, as its tensor memory is: see Tile)
-constexpr int mid_gated_smem(int stages, int nt, int wide)
-{
-    const int ring = stages * mid_gated_stage(nt, wide);
-    const int most = ring > staged_floats() * 4 ? ring : staged_floats() * 4;
-    return most + 1024 > kSmemSm / 2 ? most + 1024 : kSmemSm / 2;
-}
-
 template <int DT, int ODT, bool GATED>
 __global__ void __launch_bounds__(kOneThreads, GATED ? 1 : 2)
 matmul_mid_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ OneArgs g)
@@ -1320,34 +1257,15 @@ cudaError_t pair_go(const ProductArgs &a, int sms, cudaStream_t s)
                      kSmemBlock, done);
     if (e != cudaSuccess) return e;
     PairArgs g;
-    // The tile's width that leaves the pairs the least columns to go through, one after
-    // the other: with few tiles a pair, 256 can leave most of them idle at the end.
-    // (6400 x 1600 over 8192 columns c, 76 pairs: 175 tiles of 256 go three deep, and so
-    // do 225 of 192.)
-    // A narrower tile reads A more often: it has to save an eighth.
-    g.tiles_m = (a.m + 255) / 256;
-    int64_t least = 0;
-    for (int half = 128; half >= 64; half -= GATED ? 32 : 16) {   // blocks of 32 stay whole
-        const int64_t wide = GATED ? half : 2 * half, across = (a.n + wide - 1) / wide;
-        const int64_t deep = (across * g.tiles_m + sms / 2 - 1) / (sms / 2) * half;
-        if (half < 128 && deep * 8 > least * 7) continue;
-        least = deep;
-        g.half = half;
-        g.tiles_n = across;
-    }
+    const PairShape t = pair_shape(a.m, a.n, sms, GATED);
+    g.half = t.half, g.cut = t.cut;
+    g.tiles_m = t.tiles_m, g.tiles_n = t.tiles_n;
+    g.whole = t.whole, g.steps = t.steps;
     e = operand_maps(a, g, 128, g.half);
     if (e != cudaSuccess) return e;
     g.kt1 = (a.k + kDepth - 1) / kDepth;
     g.kt = a.a2 ? 2 * g.kt1 : g.kt1;
     g.vec = in_runs<ODT>(a);
-    // The last turn's tiles, if they leave pairs idle, in halves or quarters (a gated
-    // tile's parts are 32 columns at least, and whole blocks of 32).
-    const int64_t tiles = g.tiles_n * g.tiles_m, left = tiles % (sms / 2);
-    g.cut = 1;
-    for (int cut = 2; cut <= 4; cut *= 2)
-        if (left * cut <= sms / 2 && g.half % (cut * (GATED ? 32 : 16)) == 0) g.cut = cut;
-    g.whole = g.cut > 1 ? tiles - left : tiles;
-    g.steps = g.whole + (tiles - g.whole) * g.cut;
     const int64_t pairs = g.steps < sms / 2 ? g.steps : sms / 2;
     return launch_dependent(matmul_pair_kernel<DT, ODT, GATED>, dim3((unsigned)(2 * pairs)),
                             dim3(kPairThreads), kSmemBlock, s, a, g);
@@ -1374,60 +1292,20 @@ struct Clusters {
     }
 };
 
-// How many clusters of `splits` blocks of a kernel find a place at once: fewer than
-// the SMs' number says, because a cluster's blocks share a group of SMs.  Asked for once
-// for each split and ring length (every device of this build's kind has the same).
-struct Room {
-    std::atomic<int> known[9][16] = {};
-    int of(const void *kernel, int splits, int stages, int smem)
-    {
-        std::atomic<int> &at = known[splits][stages];
-        int n = at.load(std::memory_order_relaxed);
-        if (n) return n - 1;
-        Clusters c(splits, splits, smem, nullptr);
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &c.cfg) != cudaSuccess) {
-            cudaGetLastError();
-            n = 0;
-        }
-        at.store(n + 1, std::memory_order_relaxed);
-        return n;
-    }
-};
-
-// A split, the ring's length, and the stages of the fullest SM.
-struct Cut {
-    int splits, stages;
-    int64_t least;
-};
-
-// The split that leaves the fullest SM the fewest of the kt stages, a join
-// counting as kJoin of them, as long as all clusters find a place at once.
-// `smem(stages, splits)`: a block's shared memory; `most`: stages of the longest ring.
-template <class Smem>
-Cut choose_split(int64_t kt, int64_t tiles, int sms, const void *kernel, Room &room, int most,
-                 int blocks_sm, Smem smem)
+// Clusters of a kernel's blocks that find a place at once, through what is known of them.
+auto clusters_of(const void *kernel, Room &room)
 {
-    constexpr int kJoin = 4;
-    auto ring = [&](int splits, int per_sm) {
-        const int64_t rounds = (kt + splits - 1) / splits;
-        int st = rounds < 1 ? 1 : rounds < most ? (int)rounds : most;
-        while (st > 0 && (smem(st, splits) + 1024) * per_sm > kSmemSm) --st;
-        return st;
+    return [kernel, &room](int splits, int stages, int smem) {
+        return room.of(splits, stages, smem, [&](int n, int bytes) {
+            Clusters c(n, n, bytes, nullptr);
+            int found = 0;
+            if (cudaOccupancyMaxActiveClusters(&found, kernel, &c.cfg) != cudaSuccess) {
+                cudaGetLastError();
+                found = 0;
+            }
+            return found;
+        });
     };
-    const int64_t deep = (tiles + sms - 1) / sms;        // whole tiles of the fullest SM
-    Cut c = {1, ring(1, deep < blocks_sm ? (int)deep : blocks_sm), deep * kt};
-    for (int n = 2; n <= 8 && kt >= 2 * n; ++n) {
-        const int64_t per_sm = (tiles * n + sms - 1) / sms;
-        if (per_sm > blocks_sm) break;
-        const int64_t rounds = (kt + n - 1) / n, cost = per_sm * rounds + kJoin;
-        if (cost >= c.least) continue;
-        // (blocks that share an SM want three stages at least to keep their copies coming)
-        const int st = ring(n, (int)per_sm);
-        if (st < 1 || (st < 3 && st < rounds) || room.of(kernel, n, st, smem(st, n)) < tiles)
-            continue;
-        c = {n, st, cost};
-    }
-    return c;
 }
 
 int64_t stages_of(const ProductArgs &a)
@@ -1459,20 +1337,16 @@ template <int DT, int ODT> cudaError_t allow_mid()
 template <int DT, int ODT, bool GATED>
 Cut one_cut(const ProductArgs &a, int64_t tiles_m, int nt, int sms)
 {
-    using Tl = Tile;
     constexpr int kAcross = GATED ? 64 : 128;
     static Room room[2][16];                          // for each width of a tile
     const bool staged = needs_staging<ODT>(a);
-    int most = (kSmemBlock - 1024) / Tl::stage(nt);
-    if (most > Tl::kStages) most = Tl::kStages;
-    return choose_split(stages_of(a), (a.n + kAcross - 1) / kAcross * tiles_m, sms,
-                        reinterpret_cast<const void *>(matmul_kernel<DT, ODT, GATED>),
-                        room[staged][nt / 16 - 1], most, kMostBlocks, [&](int stages, int splits) {
-                            return Tl::smem(stages, nt, splits, staged);
-                        });
+    const auto place = clusters_of(reinterpret_cast<const void *>(matmul_kernel<DT, ODT, GATED>),
+                                   room[staged][nt / 16 - 1]);
+    return choose_split(stages_of(a), (a.n + kAcross - 1) / kAcross * tiles_m, sms, Tile::most(nt),
+                        kMostBlocks, [&](int stages, int splits) {
+                            return Tile::smem(stages, nt, splits, staged);
+                        }, place);
 }
-
-int width(int64_t m, int64_t tiles_m) { return (int)((m + tiles_m * 16 - 1) / (tiles_m * 16) * 16); }
 
 template <int DT, int ODT, bool GATED>
 cudaError_t one_go(const ProductArgs &a, int64_t tiles_m, int sms, cudaStream_t s)
@@ -1505,11 +1379,12 @@ template <int DT, int ODT> Cut mid_cut(const ProductArgs &a, int wide, int sms)
     const bool staged = needs_staging<ODT>(a);
     const int64_t kt = stages_of(a);
     if (wide < 128) return {1, kt < kMidStages ? (int)kt : kMidStages, 0};
-    return choose_split(kt, (a.n + wide - 1) / wide * ((a.m + 127) / 128), sms,
-                        reinterpret_cast<const void *>(matmul_mid_kernel<DT, ODT, false>),
-                        room[staged], kMidStages, 2, [&](int stages, int splits) {
+    const auto place = clusters_of(reinterpret_cast<const void *>(matmul_mid_kernel<DT, ODT, false>),
+                                   room[staged]);
+    return choose_split(kt, (a.n + wide - 1) / wide * ((a.m + 127) / 128), sms, kMidStages, 2,
+                        [&](int stages, int splits) {
                             return mid_smem(stages, wide, splits, staged);
-                        });
+                        }, place);
 }
 
 // (100 x 256 by 64 columns c: with 64 columns of the result a block 2.7 us, with 128 3.1)

@@ -6,6 +6,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "zero_product_sizes.h"
+
 namespace zgb {
 
 constexpr long long kPolls = 1ll << 22;
@@ -204,8 +206,5 @@ __device__ __forceinline__ void load32(uint32_t tmem, uint32_t (&r)[32])
         : "r"(tmem));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-
-constexpr int kSmemSm = 233472;      // shared memory of an SM
-constexpr int kSmemBlock = 231424;   // dynamic shared memory that leaves room for no other block
 
 }  // namespace zgb
