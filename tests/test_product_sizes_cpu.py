@@ -1,0 +1,32 @@
+"""How the 16-bit products divide their work, without a GPU."""
+from tests.product_sizes import run
+
+
+def test_no_block_wants_more_shared_memory_than_its_kernel_is_allowed():
+    """Whatever the device says of the room for clusters: every width of a tile, split,
+    depth and number of tiles, results that are turned and not, with all the
+    room there can be."""
+    out = run(r"""
+    auto all = [](int, int, int) { return 1 << 20; };
+    long long checked = 0;
+    for (int staged = 0; staged < 2; ++staged)
+        for (int64_t kt = 1; kt <= 200; kt += kt < 40 ? 1 : 13)
+            for (int64_t tiles = 1; tiles <= 320; ++tiles) {
+                for (int nt = 16; nt <= 256; nt += 16) {
+                    auto smem = [&](int st, int splits) { return Tile::smem(st, nt, splits, staged); };
+                    const Cut c = choose_split(kt, tiles, 152, Tile::most(nt), kMostBlocks, smem, all);
+                    if (c.stages < 1) continue;              // not to be taken
+                    if (smem(c.stages, c.splits) > kSmemBlock)
+                        printf("nt %d, %lld tiles, %lld stages in %d, staged %d: %d bytes\n", nt,
+                               (long long)tiles, (long long)kt, c.splits, staged,
+                               smem(c.stages, c.splits));
+                    ++checked;
+                }
+                auto smem = [&](int st, int splits) { return mid_smem(st, 128, splits, staged); };
+                const Cut c = choose_split(kt, tiles, 152, kMidStages, 2, smem, all);
+                if (smem(c.stages, c.splits) > kSmemBlock || c.stages < 1)
+                    printf("128 wide, %lld tiles, %lld stages\n", (long long)tiles, (long long)kt);
+            }
+    if (checked < 100000) printf("%lld\n", checked);
+    return 0;""")
+    assert out == "", out[:2000]

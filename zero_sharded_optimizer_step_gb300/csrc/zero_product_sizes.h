@@ -129,7 +129,10 @@ Cut choose_split(int64_t kt, int64_t tiles, int sms, int most, int blocks_sm, Sm
     auto ring = [&](int splits, int per_sm) {
         const int64_t rounds = (kt + splits - 1) / splits;
         int st = rounds < 1 ? 1 : rounds < most ? (int)rounds : most;
-        while (st > 0 && (smem(st, splits) + 1024) * per_sm > kSmemSm) --st;
+        // (a block has what its kernel is allowed, blocks together what the SM has)
+        while (st > 0 && (smem(st, splits) > kSmemBlock ||
+                          (smem(st, splits) + 1024) * per_sm > kSmemSm))
+            --st;
         return st;
     };
     const int64_t deep = (tiles + sms - 1) / sms;        // whole tiles of the fullest SM
