@@ -826,7 +826,10 @@ int zero_rms_norm_grad(const void *dy, int64_t dy_stride, const void *dsum, int6
  *   zero_matmul(dz, 0, W, 1, m, k, n)          -> dx
  *   zero_matmul(dz, 1, x, 1, n, k, m)          -> dW
  * Products are exact and summed in fp32 on the tensor cores; bias, activation and residual
- * follow in fp32, and the result is rounded once.  workspace:
+ * follow in fp32, and the result is rounded once.  The sums' order depends on the sizes,
+ * layouts and boundaries and on the device (its SMs, and how many clusters of
+ * blocks find a place on them at once): the same call on the same device gives the
+ * same bits.  workspace:
  * zero_matmul_workspace(...) bytes of the same arguments (-1 on a bad one), 16-byte aligned; 0,
  * and NULL will do, where the rows of a, b, a2 and b2 as they lie begin on 16-byte
  * boundaries: others are copied there first.

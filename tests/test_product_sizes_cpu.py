@@ -30,3 +30,33 @@ def test_no_block_wants_more_shared_memory_than_its_kernel_is_allowed():
     if (checked < 100000) printf("%lld\n", checked);
     return 0;""")
     assert out == "", out[:2000]
+
+
+def test_what_is_known_of_a_device_is_not_said_of_another():
+    """The room for clusters is a chip's own: how its SMs are grouped."""
+    assert run(r"""
+    static Room room;
+    int asked = 0;
+    auto ask = [&](int n) { return [&asked, n](int, int, int &found) { ++asked; found = n; return true; }; };
+    printf("%d", room.of(0, 4, 3, 100, ask(37)));
+    printf(" %d", room.of(1, 4, 3, 100, ask(30)));
+    printf(" %d", room.of(0, 4, 3, 100, ask(1)));
+    printf(" %d", room.of(1, 4, 3, 100, ask(1)));
+    printf(" %d", room.of(0, 5, 3, 100, ask(0)));          // no room is an answer
+    printf(" %d", room.of(0, 5, 3, 100, ask(9)));
+    printf(" of %d;", asked);
+    printf(" %d", room.of(1000, 4, 3, 100, ask(5)));       // far devices are asked every time
+    printf(" %d", room.of(1000, 4, 3, 100, ask(6)));
+    printf(" %d", room.of(-1, 4, 3, 100, ask(7)));
+    return 0;""") == "37 30 37 30 0 0 of 3; 5 6 7"
+
+
+def test_a_question_that_fails_is_asked_again():
+    assert run(r"""
+    static Room room;
+    auto fails = [](int, int, int &) { return false; };
+    auto works = [](int, int, int &found) { found = 37; return true; };
+    printf("%d", room.of(0, 4, 3, 100, fails));
+    printf(" %d", room.of(0, 4, 3, 100, works));
+    printf(" %d", room.of(0, 4, 3, 100, fails));
+    return 0;""") == "0 37 37"

@@ -1292,18 +1292,19 @@ struct Clusters {
     }
 };
 
-// Clusters of a kernel's blocks that find a place at once, through what is known of them.
+// Clusters of a kernel's blocks that find a place at once on the current device, through
+// what is known of it.
 auto clusters_of(const void *kernel, Room &room)
 {
     return [kernel, &room](int splits, int stages, int smem) {
-        return room.of(splits, stages, smem, [&](int n, int bytes) {
+        int device = -1;
+        if (cudaGetDevice(&device) != cudaSuccess) device = -1;
+        return room.of(device, splits, stages, smem, [&](int n, int bytes, int &found) {
             Clusters c(n, n, bytes, nullptr);
-            int found = 0;
-            if (cudaOccupancyMaxActiveClusters(&found, kernel, &c.cfg) != cudaSuccess) {
-                cudaGetLastError();
-                found = 0;
-            }
-            return found;
+            const bool answered =
+                cudaOccupancyMaxActiveClusters(&found, kernel, &c.cfg) == cudaSuccess;
+            if (!answered) cudaGetLastError();
+            return answered;
         });
     };
 }

@@ -96,20 +96,24 @@ inline int width(int64_t m, int64_t tiles_m)
 
 // How many clusters of `splits` blocks of a kernel find a place at once: fewer than
 // the SMs' number says, because a cluster's blocks share a group of SMs.  Asked for once
-// for each split and ring length (every device of this build's kind has the same).
+// for each device (of the first sixteen), split and ring length.
 struct Room {
-    std::atomic<int> known[9][16] = {};
-    // ask(splits, smem): the device's answer, 0 if it has none
-    template <class Ask> int of(int splits, int stages, int smem, Ask ask)
+    static constexpr int kDevices = 16, kRing = 8;       // kRing: stages of the longest ring
+    std::atomic<int16_t> known[kDevices][9][kRing + 1] = {};
+    // ask(splits, smem, found): whether the device answers, and what
+    template <class Ask> int of(int device, int splits, int stages, int smem, Ask ask)
     {
-        std::atomic<int> &at = known[splits][stages];
-        int n = at.load(std::memory_order_relaxed);
+        const bool kept = device >= 0 && device < kDevices;
+        std::atomic<int16_t> &at = known[kept ? device : 0][splits][stages];
+        const int n = kept ? at.load(std::memory_order_relaxed) : 0;
         if (n) return n - 1;
-        n = ask(splits, smem);
-        at.store(n + 1, std::memory_order_relaxed);
-        return n;
+        int found = 0;
+        if (!ask(splits, smem, found)) return 0;         // no answer: asked again next time
+        if (kept) at.store((int16_t)(found < 32766 ? found + 1 : 32767), std::memory_order_relaxed);
+        return found;
     }
 };
+static_assert(Tile::kStages <= Room::kRing && kMidStages <= Room::kRing, "the table's last entry");
 
 // A split, the ring's length, and the stages of the fullest SM.
 struct Cut {
