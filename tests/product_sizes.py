@@ -9,7 +9,7 @@ CSRC = os.path.join(ROOT, "zero_sharded_optimizer_step_gb300", "csrc")
 
 def run(body: str, *args) -> str:
     """What a program with this main() prints."""
-    program = ('#include <cstdio>\n#include <cstdlib>\n#include "zero_product_sizes.h"\n'
+    program = ('#include <cstdio>\n#include <cstdlib>\n#include <initializer_list>\n#include "zero_product_sizes.h"\n'
                "using namespace zgb;\nusing namespace zgb::product;\n"
                "int main(int argc, char **argv)\n{\n" + body + "\n}\n")
     with tempfile.TemporaryDirectory() as d:
@@ -20,3 +20,13 @@ def run(body: str, *args) -> str:
                        check=True)
         return subprocess.run([exe, *map(str, args)], check=True, capture_output=True,
                               text=True).stdout
+
+
+def pair_shape(m: int, n: int, sms: int, gated: bool) -> dict:
+    """How the pair kernel goes over an m by n result."""
+    names = ("half", "cut", "tiles_m", "tiles_n", "whole", "steps")
+    out = run("    const PairShape g = pair_shape(atoll(argv[1]), atoll(argv[2]), atoi(argv[3]), "
+              "atoi(argv[4]));\n" + "".join('    printf("%%lld ", (long long)g.%s);\n' % x
+                                            for x in names) + "    return 0;", m, n, sms,
+              int(gated))
+    return dict(zip(names, map(int, out.split())))

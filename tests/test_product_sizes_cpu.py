@@ -1,5 +1,8 @@
 """How the 16-bit products divide their work, without a GPU."""
-from tests.product_sizes import run
+import pytest
+
+from tests.product_sizes import pair_shape, run
+from tests.test_gpu_product_parts import GATED, PLAIN
 
 
 def test_no_block_wants_more_shared_memory_than_its_kernel_is_allowed():
@@ -60,3 +63,15 @@ def test_a_question_that_fails_is_asked_again():
     printf(" %d", room.of(0, 4, 3, 100, works));
     printf(" %d", room.of(0, 4, 3, 100, fails));
     return 0;""") == "0 37 37"
+
+
+@pytest.mark.parametrize("gated,case", [(False, c) for c in PLAIN] + [(True, c) for c in GATED])
+def test_the_sizes_of_the_tests_of_parts_are_divided_as_they_say(gated, case):
+    m, n, half, cut, empty = case
+    g = pair_shape(m, n, 152, gated)
+    assert (g["half"], g["cut"]) == (half, cut)
+    tile = half if gated else 2 * half                       # columns of the result
+    left = n - (g["tiles_n"] - 1) * tile
+    assert empty == (left <= tile - tile // cut)
+    # the last column of tiles is among those in parts
+    assert g["whole"] < g["tiles_m"] * g["tiles_n"]
