@@ -91,7 +91,11 @@ __device__ __forceinline__ void finish(const Norm &a, int64_t row, int64_t c0, R
         s[e] = __fmaf_rn(p, rstd.hi, __fmul_rn(p, rstd.lo));
     }
     if (a.y) rows::put<DT, VEC>(a.y, a.y_stride, row, c0, a.dim, s);
-    if (a.q) rows::pack<VEC>(pack8::view(a.q, a.n, a.dim), row, c0, turned, s);
+    if (!a.q) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)                  // (0 times a NaN or infinite rstd is not 0)
+        if (c0 + rows::column<VEC>(e) >= a.dim) s[e] = 0.0f;
+    rows::pack<VEC>(pack8::view(a.q, a.n, a.dim), row, c0, turned, s);
 }
 
 // Rows of up to W * G * 256 elements.
