@@ -39,6 +39,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import binding as z
 
@@ -83,6 +84,13 @@ def _tokens(tokens: torch.Tensor, device) -> torch.Tensor:
     return tokens.contiguous()
 
 
+def _written(*tensors) -> None:
+    """The caller's tensors were written, through their addresses: torch's autograd counts
+    that as for its own operations in place, so that a backward pass which still needs
+    what was there raises instead of using what is there now."""
+    increment_version([t for t in tensors if t is not None])
+
+
 def _same(name: str, x: torch.Tensor, like: torch.Tensor) -> None:
     if x.device != like.device or x.dtype != like.dtype or x.shape != like.shape:
         raise ValueError("%s must match in device, dtype and shape" % name)
@@ -107,6 +115,7 @@ def embed_grad(dy: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, scale
         z.zero_embed_grad(dy, _DT[dy.dtype], _stride(dy), tokens, tokens.element_size(), n, pad,
                           scale, grad, _DT[grad.dtype], rows, dim, _stride(grad), accumulate, ws,
                           need)
+    _written(grad)
     return grad
 
 
@@ -250,6 +259,7 @@ def mx4_matmul(a: Mx4Matrix, b: Mx4Matrix, dtype: torch.dtype = torch.bfloat16,
     with torch.cuda.device(out.device):
         z.zero_mx4_matmul(a.q, a.rows, b.q, b.rows, a.cols, alpha, accumulate, out,
                           _DT[out.dtype], _stride(out))
+    _written(out)
     return out
 
 
@@ -543,8 +553,10 @@ def matmul(a: torch.Tensor, b: torch.Tensor, a_cols: bool = False, b_cols: bool 
     if bias is not None and (bias.shape != (n,) or bias.dtype != a.dtype
                              or bias.device != a.device or (n > 1 and bias.stride(0) != 1)):
         raise ValueError("bias must be a vector of %d elements of the operands' type" % n)
-    return _product(a, b, a_cols, b_cols, a2, b2, bias, _activation(activation), residual, kept,
-                    packed.q if packed is not None else None, out, accumulate, m, n, k)
+    _product(a, b, a_cols, b_cols, a2, b2, bias, _activation(activation), residual, kept,
+             packed.q if packed is not None else None, out, accumulate, m, n, k)
+    _written(out, kept)
+    return out
 
 
 def _product(a, b, a_cols, b_cols, a2, b2, bias, act, residual, kept, kept_q, out, accumulate, m,
