@@ -757,7 +757,13 @@ int zero_mx4_timeouts(uint32_t *count);
  * matrices of a call that do not have one of their own.  An activation is one of
  * enum zero_activation.  What a forward pass keeps for its backward pass goes
  * into a matrix of `dtype`, or packed to 8 bits (zero_pack8) into a buffer of
- * zero_pack8_bytes bytes, or nowhere (both NULL). */
+ * zero_pack8_bytes bytes, or nowhere (both NULL).
+ *
+ * Activations and their slopes are computed in fp32, fp32 matrices' too, by the
+ * hardware's exponential and reciprocal.  A value is off by at most 5 units of
+ * 2^-23 of itself from -1 on; in the negative tails, where it is small, by up to 94
+ * (GELU at -12.9; by tanh 90 at -9; SiLU 33 at -87); a value or slope below
+ * 2^-118 may come out as 0. */
 
 enum zero_activation {
     ZERO_ACT_NONE = 0,

@@ -385,8 +385,8 @@ matvec_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ row
 // The accumulator's 128 lanes are 128 rows of B (128 consecutive columns of
 // the result, so that a warp's stores are contiguous), its columns up to 128 rows of
 // A (256 in pick()'s wide tiles): with few tokens the tile is as narrow as they are,
-// and the product reads the weights once.  A gated block's lanes are 64 rows of B and the same 64 of B2.
-// One warp issues the copies, one the products, eight write.  With fewer tiles
+// and the product reads the weights once.  A gated block's lanes are 64 rows of B and
+// the same 64 of B2.  One warp issues the copies, one the products, eight write.  With fewer tiles
 // than SMs the columns c are split over a cluster of up to 8 blocks, whose partial sums
 // join through distributed shared memory in the blocks' order.
 //

@@ -147,7 +147,9 @@ norm_kernel(const __grid_constant__ Norm a)
     }
 }
 
-// Longer rows, a block each: the elements are read again for the result.
+// Longer rows, a block each: the elements are read again for the result, from L2 as far
+// as the rows at work at one time fit there.  (4096 x 16384 in bf16 49 us, 40 of them the
+// bytes of one reading; 4096 x 12000 41 and 29.)
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 norm_long_kernel(const __grid_constant__ Norm a)
@@ -343,6 +345,7 @@ norm_grad_kernel(const __grid_constant__ NormGrad a)
 }
 
 // Rows of more than 8192 elements: dx by a block a row, which reads it twice ...
+// (4096 x 16384 in bf16, both kernels, 130 us, 60 of them the bytes of one reading)
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 norm_grad_long_kernel(const __grid_constant__ NormGrad a)

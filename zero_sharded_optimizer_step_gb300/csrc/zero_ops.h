@@ -1,7 +1,8 @@
 // Internal interface between the training operators' C ABI (zero_ops_abi.cu)
 // and their kernels (zero_embed.cu, zero_dropout.cu, zero_mx4.cu,
-// zero_mx4_matmul.cu, zero_matmul.cu, zero_norm.cu, zero_activation.cu).  Element types are the DType codes of
-// zero_internal.h; every launcher returns a cudaError_t and launches on `s`.
+// zero_mx4_matmul.cu, zero_matmul.cu, zero_norm.cu, zero_activation.cu).  Element
+// types are the DType codes of zero_internal.h; every launcher returns a
+// cudaError_t and launches on `s`.
 #pragma once
 
 #include <atomic>
