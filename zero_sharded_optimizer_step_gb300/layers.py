@@ -420,6 +420,8 @@ class _Norm(torch.autograd.Function):
         if grads:
             link = x.new_empty(0)
             ctx.save_for_backward(x if total is None else total, weight, rstd, link)
+            if total is not None and not any(ctx.needs_input_grad[:2]):
+                ctx.mark_non_differentiable(total)       # the weight has no part in it
         return y, total, link
 
     @staticmethod
